@@ -8,8 +8,9 @@
  * with W0 dequantized on the fly to bf16 inside the tensor-core GEMM, its backward pass, the
  * adapter merge, multi-adapter forwards over one shared base (a few adapters, or thousands of
  * mixed-rank adapters), DoRA's forward and backward, the adapter optimizer step (AdamW, gradient
- * accumulation, paged state), and the forward and backward with FP8 (E4M3 / E5M2) activations
- * and gradients on FP8 tensor cores.
+ * accumulation, paged state), the forward and backward with FP8 (E4M3 / E5M2) activations
+ * and gradients on FP8 tensor cores, and microscaled formats: an MXFP4 base on 4-bit tensor cores
+ * and 8-bit activation checkpoints read by the backward.
  *
  * Sources of each definition (page title, then section):
  *  [MF]  "Low-Rank Adaptation (LoRA) and QLoRA: Mathematical Foundations, Intrinsic Rank
@@ -66,7 +67,8 @@ typedef enum { QLORA_F32 = 0, QLORA_BF16 = 1 } qlora_dtype;
 typedef enum {
     QLORA_OP_FWD = 0, QLORA_OP_BWD = 1, QLORA_OP_FWD_BATCHED = 2, QLORA_OP_MERGE = 3,
     QLORA_OP_FWD_MULTI = 4, QLORA_OP_DORA_FWD = 5, QLORA_OP_FWD_FP8 = 6, QLORA_OP_FP8_QUANT = 7,
-    QLORA_OP_BWD_FP8 = 8, QLORA_OP_DORA_BWD = 9
+    QLORA_OP_BWD_FP8 = 8, QLORA_OP_DORA_BWD = 9,
+    QLORA_OP_FWD_MXFP4 = 16, QLORA_OP_BWD_MXFP4 = 17, QLORA_OP_BWD_ACT8 = 18
 } qlora_op;
 
 /* Stored NF4 weight.  Block size 64 and group size 256 are fixed.
@@ -352,6 +354,98 @@ qlora_status qlora_linear_bwd_fp8(const qlora_nf4* w, const uint8_t* X8, const f
                                   int64_t T, const void* A, const void* B, int32_t r, float alpha,
                                   void* dX, float* dA, float* dB, void* ws, size_t ws_bytes,
                                   uint32_t flags, cudaStream_t stream);
+
+/* ---- Microscaled formats ---------------------------------------------------------------------
+ * OCP Microscaling Formats v1.0: 32 consecutive elements of a row share one power-of-two scale
+ * 2^(e - 127), stored as the byte e (E8M0; 255 is NaN).  Every decoded value is exact in fp32 and the
+ * formats are defined bit for bit.  A block that holds a NaN or an infinity is stored with e = 255 and
+ * elements 0 and decodes to NaN.
+ *
+ * MXFP4: 4-bit E2M1 elements (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives; bit 3 of a code is the
+ * sign), value = E2M1 2^(e - 127).  [MF] "QLoRA: 4-Bit NormalFloat and Memory Optimization" stores the
+ * frozen base blockwise in 4 bits; this is the blockwise 4-bit format whose product B200's tensor
+ * cores take without decoding.
+ *   codes  [d_out, d_in/2] bytes: element 2j in the low nibble of byte j, 2j+1 in the high.
+ *   scales 512-byte tiles of 128 rows x 4 blocks; the scale of block b = column / 32 of row i is
+ *          byte (i % 32) * 16 + (i / 32 % 4) * 4 + b % 4
+ *          of tile (i / 128) * ceil(d_in / 128) + b / 4.  Bytes outside the matrix are 0.       */
+typedef struct {
+    const uint8_t* codes;
+    const uint8_t* scales;
+    int64_t        d_out;
+    int64_t        d_in;
+} qlora_mxfp4;
+
+/* Byte sizes of the two MXFP4 buffers of a [rows, cols] matrix (host-only): rows*cols/2 and
+ * 512*ceil(rows/128)*ceil(cols/128).  UNSUPPORTED if cols % 64 != 0 or rows < 1.                */
+qlora_status qlora_mxfp4_sizes(int64_t rows, int64_t cols, size_t* codes_bytes, size_t* scale_bytes);
+
+/* Quantize W[rows, cols] (fp32 or bf16, device), a weight or an activation, to MXFP4.  Per block:
+ * e = max(0, floor(log2 max|w|) - 2 + 127), code = E2M1(w 2^(127 - e)) rounded to nearest even and
+ * saturating at 6.  Bit-exact, deterministic; every byte of both outputs is written.            */
+qlora_status mxfp4_quantize(const void* W, qlora_dtype w_dtype, int64_t rows, int64_t cols,
+                            uint8_t* codes, uint8_t* scales, cudaStream_t stream);
+
+/* Decode to W_out[d_out, d_in] (device, fp32 exact or bf16: the exact value rounded to nearest even,
+ * which changes it only beyond bf16's range).                                                    */
+qlora_status mxfp4_dequantize(const qlora_mxfp4* w, void* W_out, qlora_dtype out_dtype,
+                              cudaStream_t stream);
+
+/* Forward over an MXFP4 base with the activation quantized to MXFP4 inside the call (bf16 X, A, B, H):
+ *   H = Q(X) W^T + (alpha/r) (X A^T) B^T
+ * Q(X) the MXFP4 value of X (as mxfp4_quantize), W the stored weight; the base product runs on
+ * block-scaled 4-bit tensor cores (exact products, fp32 accumulation), the adapter term takes the
+ * unquantized X and is added in the same accumulator with (alpha/r) X A^T rounded to bf16.
+ * Any T >= 1, from single tokens up.  U_save as in qlora_linear_fwd.  [MF] "Intrinsic Dimensionality and Low-Rank Parameter Dynamics".
+ * ws >= qlora_workspace_bytes(QLORA_OP_FWD_MXFP4, QLORA_BF16, T, d_out, d_in, r).
+ * Stream order holds for every argument, as for the other calls.                               */
+qlora_status qlora_linear_fwd_mxfp4(const qlora_mxfp4* w, const void* X, int64_t T, const void* A,
+                                    const void* B, int32_t r, float alpha, void* H, void* U_save,
+                                    void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* 8-bit activation checkpoint of X[T, d_in]: OCP MXINT8, value = q 2^(e - 133), |q| <= 127
+ * ([UH] "1.3 Activation Memory Savings via FlashAttention-2 & Activation Checkpointing").
+ *   q [T, d_in] int8; scales [T, d_in/32] bytes, both row-major.                                */
+typedef struct {
+    const int8_t*  q;
+    const uint8_t* scales;
+} qlora_act8;
+
+/* Byte sizes of the two buffers (host-only).  UNSUPPORTED if d_in % 64 != 0 or T < 1.          */
+qlora_status qlora_act8_sizes(int64_t T, int64_t d_in, size_t* q_bytes, size_t* scale_bytes);
+
+/* Keep X (bf16 or fp32, device) as 8-bit: per block of 32 e = floor(log2 max|x|) + 127 (0 where
+ * that is less), q = x 2^(133 - e) rounded to nearest even, to at most 127 in magnitude: the error
+ * is at most 2^-7 of the block's largest |x|, and half of that except at |q| = 127.  Bit-exact.  */
+qlora_status qlora_act8_quantize(const void* X, qlora_dtype x_dtype, int64_t T, int64_t d_in,
+                                 int8_t* q, uint8_t* scales, cudaStream_t stream);
+
+/* The stored values as bf16 or fp32, exact in either.                                           */
+qlora_status qlora_act8_dequantize(const qlora_act8* a, int64_t T, int64_t d_in, void* X_out,
+                                   qlora_dtype out_dtype, cudaStream_t stream);
+
+/* Backward of qlora_linear_fwd_mxfp4 (the activation's quantization passed straight through), from
+ * the bf16 activation X or an 8-bit checkpoint X8 of it (exactly one is given, the other NULL):
+ *   dX = dH W + s (dH B) A,   dA = s (dH B)^T X~,   dB = s dH^T (X~ A^T),   s = alpha/r,
+ * X~ = X or the checkpoint's values.  U_saved (nullable): the forward's U, used for X~ A^T.  dX
+ * (nullable: skipped) in bf16; dA, dB fp32, with s (dH B) and a recomputed U carried to the tensor
+ * cores as pairs of bf16 (16 significant bits).  flags as in qlora_linear_bwd_ex, the two-phase form
+ * included (QLORA_BWD_DX_FROM_WS reads no activation, but one must be given).
+ * [MF] "Gradient Dynamics and Backpropagation Mechanics".
+ * ws >= qlora_workspace_bytes(QLORA_OP_BWD_MXFP4, QLORA_BF16, T, d_out, d_in, r): no copy of X.   */
+qlora_status qlora_linear_bwd_mxfp4(const qlora_mxfp4* w, const void* X, const qlora_act8* X8,
+                                    const void* dH, int64_t T, const void* A, const void* B,
+                                    int32_t r, float alpha, const void* U_saved, void* dX, float* dA,
+                                    float* dB, void* ws, size_t ws_bytes, uint32_t flags,
+                                    cudaStream_t stream);
+
+/* qlora_linear_bwd_ex (bf16) from an 8-bit checkpoint of X instead of X, with the arithmetic and
+ * flags of qlora_linear_bwd_mxfp4 over the NF4 base.
+ * ws >= qlora_workspace_bytes(QLORA_OP_BWD_ACT8, QLORA_BF16, T, d_out, d_in, r).                  */
+qlora_status qlora_linear_bwd_act8(const qlora_nf4* w, const qlora_act8* X8, const void* dH, int64_t T,
+                                   const void* A, const void* B, int32_t r, float alpha,
+                                   const void* U_saved, void* dX, float* dA, float* dB, void* ws,
+                                   size_t ws_bytes, uint32_t flags, cudaStream_t stream);
 
 /* Size of the device scratch array behind qlora_linear_fwd_noalloc (bytes per GPU). */
 #define QLORA_NOALLOC_SCRATCH_BYTES ((size_t)16 << 20)

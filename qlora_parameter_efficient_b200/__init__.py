@@ -13,10 +13,15 @@ adapters), ``qlora_dora_fwd`` / ``qlora_dora_bwd`` / ``dora_row_norms`` (and
 ``qlora_dora_fwd_save`` whose saved tensors ``qlora_dora_bwd(saved=...)`` reuses), ``adamw_step`` /
 ``prefetch`` (optimizer step, unified-memory state), and the FP8 path:
 ``fp8_quantize`` (E4M3 activation), ``fp8_quantize_grad`` (E5M2 gradient),
-``fp8_weight_scale``, ``qlora_linear_fwd_fp8``, ``qlora_linear_bwd_fp8``.
+``fp8_weight_scale``, ``qlora_linear_fwd_fp8``, ``qlora_linear_bwd_fp8``; and the microscaled
+formats: ``mxfp4_quantize`` / ``mxfp4_dequantize``, the layer over an MXFP4 base
+(``qlora_linear_fwd_mxfp4``, ``qlora_linear_bwd_mxfp4``), 8-bit activation checkpoints
+(``act8_quantize`` / ``act8_dequantize``) and the NF4 layer's backward from one
+(``qlora_linear_bwd_act8``).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -32,6 +37,7 @@ STATUS = {0: "QLORA_OK", 1: "QLORA_ERR_INVALID_ARG", 2: "QLORA_ERR_UNSUPPORTED",
 F32, BF16 = 0, 1
 OP_FWD, OP_BWD, OP_FWD_BATCHED, OP_MERGE, OP_FWD_MULTI, OP_DORA_FWD = 0, 1, 2, 3, 4, 5
 OP_FWD_FP8, OP_FP8_QUANT, OP_BWD_FP8, OP_DORA_BWD = 6, 7, 8, 9
+OP_FWD_MXFP4, OP_BWD_MXFP4, OP_BWD_ACT8 = 16, 17, 18
 
 # Every symbol include/qlora.h declares.
 EXPORTS = ["qlora_nf4_sizes", "qlora_nf4_levels", "nf4_quantize", "nf4_dequantize",
@@ -40,6 +46,9 @@ EXPORTS = ["qlora_nf4_sizes", "qlora_nf4_levels", "nf4_quantize", "nf4_dequantiz
            "qlora_dora_bwd", "qlora_dora_fwd_save", "qlora_dora_bwd_saved", "qlora_dora_row_norms", "qlora_fp8_quantize", "qlora_fp8_weight_scale",
            "qlora_linear_fwd_fp8", "qlora_fp8_quantize_grad", "qlora_linear_bwd_fp8",
            "qlora_linear_fwd_batched", "qlora_linear_fwd_multi", "qlora_linear_fwd_noalloc",
+           "qlora_mxfp4_sizes", "mxfp4_quantize", "mxfp4_dequantize", "qlora_linear_fwd_mxfp4",
+           "qlora_linear_bwd_mxfp4", "qlora_act8_sizes", "qlora_act8_quantize",
+           "qlora_act8_dequantize", "qlora_linear_bwd_act8",
            "qlora_get_device_error",
            "qlora_selftest_wait_timeout", "qlora_set_gemm_events", "qlora_launch_count",
            "qlora_status_string"]
@@ -56,6 +65,15 @@ class _NF4(ctypes.Structure):
                 ("c2", ctypes.c_void_p), ("d_out", ctypes.c_int64), ("d_in", ctypes.c_int64)]
 
 
+class _MXFP4(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("d_out", ctypes.c_int64), ("d_in", ctypes.c_int64)]
+
+
+class _ACT8(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -70,6 +88,7 @@ def load() -> ctypes.CDLL:
     L = ctypes.CDLL(LIB_PATH)
     vp, i64, i32, f32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
     pnf4 = ctypes.POINTER(_NF4)
+    pmx, pa8, psz, u32 = ctypes.POINTER(_MXFP4), ctypes.POINTER(_ACT8), ctypes.POINTER(sz), ctypes.c_uint32
     sig = {
         "qlora_nf4_sizes": ([i64, i64, ctypes.POINTER(sz), ctypes.POINTER(sz), ctypes.POINTER(sz)], ctypes.c_int),
         "qlora_nf4_levels": ([ctypes.POINTER(ctypes.c_float)], ctypes.c_int),
@@ -102,6 +121,17 @@ def load() -> ctypes.CDLL:
         "qlora_linear_bwd_fp8": ([pnf4, vp, vp, vp, vp, vp, i64, vp, vp, i32, f32, vp, vp, vp, vp, sz,
                                   ctypes.c_uint32, vp], ctypes.c_int),
         "qlora_linear_fwd_noalloc": ([pnf4, vp, i64, vp, vp, i32, f32, ctypes.c_int, vp, vp, vp], ctypes.c_int),
+        "qlora_mxfp4_sizes": ([i64, i64, psz, psz], ctypes.c_int),
+        "mxfp4_quantize": ([vp, ctypes.c_int, i64, i64, vp, vp, vp], ctypes.c_int),
+        "mxfp4_dequantize": ([pmx, vp, ctypes.c_int, vp], ctypes.c_int),
+        "qlora_linear_fwd_mxfp4": ([pmx, vp, i64, vp, vp, i32, f32, vp, vp, vp, sz, vp], ctypes.c_int),
+        "qlora_linear_bwd_mxfp4": ([pmx, vp, pa8, vp, i64, vp, vp, i32, f32, vp, vp, vp, vp, vp, sz, u32, vp],
+                                   ctypes.c_int),
+        "qlora_act8_sizes": ([i64, i64, psz, psz], ctypes.c_int),
+        "qlora_act8_quantize": ([vp, ctypes.c_int, i64, i64, vp, vp, vp], ctypes.c_int),
+        "qlora_act8_dequantize": ([pa8, i64, i64, vp, ctypes.c_int, vp], ctypes.c_int),
+        "qlora_linear_bwd_act8": ([pnf4, pa8, vp, i64, vp, vp, i32, f32, vp, vp, vp, vp, vp, sz, u32, vp],
+                                  ctypes.c_int),
         "qlora_get_device_error": ([vp], ctypes.c_int),
         "qlora_selftest_wait_timeout": ([ctypes.c_uint64, vp], ctypes.c_int),
         "qlora_set_gemm_events": ([vp, vp], ctypes.c_int),
@@ -540,6 +570,265 @@ def qlora_linear_fwd_multi(w: NF4Weight, X, adapter_id, table: AdapterTable, H=N
         _ptr(table.B_ptrs), _ptr(table.ranks), _ptr(table.alphas), table.r_max, _ptr(H),
         _ptr(ws), ws.numel(), _stream(stream)))
     return H
+
+
+# ------------------------------------------------------------------ microscaled formats
+#
+# These calls check dtypes, shapes, devices and contiguity, run on the tensors' device whatever the
+# current one is, and allocate what they allocate on the stream they run on (so that a workspace
+# given back on return is only reused behind the call's kernels).
+
+def _need(name, t, dtype, shape, dev):
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _need_cuda(name, t):
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def _run_on(dev, stream):
+    torch = _torch()
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"stream is on {stream.device}, the tensors are on {dev}")
+        return torch.cuda.stream(stream)
+    if torch.cuda.current_device() == dev.index:
+        return contextlib.nullcontext()
+    return torch.cuda.device(dev)
+
+
+def _need_ws(op, T, d_out, d_in, r, dev, ws):
+    torch = _torch()
+    need = workspace_bytes(op, BF16, T, d_out, d_in, r)
+    if need == 0:
+        raise ValueError(f"unsupported shape: T={T}, d_out={d_out}, d_in={d_in}, r={r} "
+                         "(d_in % 64 == 0, 1 <= r <= 128)")
+    if ws is None:
+        return torch.empty(need, dtype=torch.uint8, device=dev)
+    if ws.device != dev or not ws.is_contiguous() or ws.numel() * ws.element_size() < need:
+        raise ValueError(f"ws must be a contiguous buffer of at least {need} bytes on {dev}")
+    return ws
+
+
+@dataclass
+class MXFP4Weight:
+    """Device buffers of an MXFP4 matrix: packed E2M1 codes and the tiled E8M0 scales."""
+    codes: object      # uint8 [d_out, d_in/2]
+    scales: object     # uint8 [512 * ceil(d_out/128) * ceil(d_in/128)]
+    d_out: int
+    d_in: int
+
+    def _c(self):
+        return _MXFP4(self.codes.data_ptr(), self.scales.data_ptr(), self.d_out, self.d_in)
+
+    def _check(self):
+        torch = _torch()
+        dev = _need_cuda("codes", self.codes)
+        _need("codes", self.codes, torch.uint8, (self.d_out, self.d_in // 2), dev)
+        _need("scales", self.scales, torch.uint8, (512 * -(-self.d_out // 128) * -(-self.d_in // 128),), dev)
+        return dev
+
+
+@dataclass
+class Act8:
+    """8-bit checkpoint of an activation [T, d_in]: int8 values and one E8M0 scale per 32 of them."""
+    q: object          # int8 [T, d_in]
+    scales: object     # uint8 [T, d_in/32]
+
+    def _c(self):
+        return _ACT8(self.q.data_ptr(), self.scales.data_ptr())
+
+    def _check(self):
+        torch = _torch()
+        dev = _need_cuda("q", self.q)
+        if self.q.dim() != 2:
+            raise ValueError("q must be [T, d_in]")
+        T, d_in = self.q.shape
+        _need("q", self.q, torch.int8, (T, d_in), dev)
+        _need("scales", self.scales, torch.uint8, (T, d_in // 32), dev)
+        return dev
+
+
+def mxfp4_sizes(rows, cols):
+    a, b = ctypes.c_size_t(), ctypes.c_size_t()
+    _check("qlora_mxfp4_sizes", load().qlora_mxfp4_sizes(rows, cols, ctypes.byref(a), ctypes.byref(b)))
+    return a.value, b.value
+
+
+def mxfp4_quantize(W, codes=None, scales=None, stream=None) -> MXFP4Weight:
+    """Quantize a device fp32/bf16 matrix [rows, cols] (a weight or an activation) to MXFP4."""
+    torch = _torch()
+    dev = _need_cuda("W", W)
+    if W.dim() != 2:
+        raise ValueError("W must be [rows, cols]")
+    _contig(W)
+    rows, cols = W.shape
+    dt = _dtype_code(W.dtype)
+    _, ns = mxfp4_sizes(rows, cols)
+    with _run_on(dev, stream):
+        if codes is None:
+            codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=dev)
+        if scales is None:
+            scales = torch.empty(ns, dtype=torch.uint8, device=dev)
+        w = MXFP4Weight(codes, scales, rows, cols)
+        w._check()
+        _check("mxfp4_quantize", load().mxfp4_quantize(_ptr(W), dt, rows, cols, _ptr(codes), _ptr(scales),
+                                                       _stream(stream)))
+    return w
+
+
+def mxfp4_dequantize(w: MXFP4Weight, dtype, out=None, stream=None):
+    torch = _torch()
+    dev = w._check()
+    dt = _dtype_code(dtype)
+    with _run_on(dev, stream):
+        if out is None:
+            out = torch.empty((w.d_out, w.d_in), dtype=dtype, device=dev)
+        else:
+            _need("out", out, dtype, (w.d_out, w.d_in), dev)
+        _check("mxfp4_dequantize", load().mxfp4_dequantize(ctypes.byref(w._c()), _ptr(out), dt, _stream(stream)))
+    return out
+
+
+def qlora_linear_fwd_mxfp4(w: MXFP4Weight, X, A, B, alpha, H=None, U_save=None, ws=None, stream=None,
+                           save_u=True):
+    """H = Q(X) W^T + (alpha/r) (X A^T) B^T over an MXFP4 base, X (bf16) quantized to MXFP4 inside the
+    call for the base product.  Returns (H, U_save)."""
+    torch = _torch()
+    bf = torch.bfloat16
+    dev = w._check()
+    T, r = X.shape[0], A.shape[0]
+    _need("X", X, bf, (T, w.d_in), dev)
+    _need("A", A, bf, (r, w.d_in), dev)
+    _need("B", B, bf, (w.d_out, r), dev)
+    with _run_on(dev, stream):
+        ws = _need_ws(OP_FWD_MXFP4, T, w.d_out, w.d_in, r, dev, ws)
+        if H is None:
+            H = torch.empty((T, w.d_out), dtype=bf, device=dev)
+        else:
+            _need("H", H, bf, (T, w.d_out), dev)
+        if U_save is None:
+            if save_u:
+                U_save = torch.empty((T, r), dtype=bf, device=dev)
+        else:
+            _need("U_save", U_save, bf, (T, r), dev)
+        _check("qlora_linear_fwd_mxfp4", load().qlora_linear_fwd_mxfp4(
+            ctypes.byref(w._c()), _ptr(X), T, _ptr(A), _ptr(B), r, float(alpha), _ptr(H), _ptr(U_save),
+            _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+    return H, U_save
+
+
+def act8_quantize(X, q=None, scales=None, stream=None) -> Act8:
+    """8-bit checkpoint of a device fp32/bf16 activation [T, d_in]."""
+    torch = _torch()
+    dev = _need_cuda("X", X)
+    if X.dim() != 2:
+        raise ValueError("X must be [T, d_in]")
+    _contig(X)
+    T, d_in = X.shape
+    dt = _dtype_code(X.dtype)
+    with _run_on(dev, stream):
+        if q is None:
+            q = torch.empty((T, d_in), dtype=torch.int8, device=dev)
+        if scales is None:
+            scales = torch.empty((T, d_in // 32), dtype=torch.uint8, device=dev)
+        a = Act8(q, scales)
+        a._check()
+        _need("q", q, torch.int8, (T, d_in), dev)
+        _check("qlora_act8_quantize", load().qlora_act8_quantize(_ptr(X), dt, T, d_in, _ptr(q), _ptr(scales),
+                                                                 _stream(stream)))
+    return a
+
+
+def act8_dequantize(a: Act8, dtype, out=None, stream=None):
+    """The checkpoint's values (exact in bf16 and fp32)."""
+    torch = _torch()
+    dev = a._check()
+    dt = _dtype_code(dtype)
+    T, d_in = a.q.shape
+    with _run_on(dev, stream):
+        if out is None:
+            out = torch.empty((T, d_in), dtype=dtype, device=dev)
+        else:
+            _need("out", out, dtype, (T, d_in), dev)
+        _check("qlora_act8_dequantize", load().qlora_act8_dequantize(ctypes.byref(a._c()), T, d_in, _ptr(out), dt,
+                                                                     _stream(stream)))
+    return out
+
+
+def _bwd_act(fn, op, w, dev, X, dH, A, B, alpha, U_saved, dX, dA, dB, ws, want_dx, accumulate, phase, stream):
+    torch = _torch()
+    bf, f32 = torch.bfloat16, torch.float32
+    if phase not in _BWD_PHASES:
+        raise ValueError(f"phase must be one of {sorted(_BWD_PHASES)}")
+    if phase == "dx" and ws is None:
+        raise ValueError('phase="dx" reads the workspace of the preceding phase="grads" call')
+    if accumulate and phase != "dx" and (dA is None or dB is None):
+        raise ValueError("accumulate=True adds into dA and dB: both must be given")
+    T, r = dH.shape[0], A.shape[0]
+    x8 = None
+    if isinstance(X, Act8):
+        if X._check() != dev:
+            raise ValueError(f"the checkpoint is on {X.q.device}, expected {dev}")
+        _need("X.q", X.q, torch.int8, (T, w.d_in), dev)
+        x8 = X._c()
+    else:
+        _need("X", X, bf, (T, w.d_in), dev)
+    _need("dH", dH, bf, (T, w.d_out), dev)
+    _need("A", A, bf, (r, w.d_in), dev)
+    _need("B", B, bf, (w.d_out, r), dev)
+    for name, t, dt, shape in (("U_saved", U_saved, bf, (T, r)), ("dX", dX, bf, (T, w.d_in)),
+                               ("dA", dA, f32, (r, w.d_in)), ("dB", dB, f32, (w.d_out, r))):
+        if t is not None:
+            _need(name, t, dt, shape, dev)
+    with _run_on(dev, stream):
+        ws = _need_ws(op, T, w.d_out, w.d_in, r, dev, ws)
+        if dX is None and want_dx and phase != "grads":
+            dX = torch.empty((T, w.d_in), dtype=bf, device=dev)
+        if phase != "dx":
+            if dA is None:
+                dA = torch.empty((r, w.d_in), dtype=f32, device=dev)
+            if dB is None:
+                dB = torch.empty((w.d_out, r), dtype=f32, device=dev)
+        flags = _BWD_PHASES[phase] | (BWD_ACCUMULATE if accumulate else 0)
+        p8 = ctypes.byref(x8) if x8 is not None else None
+        act = (p8,) if op == OP_BWD_ACT8 else (None if x8 is not None else _ptr(X), p8)
+        _check(fn, getattr(load(), fn)(
+            ctypes.byref(w._c()), *act, _ptr(dH), T, _ptr(A), _ptr(B), r, float(alpha), _ptr(U_saved), _ptr(dX),
+            _ptr(dA), _ptr(dB), _ptr(ws), ws.numel() * ws.element_size(), flags, _stream(stream)))
+    return dX, dA, dB
+
+
+def qlora_linear_bwd_mxfp4(w: MXFP4Weight, X, dH, A, B, alpha, U_saved=None, dX=None, dA=None, dB=None,
+                           ws=None, stream=None, want_dx=True, accumulate=False, phase="all"):
+    """Backward of qlora_linear_fwd_mxfp4 from X, a bf16 tensor or the Act8 checkpoint of one.
+    Returns (dX, dA, dB); dA, dB fp32.  accumulate and phase as in qlora_linear_bwd."""
+    return _bwd_act("qlora_linear_bwd_mxfp4", OP_BWD_MXFP4, w, w._check(), X, dH, A, B, alpha, U_saved, dX, dA, dB,
+                    ws, want_dx, accumulate, phase, stream)
+
+
+def qlora_linear_bwd_act8(w: NF4Weight, X8: Act8, dH, A, B, alpha, U_saved=None, dX=None, dA=None, dB=None,
+                          ws=None, stream=None, want_dx=True, accumulate=False, phase="all"):
+    """qlora_linear_bwd (bf16) over an NF4 base from the 8-bit checkpoint of X.  Returns (dX, dA, dB)."""
+    torch = _torch()
+    if not isinstance(X8, Act8):
+        raise TypeError("X8 must be an Act8 checkpoint (act8_quantize)")
+    dev = _need_cuda("codes", w.codes)
+    _need("codes", w.codes, torch.uint8, (w.d_out, w.d_in // 2), dev)
+    for name, t in (("absmax_q", w.absmax_q), ("c2", w.c2)):
+        if t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    return _bwd_act("qlora_linear_bwd_act8", OP_BWD_ACT8, w, dev, X8, dH, A, B, alpha, U_saved, dX, dA, dB, ws,
+                    want_dx, accumulate, phase, stream)
 
 
 def get_device_error(stream=None) -> int:

@@ -1,0 +1,573 @@
+// mx_api.cuh -- host side of the microscaled entry points (included by qlora_api.cu): planning,
+// argument checks and launch sequences of the MXFP4 layer, the 8-bit activation checkpoints and the
+// backward passes that read them.
+#pragma once
+
+namespace {
+
+// ======================================================================= planning
+
+constexpr int64_t kMaxDim = 1LL << 30;
+
+qlora_status mx_check_dims(int64_t rows, int64_t cols) {
+    if (rows < 1 || rows > kMaxDim || cols < 64 || cols % 64 || cols > kMaxDim) return QLORA_ERR_UNSUPPORTED;
+    if (cdiv(rows, 128) * mx_col_tiles(cols) > 0x7FFFFFFFLL) return QLORA_ERR_UNSUPPORTED;
+    return QLORA_OK;
+}
+inline size_t mx_scale_bytes(int64_t rows, int64_t cols) {
+    return static_cast<size_t>(cdiv(rows, 128)) * mx_col_tiles(cols) * kMxTileBytes;
+}
+qlora_status check_mxfp4(const qlora_mxfp4* w) {
+    if (!w || !aligned16(w->codes) || !aligned16(w->scales)) return QLORA_ERR_INVALID_ARG;
+    return mx_check_dims(w->d_out, w->d_in);
+}
+
+// Routes of the MXFP4 forward by the number of tokens.
+enum MxRoute { kMxDecode, kMxStream64, kMxStream128 };
+MxRoute mx_route(int64_t T) {
+    if (T <= kMxDecodeT) return kMxDecode;
+    return T <= 64 ? kMxStream64 : kMxStream128;
+}
+
+// Ranks of a weight-stream cluster: as many of 8, 4, 2, 1 as K has stages for and the resident CTAs
+// (slots) can take at once.
+int mx_ranks(int64_t tiles, int64_t chunks, int64_t slots) {
+    for (int c = 8; c > 1; c >>= 1)
+        if (chunks >= c && tiles * c <= slots) return c;
+    return 1;
+}
+
+struct MxFwdPlan {
+    int RP = 0, split_u = 1;
+    size_t codes = 0, scales = 0, us = 0, b_pad = 0, part = 0, total = 0;
+};
+MxFwdPlan mx_fwd_plan(int64_t T, int64_t d_out, int64_t d_in, int r) {
+    MxFwdPlan p;
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t o = off;
+        off = align256(off + bytes);
+        return o;
+    };
+    p.RP = pad_rank(r);
+    p.codes = take(static_cast<size_t>(T) * d_in / 2);
+    p.scales = take(mx_scale_bytes(T, d_in));
+    p.us = take(static_cast<size_t>(T) * p.RP * 2);
+    if (r % 8) p.b_pad = take(static_cast<size_t>(d_out) * p.RP * 2);
+    if (mx_route(T) != kMxDecode) {
+        p.split_u = choose_split(cdiv(T, kBM), cdiv(d_in, kBK));
+        p.part = take(static_cast<size_t>(p.split_u) * T * p.RP * 4);
+    }
+    p.total = off;
+    return p;
+}
+
+// The backward of an MXFP4 or NF4 base from a bf16 activation or an 8-bit checkpoint.
+struct MxBwdPlan {
+    int RP = 0, split_u = 1, split_g = 1, split_da = 1, split_db = 1;
+    size_t b_pad = 0, dh_pad = 0, u_hi = 0, u_lo = 0, g_hi = 0, g_lo = 0, part = 0, g2 = 0, total = 0;
+};
+// k_act_gemm runs one CTA per SM: one wave of them.
+int act_split(int64_t tiles, int64_t k_steps) {
+    int64_t s = std::max<int64_t>(1, kSmsForSplit / tiles);
+    s = std::min<int64_t>(s, std::max<int64_t>(1, k_steps / 4));
+    return static_cast<int>(cdiv(k_steps, cdiv(k_steps, s)));
+}
+MxBwdPlan mx_bwd_plan(int64_t T, int64_t d_out, int64_t d_in, int r) {
+    MxBwdPlan p;
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t o = off;
+        off = align256(off + bytes);
+        return o;
+    };
+    p.RP = pad_rank(r);
+    const size_t rp = static_cast<size_t>(p.RP), row = static_cast<size_t>(T) * rp;
+    if (r % 8) p.b_pad = take(static_cast<size_t>(d_out) * rp * 2);
+    if (d_out % 8) p.dh_pad = take(static_cast<size_t>(T) * ((d_out + 7) / 8 * 8) * 2);
+    p.u_hi = take(row * 2);
+    p.u_lo = take(row * 2);
+    p.g_hi = take(row * 2);
+    p.g_lo = take(row * 2);
+    p.split_u = choose_split(cdiv(T, kBM), cdiv(d_in, kBK));
+    p.split_g = choose_split(cdiv(T, kBM), cdiv(d_out, kBK));
+    p.split_da = act_split(cdiv(d_in, 128), cdiv(T, 64));
+    p.split_db = act_split(cdiv(d_out, 128), cdiv(T, 64));
+    size_t part = static_cast<size_t>(std::max(p.split_u, p.split_g)) * row * 4;
+    part = std::max(part, static_cast<size_t>(p.split_da) * d_in * r * 4);
+    part = std::max(part, static_cast<size_t>(p.split_db) * d_out * rp * 4);
+    p.part = take(part);
+    p.g2 = take(g2_schedule(T, d_in, d_out).bytes());
+    p.total = off;
+    return p;
+}
+
+size_t mx_workspace_bytes(int op, qlora_dtype dtype, int64_t T, int64_t d_out, int64_t d_in, int32_t r) {
+    if (dtype != QLORA_BF16 || T < 1 || T > kMaxDim || r < 1 || r > 128) return 0;
+    if (mx_check_dims(d_out, d_in) != QLORA_OK) return 0;
+    if (op == QLORA_OP_FWD_MXFP4)
+        return mx_check_dims(T, d_in) == QLORA_OK ? mx_fwd_plan(T, d_out, d_in, r).total : 0;
+    return mx_bwd_plan(T, d_out, d_in, r).total;
+}
+
+// ======================================================================= launchers
+
+template <typename K>
+qlora_status allow_smem(K kern, int bytes, std::atomic<uint64_t>& configured) {
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(configured.load() & bit)) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+            return QLORA_ERR_CUDA;
+        configured.fetch_or(bit);
+    }
+    return QLORA_OK;
+}
+
+template <int NT>
+qlora_status launch_mx_stream(const CUtensorMap& tw, const CUtensorMap& tx, const CUtensorMap& tb,
+                              const CUtensorMap& tu, MxStreamArgs g, cudaStream_t st) {
+    using L = MxStreamCfg<NT>;
+    static std::atomic<uint64_t> configured{0};
+    QL_TRY(allow_smem(k_mx_stream<NT>, L::kTotal, configured));
+    const int64_t tiles = cdiv(g.d_out, 128), tok = cdiv(g.T, NT);
+    // one CTA per SM above 64 tokens, two below
+    g.ranks = mx_ranks(tiles * tok, cdiv(g.k64, 4), NT <= 64 ? 2 * kSmsForSplit : kSmsForSplit);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(g.ranks);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles * g.ranks), static_cast<unsigned>(tok));
+    cfg.blockDim = dim3(L::kThreads);
+    cfg.dynamicSmemBytes = L::kTotal;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = g.ranks > 1 ? 2 : 1;
+    if (cudaLaunchKernelEx(&cfg, k_mx_stream<NT>, tw, tx, tb, tu, g) != cudaSuccess) return QLORA_ERR_CUDA;
+    QL_LAUNCH_CHECK();
+    return QLORA_OK;
+}
+
+template <int MODE, int RPT>
+qlora_status launch_act_gemm(const CUtensorMap& ta, const CUtensorMap& tb0, const CUtensorMap& tb1,
+                             const ActGemmArgs& g, cudaStream_t st) {
+    using L = ActGemmSmem<MODE, RPT>;
+    static std::atomic<uint64_t> configured{0};
+    QL_TRY(allow_smem(k_act_gemm<MODE, RPT>, L::kTotal, configured));
+    const dim3 grid(static_cast<unsigned>(cdiv(g.M, 128)), static_cast<unsigned>(g.split));
+    if (launch_pdl(k_act_gemm<MODE, RPT>, grid, dim3(320), L::kTotal, st, ta, tb0, tb1, g) != cudaSuccess)
+        return QLORA_ERR_CUDA;
+    QL_LAUNCH_CHECK();
+    return QLORA_OK;
+}
+template <int MODE>
+qlora_status act_gemm(int RP, const CUtensorMap& ta, const CUtensorMap& tb0, const CUtensorMap& tb1,
+                      const ActGemmArgs& g, cudaStream_t st) {
+    return RP == 64 ? launch_act_gemm<MODE, 64>(ta, tb0, tb1, g, st) : launch_act_gemm<MODE, 128>(ta, tb0, tb1, g, st);
+}
+
+// bf16 [rows, cols] with row stride ld, 128-byte swizzle, 64 columns x box_rows; columns past
+// `cols` are filled with 0 (cols need not be whole 16-byte units, ld does).
+qlora_status tmap_rank(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld, uint32_t box_rows) {
+    return tmap_bf16(m, base, rows, cols, ld, box_rows);
+}
+
+// dX = dH W4 + (sG) A: the fused decode GEMM with its decoders reading MXFP4.
+qlora_status mx_dx_gemm(const qlora_mxfp4* w, const void* dH, int64_t dh_ld, int64_t T, const void* g_hi,
+                        const void* A, int RP, int r, void* dX, void* g2ws, int* err, cudaStream_t st) {
+    const int64_t d_out = w->d_out, d_in = w->d_in;
+    CUtensorMap ta, tc, tax, tbx;
+    QL_TRY(tmap_bf16(&ta, dH, T, d_out, dh_ld, 128));
+    QL_TRY(tmap_u8(&tc, w->codes, d_out, d_in / 2, d_in / 2, 64, 64));
+    QL_TRY(tmap_bf16(&tax, g_hi, T, RP, RP, 128));
+    QL_TRY(tmap_bf16(&tbx, A, r, d_in, d_in, 64));
+    Gemm2Args g{};
+    g.M = static_cast<int>(T);
+    g.N = static_cast<int>(d_in);
+    g.k_steps = static_cast<int>(cdiv(d_out, 64));
+    g.ext_steps = RP / 64;
+    g.ext_k16_last = static_cast<int>(std::min<int64_t>(4, cdiv(r - 64 * (g.ext_steps - 1), 16)));
+    g.m_tiles = static_cast<int>(cdiv(T, 256));
+    g.n_tiles = static_cast<int>(cdiv(d_in, 256));
+    g.mx_scales = w->scales;
+    g.mx_col_tiles = static_cast<int>(mx_col_tiles(d_in));
+    g.nf4_rows = static_cast<int>(d_out);
+    g.nf4_bpr = static_cast<int>(d_in / 64);
+    g.out = static_cast<__nv_bfloat16*>(dX);
+    g.ld_out = d_in;
+    g.err = err;
+    g.wait_ns = kWaitNs;
+    const G2Sched sch = g2_schedule(T, d_in, d_out);
+    g.split_tiles = sch.split_tiles;
+    if (sch.split_tiles > 0) {
+        g.part = static_cast<float*>(g2ws);
+        g.cnt = reinterpret_cast<int*>(static_cast<uint8_t*>(g2ws) + sch.part_bytes);
+        if (cudaMemsetAsync(g.cnt, 0, sch.cnt_bytes, st) != cudaSuccess) return QLORA_ERR_CUDA;
+    }
+    auto kern = k_nf4_gemm2<true, false, kWMxfp4>;
+    static std::atomic<uint64_t> configured{0};
+    QL_TRY(allow_smem(kern, G2Smem<false>::kTotal, configured));
+    if (launch_pdl(kern, dim3(2 * sch.pairs), dim3(G2Smem<false>::kThreads), G2Smem<false>::kTotal, st, ta, tc, tax,
+                   tbx, g) != cudaSuccess)
+        return QLORA_ERR_CUDA;
+    QL_LAUNCH_CHECK();
+    return QLORA_OK;
+}
+
+// ======================================================================= sequences
+
+qlora_status mx_fwd(const qlora_mxfp4* w, const void* X, int64_t T, const void* A, const void* B, int r, float s,
+                    void* H, void* U_save, void* ws, int* err, cudaStream_t st) {
+    using bf = __nv_bfloat16;
+    const int64_t d_out = w->d_out, d_in = w->d_in;
+    const MxFwdPlan p = mx_fwd_plan(T, d_out, d_in, r);
+    const MxRoute route = mx_route(T);
+    const int RP = p.RP;
+    auto* codes = at<uint8_t>(ws, p.codes);
+    auto* scales = at<uint8_t>(ws, p.scales);
+    auto* us = at<bf>(ws, p.us);
+    // B as the extension operand: the caller's where its rows are whole 16-byte units (the tensor
+    // map fills the rank padding with 0), else a padded copy
+    const bool direct = r % 8 == 0;
+    const void* b_src = direct ? B : at<void>(ws, p.b_pad);
+    const int b_ld = direct ? r : RP;
+    // The first kernel is launched without programmatic dependent launch: whatever wrote the weight
+    // and whatever used this workspace has finished before it starts.
+    if (route == kMxDecode) {
+        MxPrepArgs a{};
+        a.X = static_cast<const bf*>(X);
+        a.A = static_cast<const bf*>(A);
+        a.B = static_cast<const bf*>(B);
+        a.T = static_cast<int>(T);
+        a.r = r;
+        a.col_tiles = static_cast<int>(mx_col_tiles(d_in));
+        a.ld_us = RP;
+        a.ld_b = RP;
+        a.d_in = d_in;
+        a.d_out = d_out;
+        a.s = s;
+        a.codes = codes;
+        a.scales = scales;
+        a.u_save = static_cast<bf*>(U_save);
+        a.us = us;
+        a.b_pad = direct ? nullptr : at<bf>(ws, p.b_pad);
+        const int pad_ctas = direct ? 0 : static_cast<int>(std::min<int64_t>(cdiv(d_out * RP, 256), kSmsForSplit));
+        k_mx_prepare<<<static_cast<unsigned>(a.col_tiles + r + pad_ctas), 256, 0, st>>>(a);
+        QL_LAUNCH_CHECK();
+    } else {
+        k_mxfp4_quantize<bf><<<static_cast<unsigned>(cdiv(T, 128) * mx_col_tiles(d_in)), 256, 0, st>>>(
+            static_cast<const bf*>(X), T, d_in, codes, scales);
+        QL_LAUNCH_CHECK();
+        if (!direct)
+            QL_TRY(pad_bf16(static_cast<const bf*>(B), d_out, r, r, at<bf>(ws, p.b_pad), d_out, RP, 0, RP, st));
+        QL_TRY(compute_u_bf16(X, T, d_in, A, r, RP, r, s, p.split_u, at<float>(ws, p.part), static_cast<bf*>(U_save),
+                              nullptr, us, err, st));
+    }
+    CUtensorMap tw, tx, tb, tu;
+    const uint32_t nt = route == kMxDecode ? 16 : (route == kMxStream64 ? 64 : 128);
+    QL_TRY(tmap_u8_sw128(&tw, w->codes, d_out, d_in / 2, d_in / 2, 128));
+    QL_TRY(tmap_u8_sw128(&tx, codes, T, d_in / 2, d_in / 2, nt));
+    QL_TRY(tmap_rank(&tb, b_src, d_out, r, b_ld, 128));
+    QL_TRY(tmap_rank(&tu, us, T, r, RP, nt));
+    MxStreamArgs g{};
+    g.T = static_cast<int>(T);
+    g.d_out = static_cast<int>(d_out);
+    g.k64 = static_cast<int>(d_in / 64);
+    g.col_tiles = static_cast<int>(mx_col_tiles(d_in));
+    g.ext_steps = RP / 64;
+    g.ext_k16_last = static_cast<int>(cdiv(r - 64 * (g.ext_steps - 1), 16));
+    g.w_scales = w->scales;
+    g.x_scales = scales;
+    g.out = static_cast<bf*>(H);
+    g.err = err;
+    g.wait_ns = kWaitNs;
+    if (route == kMxDecode) return launch_mx_stream<16>(tw, tx, tb, tu, g, st);
+    if (route == kMxStream64) return launch_mx_stream<64>(tw, tx, tb, tu, g, st);
+    return launch_mx_stream<128>(tw, tx, tb, tu, g, st);
+}
+
+// The base weight of a backward: exactly one of the two.
+struct MxBase {
+    const qlora_nf4* nf4;
+    const qlora_mxfp4* mx;
+};
+
+// X (bf16) or X8 (8-bit checkpoint), exactly one of the two, is the layer's activation.
+qlora_status mx_bwd(MxBase base, const void* X, const qlora_act8* X8, const void* dH, int64_t T, const void* A,
+                    const void* B, int r, float s, const void* U_saved, void* dX, float* dA, float* dB, void* ws,
+                    int acc, BwdPhase phase, int* err, cudaStream_t st) {
+    using bf = __nv_bfloat16;
+    const int64_t d_out = base.mx ? base.mx->d_out : base.nf4->d_out;
+    const int64_t d_in = base.mx ? base.mx->d_in : base.nf4->d_in;
+    const MxBwdPlan p = mx_bwd_plan(T, d_out, d_in, r);
+    const int RP = p.RP;
+    auto* part = at<float>(ws, p.part);
+    auto* u_hi = at<bf>(ws, p.u_hi);
+    auto* u_lo = at<bf>(ws, p.u_lo);
+    auto* g_hi = at<bf>(ws, p.g_hi);
+    auto* g_lo = at<bf>(ws, p.g_lo);
+    int64_t dh_ld = d_out;
+    if (d_out % 8) {          // rows that are no whole 16-byte units cannot be read by a tensor map
+        dh_ld = (d_out + 7) / 8 * 8;
+        QL_TRY(pad_bf16(static_cast<const bf*>(dH), T, d_out, d_out, at<bf>(ws, p.dh_pad), T, dh_ld, 0, dh_ld, st));
+        dH = at<void>(ws, p.dh_pad);
+    }
+    auto pair = [&](int split, float scale, bf* hi, bf* lo) -> qlora_status {
+        if (launch_pdl(k_finalize_pair, grid1d(T * RP), dim3(256), 0, st, part, split, T, r, RP, scale, RP, hi, lo) !=
+            cudaSuccess)
+            return QLORA_ERR_CUDA;
+        QL_LAUNCH_CHECK();
+        return QLORA_OK;
+    };
+    ActGemmArgs g{};
+    g.N = r;
+    g.err = err;
+    g.wait_ns = kWaitNs;
+    g.part = part;
+    int u_nb = 2;                 // matrices that make up U
+    const void* u_src = u_hi;
+    int u_ld = RP;
+    if (phase != kBwdDx) {
+        // U = X~ A^T, unless the forward kept it
+        if (U_saved) {
+            u_nb = 1;
+            if (r % 8 == 0) {
+                u_src = U_saved;
+                u_ld = r;
+            } else {
+                QL_TRY(pad_bf16(static_cast<const bf*>(U_saved), T, r, r, u_hi, T, RP, 0, RP, st));
+            }
+        } else if (X8) {
+            CUtensorMap ta, tb;
+            QL_TRY(tmap_u8(&ta, X8->q, T, d_in, d_in, 64, 128));
+            QL_TRY(tmap_bf16(&tb, A, r, d_in, d_in, static_cast<uint32_t>(RP)));
+            g.M = static_cast<int>(T);
+            g.K = d_in;
+            g.k_steps = static_cast<int>(d_in / 64);
+            g.split = p.split_u;
+            g.nb = 1;
+            g.scales = X8->scales;
+            g.ld_scales = d_in / 32;
+            g.ldp = RP;
+            QL_TRY((act_gemm<kActInt8K>(RP, ta, tb, tb, g, st)));
+            QL_TRY(pair(p.split_u, 1.f, u_hi, u_lo));
+        } else {
+            CUtensorMap ta, tb;
+            QL_TRY(tmap_bf16(&ta, X, T, d_in, d_in, kBM));
+            QL_TRY(tmap_bf16(&tb, A, r, d_in, d_in, RP));
+            QL_TRY(skinny_gemm(false, false, RP, r, ta, tb, T, cdiv(d_in, kBK), p.split_u, part, err, st));
+            QL_TRY(pair(p.split_u, 1.f, u_hi, u_lo));
+        }
+        // s G = s dH B
+        const void* b_src = B;
+        int b_ld = r;
+        if (r % 8) {
+            QL_TRY(pad_bf16(static_cast<const bf*>(B), d_out, r, r, at<bf>(ws, p.b_pad), d_out, RP, 0, RP, st));
+            b_src = at<void>(ws, p.b_pad);
+            b_ld = RP;
+        }
+        CUtensorMap ta, tb;
+        QL_TRY(tmap_bf16(&ta, dH, T, d_out, dh_ld, kBM));
+        QL_TRY(tmap_bf16(&tb, b_src, d_out, b_ld, b_ld, 64));
+        QL_TRY(skinny_gemm(false, true, RP, r, ta, tb, T, cdiv(d_out, kBK), p.split_g, part, err, st));
+        QL_TRY(pair(p.split_g, s, g_hi, g_lo));
+    }
+    // dX = dH W + (sG) A; the adapter term's s G is rounded to bf16 (2^-9 of that term, as dX itself is)
+    if (dX && phase != kBwdGrads) {
+        if (base.mx)
+            QL_TRY(mx_dx_gemm(base.mx, dH, dh_ld, T, g_hi, A, RP, r, dX, at<void>(ws, p.g2), err, st));
+        else
+            QL_TRY(nf4_gemm(true, base.nf4, dH, T, g_hi, A, RP, r, r, dX, at<void>(ws, p.g2), err, st, nullptr, nullptr,
+                            nullptr, dh_ld));
+    }
+    if (phase == kBwdDx) return QLORA_OK;
+    // dA^T[d_in, r] = X~^T (s G), partials stored as [split][r][d_in]
+    {
+        CUtensorMap ta, t0, t1;
+        QL_TRY(tmap_bf16(&t0, g_hi, T, r, RP, 64));
+        QL_TRY(tmap_bf16(&t1, g_lo, T, r, RP, 64));
+        g.M = static_cast<int>(d_in);
+        g.K = T;
+        g.k_steps = static_cast<int>(cdiv(T, 64));
+        g.split = p.split_da;
+        g.nb = 2;
+        g.transposed = 1;
+        if (X8) {
+            QL_TRY(tmap_u8(&ta, X8->q, T, d_in, d_in, 128, 64));
+            g.scales = X8->scales;
+            g.ld_scales = d_in / 32;
+            QL_TRY((act_gemm<kActInt8Mn>(RP, ta, t0, t1, g, st)));
+        } else {
+            QL_TRY(tmap_bf16(&ta, X, T, d_in, d_in, 64));
+            QL_TRY((act_gemm<kActBf16Mn>(RP, ta, t0, t1, g, st)));
+        }
+        const int64_t n = static_cast<int64_t>(r) * d_in;
+        if (launch_pdl(k_finalize_flat, grid1d(n), dim3(256), 0, st, part, p.split_da, n, 1.f, dA, acc) != cudaSuccess)
+            return QLORA_ERR_CUDA;
+        QL_LAUNCH_CHECK();
+    }
+    // dB[d_out, r] = s dH^T U
+    {
+        CUtensorMap ta, t0, t1;
+        QL_TRY(tmap_bf16(&ta, dH, T, d_out, dh_ld, 64));
+        QL_TRY(tmap_bf16(&t0, u_src, T, r, u_ld, 64));
+        QL_TRY(tmap_bf16(&t1, u_nb > 1 ? u_lo : u_src, T, r, u_ld, 64));
+        g.M = static_cast<int>(d_out);
+        g.split = p.split_db;
+        g.nb = u_nb;
+        g.transposed = 0;
+        g.ldp = RP;
+        QL_TRY((act_gemm<kActBf16Mn>(RP, ta, t0, t1, g, st)));
+        if (launch_pdl(k_finalize_strided, grid1d(d_out * r), dim3(256), 0, st, part, p.split_db, d_out, r, RP, s, dB,
+                       acc) != cudaSuccess)
+            return QLORA_ERR_CUDA;
+        QL_LAUNCH_CHECK();
+    }
+    return QLORA_OK;
+}
+
+constexpr uint32_t kBwdFlags = QLORA_BWD_ACCUMULATE | QLORA_BWD_GRADS_ONLY | QLORA_BWD_DX_FROM_WS;
+
+// Checks shared by the two backward entries; X or X8 is the activation (checked by the caller's
+// rule), then the launch sequence.
+qlora_status mx_bwd_entry(MxBase base, const void* X, const qlora_act8* X8, const void* dH, int64_t T, const void* A,
+                          const void* B, int32_t r, float alpha, const void* U_saved, void* dX, float* dA, float* dB,
+                          void* ws, size_t ws_bytes, uint32_t flags, cudaStream_t st) {
+    if (T < 1 || T > kMaxDim || r < 1 || r > 128) return QLORA_ERR_UNSUPPORTED;
+    if (flags & ~kBwdFlags) return QLORA_ERR_INVALID_ARG;
+    const bool grads_only = flags & QLORA_BWD_GRADS_ONLY, dx_only = flags & QLORA_BWD_DX_FROM_WS;
+    if (grads_only && dx_only) return QLORA_ERR_INVALID_ARG;
+    if (X8 ? (X != nullptr || !aligned16(X8->q) || !aligned16(X8->scales)) : !aligned16(X)) return QLORA_ERR_INVALID_ARG;
+    if (!aligned16(dH) || !aligned16(A) || !aligned16(B) || !aligned16_or_null(U_saved)) return QLORA_ERR_INVALID_ARG;
+    if (dx_only ? !aligned16(dX) : (!aligned16(dA) || !aligned16(dB))) return QLORA_ERR_INVALID_ARG;
+    if (!grads_only && !aligned16_or_null(dX)) return QLORA_ERR_INVALID_ARG;
+    const int64_t d_out = base.mx ? base.mx->d_out : base.nf4->d_out;
+    const int64_t d_in = base.mx ? base.mx->d_in : base.nf4->d_in;
+    QL_TRY(check_ws(ws, ws_bytes, mx_bwd_plan(T, d_out, d_in, r).total));
+    int* err = nullptr;
+    QL_TRY(err_word(&err, st));
+    return mx_bwd(base, X, X8, dH, T, A, B, r, alpha / static_cast<float>(r), U_saved, dX, dA, dB, ws,
+                  (flags & QLORA_BWD_ACCUMULATE) ? 1 : 0, grads_only ? kBwdGrads : (dx_only ? kBwdDx : kBwdAll), err, st);
+}
+
+}  // namespace
+
+// ======================================================================= C ABI
+
+extern "C" {
+
+qlora_status qlora_mxfp4_sizes(int64_t rows, int64_t cols, size_t* codes_bytes, size_t* scale_bytes) {
+    if (!codes_bytes || !scale_bytes) return QLORA_ERR_INVALID_ARG;
+    QL_TRY(mx_check_dims(rows, cols));
+    *codes_bytes = static_cast<size_t>(rows) * cols / 2;
+    *scale_bytes = mx_scale_bytes(rows, cols);
+    return QLORA_OK;
+}
+
+qlora_status mxfp4_quantize(const void* W, qlora_dtype w_dtype, int64_t rows, int64_t cols, uint8_t* codes,
+                            uint8_t* scales, cudaStream_t stream) {
+    if (!aligned16(W) || !aligned16(codes) || !aligned16(scales)) return QLORA_ERR_INVALID_ARG;
+    if (w_dtype != QLORA_F32 && w_dtype != QLORA_BF16) return QLORA_ERR_INVALID_ARG;
+    QL_TRY(mx_check_dims(rows, cols));
+    const unsigned tiles = static_cast<unsigned>(cdiv(rows, 128) * mx_col_tiles(cols));
+    if (w_dtype == QLORA_F32)
+        k_mxfp4_quantize<float><<<tiles, 256, 0, stream>>>(static_cast<const float*>(W), rows, cols, codes, scales);
+    else
+        k_mxfp4_quantize<__nv_bfloat16><<<tiles, 256, 0, stream>>>(static_cast<const __nv_bfloat16*>(W), rows, cols,
+                                                                   codes, scales);
+    QL_LAUNCH_CHECK();
+    return QLORA_OK;
+}
+
+qlora_status mxfp4_dequantize(const qlora_mxfp4* w, void* W_out, qlora_dtype out_dtype, cudaStream_t stream) {
+    if (!aligned16(W_out) || (out_dtype != QLORA_F32 && out_dtype != QLORA_BF16)) return QLORA_ERR_INVALID_ARG;
+    QL_TRY(check_mxfp4(w));
+    const dim3 grid = grid1d(w->d_out * w->d_in / 8);
+    if (out_dtype == QLORA_F32)
+        k_mxfp4_dequant<float><<<grid, 256, 0, stream>>>(w->codes, w->scales, w->d_out, w->d_in,
+                                                         static_cast<float*>(W_out));
+    else
+        k_mxfp4_dequant<__nv_bfloat16><<<grid, 256, 0, stream>>>(w->codes, w->scales, w->d_out, w->d_in,
+                                                                 static_cast<__nv_bfloat16*>(W_out));
+    QL_LAUNCH_CHECK();
+    return QLORA_OK;
+}
+
+qlora_status qlora_linear_fwd_mxfp4(const qlora_mxfp4* w, const void* X, int64_t T, const void* A, const void* B,
+                                    int32_t r, float alpha, void* H, void* U_save, void* ws, size_t ws_bytes,
+                                    cudaStream_t stream) {
+    QL_TRY(check_mxfp4(w));
+    QL_TRY(mx_check_dims(T, w->d_in));
+    if (r < 1 || r > 128) return QLORA_ERR_UNSUPPORTED;
+    if (!aligned16(X) || !aligned16(A) || !aligned16(B) || !aligned16(H) || !aligned16_or_null(U_save))
+        return QLORA_ERR_INVALID_ARG;
+    QL_TRY(check_ws(ws, ws_bytes, mx_fwd_plan(T, w->d_out, w->d_in, r).total));
+    int* err = nullptr;
+    QL_TRY(err_word(&err, stream));
+    return mx_fwd(w, X, T, A, B, r, alpha / static_cast<float>(r), H, U_save, ws, err, stream);
+}
+
+qlora_status qlora_linear_bwd_mxfp4(const qlora_mxfp4* w, const void* X, const qlora_act8* X8, const void* dH,
+                                    int64_t T, const void* A, const void* B, int32_t r, float alpha,
+                                    const void* U_saved, void* dX, float* dA, float* dB, void* ws, size_t ws_bytes,
+                                    uint32_t flags, cudaStream_t stream) {
+    QL_TRY(check_mxfp4(w));
+    return mx_bwd_entry(MxBase{nullptr, w}, X, X8, dH, T, A, B, r, alpha, U_saved, dX, dA, dB, ws, ws_bytes, flags,
+                        stream);
+}
+
+qlora_status qlora_linear_bwd_act8(const qlora_nf4* w, const qlora_act8* X8, const void* dH, int64_t T, const void* A,
+                                   const void* B, int32_t r, float alpha, const void* U_saved, void* dX, float* dA,
+                                   float* dB, void* ws, size_t ws_bytes, uint32_t flags, cudaStream_t stream) {
+    QL_TRY(check_nf4(w));
+    if (!X8) return QLORA_ERR_INVALID_ARG;
+    return mx_bwd_entry(MxBase{w, nullptr}, nullptr, X8, dH, T, A, B, r, alpha, U_saved, dX, dA, dB, ws, ws_bytes,
+                        flags, stream);
+}
+
+qlora_status qlora_act8_sizes(int64_t T, int64_t d_in, size_t* q_bytes, size_t* scale_bytes) {
+    if (!q_bytes || !scale_bytes) return QLORA_ERR_INVALID_ARG;
+    if (T < 1 || T > kMaxDim || d_in < 64 || d_in % 64 || d_in > kMaxDim) return QLORA_ERR_UNSUPPORTED;
+    *q_bytes = static_cast<size_t>(T) * d_in;
+    *scale_bytes = static_cast<size_t>(T) * d_in / 32;
+    return QLORA_OK;
+}
+
+qlora_status qlora_act8_quantize(const void* X, qlora_dtype x_dtype, int64_t T, int64_t d_in, int8_t* q,
+                                 uint8_t* scales, cudaStream_t stream) {
+    if (!aligned16(X) || !aligned16(q) || !aligned16(scales)) return QLORA_ERR_INVALID_ARG;
+    if (x_dtype != QLORA_F32 && x_dtype != QLORA_BF16) return QLORA_ERR_INVALID_ARG;
+    size_t qb, sb;
+    QL_TRY(qlora_act8_sizes(T, d_in, &qb, &sb));
+    const int64_t n8 = T * d_in / 8;
+    if (x_dtype == QLORA_F32)
+        k_act8_quantize<float><<<grid1d(n8), 256, 0, stream>>>(static_cast<const float*>(X), n8, q, scales);
+    else
+        k_act8_quantize<__nv_bfloat16><<<grid1d(n8), 256, 0, stream>>>(static_cast<const __nv_bfloat16*>(X), n8, q,
+                                                                       scales);
+    QL_LAUNCH_CHECK();
+    return QLORA_OK;
+}
+
+qlora_status qlora_act8_dequantize(const qlora_act8* a, int64_t T, int64_t d_in, void* X_out, qlora_dtype out_dtype,
+                                   cudaStream_t stream) {
+    if (!a || !aligned16(a->q) || !aligned16(a->scales) || !aligned16(X_out)) return QLORA_ERR_INVALID_ARG;
+    if (out_dtype != QLORA_F32 && out_dtype != QLORA_BF16) return QLORA_ERR_INVALID_ARG;
+    size_t qb, sb;
+    QL_TRY(qlora_act8_sizes(T, d_in, &qb, &sb));
+    const int64_t n8 = T * d_in / 8;
+    if (out_dtype == QLORA_F32)
+        k_act8_dequant<float><<<grid1d(n8), 256, 0, stream>>>(a->q, a->scales, n8, static_cast<float*>(X_out));
+    else
+        k_act8_dequant<__nv_bfloat16><<<grid1d(n8), 256, 0, stream>>>(a->q, a->scales, n8,
+                                                                      static_cast<__nv_bfloat16*>(X_out));
+    QL_LAUNCH_CHECK();
+    return QLORA_OK;
+}
+
+}  // extern "C"

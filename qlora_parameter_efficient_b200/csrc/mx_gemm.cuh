@@ -1,0 +1,417 @@
+// mx_gemm.cuh -- block-scaled MXFP4 products of the layer's forward (sm_100a kind::mxf4).
+//
+//   H[T, d_out] = X4[T, d_in] W4[d_out, d_in]^T + sU[T, RP] B[d_out, RP]^T
+//
+// Both operands of the main K steps stay 4-bit: tcgen05.mma kind::mxf4.block_scale reads the E2M1
+// codes from swizzled shared memory and the E8M0 scales from tensor memory, and accumulates the
+// exact products of the stored values in fp32, so nothing is decoded.  The adapter enters as bf16
+// kind::f16 K steps into the same accumulator.  A K stage is 256 elements: one 128-byte swizzled row
+// of codes per matrix row, and per 128 rows two stored 512-byte scale tiles, which
+// tcgen05.cp.32x128b.warpx4 copies into four tensor-memory columns each; an MMA (K = 64) takes half
+// a tile, picked by the scale-factor id of its instruction descriptor.
+//
+// k_mx_stream: one CTA per 128 weight rows, the tokens as the (narrow) N operand, K split over the
+//   ranks of a cluster whose partials meet in shared memory.  For token counts whose time is the
+//   weight stream.
+// k_mx_gemm: persistent pairs of CTAs (cta_group::2) on 256 x 256 tiles, for the rest.
+#pragma once
+
+#include "common.cuh"
+#include "mxfp4.cuh"
+#include "nf4_gemm2.cuh"
+
+namespace qlora {
+
+// ------------------------------------------------------------------ PTX
+
+// Instruction descriptor of kind::mxf4: E2M1 x E2M1, E8M0 scales, fp32 D, K-major operands.
+// a_id / b_id: which half (0 or 2) of the four scale bytes of a tensor-memory word is used.
+__device__ __forceinline__ uint32_t make_idesc_mxf4(int M, int N, uint32_t a_id, uint32_t b_id) {
+    return (b_id << 4)                                // B scale-factor id
+           | (1u << 7)                                // A format E2M1
+           | (1u << 10)                               // B format E2M1
+           | (static_cast<uint32_t>(N >> 3) << 17)    // N / 8
+           | (1u << 23)                               // scale format E8M0
+           | (static_cast<uint32_t>(M >> 7) << 27)    // M / 128
+           | (a_id << 29);                            // A scale-factor id
+}
+
+template <int CG>
+__device__ __forceinline__ void umma_mxf4_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                             uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+    if constexpr (CG == 1)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(
+                d_tmem),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(
+                d_tmem),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
+}
+
+// Copy one 512-byte scale tile (32 lines of 16 bytes) to four tensor-memory columns, repeated for
+// the four lane quarters.
+template <int CG>
+__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint32_t saddr) {
+    // no swizzle: 8-line groups of 128 bytes, 128 bytes apart
+    const uint64_t desc = static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (1ull << 16) | (8ull << 32) | (1ull << 46);
+    if constexpr (CG == 1)
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+    else
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+// Prepare a decode-size call (T <= 16) in one launch.  CTAs [0, col_tiles): MXFP4 of X, one scale
+// tile each; [col_tiles, col_tiles + r): one adapter row j each, U[:, j] = X A[j]^T in fp32, written
+// unscaled to u_save (nullable, [T, r]) and as bf16(s U) to us [T, ld_us]; the rest: B copied to rows
+// of ld_b (only where r is not a multiple of 8 and B's rows are no whole 16-byte units).
+// s U in bf16 costs 2^-9 of the adapter term, as the rounding of H costs 2^-9 of H.
+constexpr int kMxDecodeT = 16;
+struct MxPrepArgs {
+    const __nv_bfloat16 *X, *A, *B;
+    int T, r, col_tiles, ld_us, ld_b;
+    int64_t d_in, d_out;
+    float s;
+    uint8_t *codes, *scales;
+    __nv_bfloat16 *u_save, *us, *b_pad;
+};
+__global__ void __launch_bounds__(256) k_mx_prepare(const MxPrepArgs a) {
+    __shared__ __align__(16) uint8_t s_sc[kMxTileBytes];
+    __shared__ float s_red[8][kMxDecodeT];
+    griddep_launch_dependents();
+    const int b = blockIdx.x;
+    if (b < a.col_tiles) {
+        mxfp4_quantize_tile(a.X, a.T, a.d_in, 0, b, a.codes, a.scales, s_sc);
+    } else if (b < a.col_tiles + a.r) {
+        const int j = b - a.col_tiles;
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        float acc[kMxDecodeT];
+#pragma unroll
+        for (int t = 0; t < kMxDecodeT; ++t) acc[t] = 0.f;
+        for (int64_t c = threadIdx.x * 8; c < a.d_in; c += 256 * 8) {
+            float w[8], x[8];
+            load8(a.A + j * a.d_in + c, w);
+#pragma unroll
+            for (int t = 0; t < kMxDecodeT; ++t)
+                if (t < a.T) {
+                    load8(a.X + t * a.d_in + c, x);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) acc[t] = fmaf(w[i], x[i], acc[t]);
+                }
+        }
+#pragma unroll
+        for (int t = 0; t < kMxDecodeT; ++t)
+            if (t < a.T) {
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], o);
+                if (lane == 0) s_red[warp][t] = acc[t];
+            }
+        __syncthreads();
+        if (threadIdx.x < a.T) {
+            const int t = threadIdx.x;
+            float u = 0.f;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) u += s_red[w][t];
+            if (a.u_save) a.u_save[t * a.r + j] = __float2bfloat16_rn(u);
+            a.us[t * a.ld_us + j] = __float2bfloat16_rn(a.s * u);
+        }
+    } else {
+        const int64_t n = a.d_out * a.ld_b;
+        for (int64_t i = static_cast<int64_t>(b - a.col_tiles - a.r) * 256 + threadIdx.x; i < n;
+             i += static_cast<int64_t>(gridDim.x - a.col_tiles - a.r) * 256) {
+            const int64_t row = i / a.ld_b;
+            const int c = static_cast<int>(i - row * a.ld_b);
+            a.b_pad[i] = c < a.r ? a.B[row * a.r + c] : __float2bfloat16_rn(0.f);
+        }
+    }
+}
+
+// Untiled copy of whole scale tiles (16-byte aligned, a multiple of 16 bytes).
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+__device__ __forceinline__ void st_cluster_f32(uint32_t cluster_addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
+}
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+
+// ------------------------------------------------------------------ weight-streaming kernel
+
+struct MxStreamArgs {
+    int T, d_out;
+    int k64;                  // d_in / 64: MMAs of the whole contraction
+    int col_tiles;            // scale tiles per row of tiles (d_in / 128, rounded up)
+    int ranks;                // CTAs per cluster, K split over them
+    int ext_steps;            // adapter K steps of 64, taken by the last rank
+    int ext_k16_last;
+    const uint8_t* w_scales;
+    const uint8_t* x_scales;
+    __nv_bfloat16* out;       // [T, d_out]
+    int* err;
+    uint64_t wait_ns;
+};
+
+// NT: tokens per CTA (the MMA's N): 16 or 64 for calls of up to that many tokens, 128 (a whole scale
+// tile) in several token tiles above.  The cluster has 1, 2, 4 or 8 ranks, so that NT tokens divide
+// evenly over them.
+template <int NT>
+struct MxStreamCfg {
+    static constexpr int kA = 128 * 128;            // codes of 128 weight rows, one stage
+    static constexpr int kB = NT * 128;             // codes of the tokens
+    static constexpr int kSf = 1024;                // two scale tiles (each operand)
+    static constexpr int kStage = kA + kB + 2 * kSf;
+    // two CTAs per SM up to 64 tokens, and one above
+    static constexpr int kStages = NT <= 16 ? 5 : (NT <= 64 ? 3 : 4);
+    static constexpr int kRed = NT * 128 * 4;       // partials of this rank's share of the tokens
+    static constexpr int kTotal = 1024 + kStages * kStage + kRed + 256;
+    static constexpr int kThreads = 192;
+    static constexpr int kAcc = NT < 32 ? 32 : NT;  // accumulator columns
+    static constexpr uint32_t kTmem = NT <= 32 ? 64 : (NT <= 64 ? 128 : 256);   // + 2 x 16 scale columns
+    static_assert(kAcc + 32 <= static_cast<int>(kTmem), "tensor memory");
+    static_assert(kTotal * (NT <= 64 ? 2 : 1) <= 232448, "shared memory budget");
+};
+
+// grid: x = weight tile * ranks + rank, y = token tile; clusters of `ranks` along x.
+// Launched with programmatic dependent launch: the weight's tiles are read before the kernel
+// that quantizes X has finished (that kernel is launched without it, so whatever wrote
+// the weight is done), everything else after.
+template <int NT>
+__global__ void __launch_bounds__(MxStreamCfg<NT>::kThreads)
+    k_mx_stream(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                const __grid_constant__ CUtensorMap tmBx, const __grid_constant__ CUtensorMap tmUx,
+                const MxStreamArgs args) {
+    using L = MxStreamCfg<NT>;
+    constexpr int S = L::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    uint8_t* sA = smem;
+    uint8_t* sB = sA + S * L::kA;
+    uint8_t* sSa = sB + S * L::kB;
+    uint8_t* sSb = sSa + S * L::kSf;
+    float* red = reinterpret_cast<float*>(sSb + S * L::kSf);
+    uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(red) + L::kRed);
+    uint64_t* empty = full + S;
+    uint64_t* accf = empty + S;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(accf + 1);
+    volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int C = args.ranks;
+    const int rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int tile = blockIdx.x / C;
+    const int n0 = tile * 128;
+    const int t0 = blockIdx.y * NT;
+    const int chunks = (args.k64 + 3) / 4;            // stages of 256 elements
+    const int c_begin = static_cast<int>(static_cast<int64_t>(chunks) * rank / C);
+    const int c_end = static_cast<int>(static_cast<int64_t>(chunks) * (rank + 1) / C);
+    const int n_main = c_end - c_begin;
+    const int n_iters = n_main + (rank == C - 1 ? args.ext_steps : 0);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        mbar_init(accf, 1);
+        *abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&tmW);
+        tma_prefetch_desc(&tmX);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, L::kTmem);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    if (C > 1) cluster_arrive();
+    griddep_launch_dependents();
+
+    // MMAs (K = 64) and scale tiles of main stage `it`
+    auto mmas_of = [&](int it) { return min(4, args.k64 - (c_begin + it) * 4); };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            auto load_w = [&](int it) {
+                const int s = it % S;
+                const int c = c_begin + it;
+                const uint32_t sf = static_cast<uint32_t>((mmas_of(it) + 1) / 2) * kMxTileBytes;
+                mbar_arrive_expect_tx(&full[s], L::kA + L::kB + 2 * sf);
+                tma_load_2d(sA + s * L::kA, &tmW, &full[s], c * 128, n0);
+                bulk_load(sSa + s * L::kSf,
+                          args.w_scales + (static_cast<int64_t>(tile) * args.col_tiles + 2 * c) * kMxTileBytes, sf,
+                          &full[s]);
+            };
+            auto load_x = [&](int it) {
+                const int s = it % S;
+                const int c = c_begin + it;
+                const uint32_t sf = static_cast<uint32_t>((mmas_of(it) + 1) / 2) * kMxTileBytes;
+                tma_load_2d(sB + s * L::kB, &tmX, &full[s], c * 128, t0);
+                bulk_load(sSb + s * L::kSf,
+                          args.x_scales + (static_cast<int64_t>(t0 >> 7) * args.col_tiles + 2 * c) * kMxTileBytes, sf,
+                          &full[s]);
+            };
+            const int ahead = min(S, n_main);
+            for (int it = 0; it < ahead; ++it) load_w(it);
+            griddep_wait();
+            for (int it = 0; it < ahead; ++it) load_x(it);
+            int issued = ahead;
+            for (int it = ahead; it < n_iters; ++it) {
+                const int s = it % S;
+                if (!mbar_wait(&empty[s], ((it / S) & 1) ^ 1, abort, args.wait_ns)) {
+                    set_error(args.err, kErrTimeout);
+                    *abort = 1;
+                    break;
+                }
+                if (it < n_main) {
+                    load_w(it);
+                    load_x(it);
+                } else {
+                    const int kx = (it - n_main) * 64;
+                    mbar_arrive_expect_tx(&full[s], L::kA + L::kB);
+                    tma_load_2d(sA + s * L::kA, &tmBx, &full[s], kx, n0);
+                    tma_load_2d(sB + s * L::kB, &tmUx, &full[s], kx, t0);
+                }
+                issued = it + 1;
+            }
+            if (*abort)
+                for (int it = max(0, issued - S); it < issued; ++it)
+                    mbar_wait(&full[it % S], (it / S) & 1, nullptr, args.wait_ns);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t idesc_x = make_idesc_bf16(128, NT, false, false);
+            bool ok = true;
+            for (int it = 0; it < n_iters; ++it) {
+                const int s = it % S;
+                ok = mbar_wait(&full[s], (it / S) & 1, abort, args.wait_ns);
+                // scale columns are used in turn: those of step it - 2 are free once its MMAs are done
+                if (ok && it >= 2) ok = mbar_wait(&empty[(it - 2) % S], ((it - 2) / S) & 1, abort, args.wait_ns);
+                if (!ok) {
+                    set_error(args.err, kErrTimeout);
+                    *abort = 1;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t a = smem_u32(sA + s * L::kA), b = smem_u32(sB + s * L::kB);
+                if (it < n_main) {
+                    const uint32_t sfa = tmem + L::kAcc + (it & 1) * 16, sfb = sfa + 8;
+                    const int nk = mmas_of(it);
+                    for (int h = 0; h < (nk + 1) / 2; ++h) {
+                        tmem_cp_scales<1>(sfa + 4 * h, smem_u32(sSa + s * L::kSf + h * kMxTileBytes));
+                        tmem_cp_scales<1>(sfb + 4 * h, smem_u32(sSb + s * L::kSf + h * kMxTileBytes));
+                    }
+                    for (int k = 0; k < nk; ++k) {
+                        const uint32_t id = (k & 1) * 2;
+                        umma_mxf4_ss<1>(tmem, make_sw128_desc(a + k * 32, 16, 1024),
+                                        make_sw128_desc(b + k * 32, 16, 1024), make_idesc_mxf4(128, NT, id, id),
+                                        sfa + 4 * (k >> 1), sfb + 4 * (k >> 1), (it > 0 || k > 0) ? 1u : 0u);
+                    }
+                } else {
+                    const int nk = it == n_iters - 1 ? args.ext_k16_last : 4;
+                    for (int k = 0; k < nk; ++k)
+                        umma_bf16_ss(tmem, make_sw128_desc(a + k * 32, 16, 1024), make_sw128_desc(b + k * 32, 16, 1024),
+                                     idesc_x, (it > 0 || k > 0) ? 1u : 0u);
+                }
+                umma_commit(&empty[s]);
+            }
+            umma_commit(accf);
+        }
+    }
+    __syncwarp();
+
+    // ------------------------------------------------------------ join the ranks, store
+    const int q = warp & 3;                            // tensor-memory lane quarter of this warp
+    const int row = n0 + q * 32 + lane;                // weight row = output column
+    const uint32_t tbase = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    const int t_end = min(NT, args.T - t0);
+    if (warp >= 2) {
+        if (!mbar_wait_warp(accf, 0, nullptr, args.wait_ns)) {
+            set_error(args.err, kErrTimeout);
+            *abort = 1;
+        }
+        tc_fence_after();
+    }
+    if (C == 1) {
+        griddep_wait();          // earlier kernels of the stream may still read or write H
+        if (warp >= 2 && !*abort) {
+#pragma unroll 1
+            for (int c0 = 0; c0 < t_end; c0 += 16) {
+                uint32_t r[16];
+                tmem_ld_32x32b_x16(tbase + c0, r);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    if (row < args.d_out && c0 + j < t_end)
+                        args.out[static_cast<int64_t>(t0 + c0 + j) * args.d_out + row] =
+                            __float2bfloat16_rn(__uint_as_float(r[j]));
+            }
+        }
+    } else {
+        // rank o sums the tokens o, o + C, ... of the tile; every rank sends it its partials:
+        // red[source rank][token / C][128 rows]
+        cluster_wait();          // every rank has started (its shared memory may be written)
+        const int per = NT / C;
+        if (warp >= 2 && !*abort) {
+#pragma unroll 1
+            for (int c0 = 0; c0 < t_end; c0 += 16) {
+                uint32_t r[16];
+                tmem_ld_32x32b_x16(tbase + c0, r);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const int t = c0 + j;
+                    if (t < t_end)
+                        st_cluster_f32(mapa_shared(smem_u32(red + (rank * per + t / C) * 128 + q * 32 + lane),
+                                                   static_cast<uint32_t>(t % C)),
+                                       __uint_as_float(r[j]));
+                }
+            }
+        }
+        cluster_arrive();
+        cluster_wait();
+        griddep_wait();
+        if (warp >= 2 && !*abort && row < args.d_out) {
+            for (int t = rank; t < t_end; t += C) {
+                float acc = 0.f;
+                for (int c = 0; c < C; ++c) acc += red[(c * per + t / C) * 128 + q * 32 + lane];
+                args.out[static_cast<int64_t>(t0 + t) * args.d_out + row] = __float2bfloat16_rn(acc);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, L::kTmem);
+    }
+}
+
+}  // namespace qlora

@@ -20,6 +20,9 @@
 #include "fp8.cuh"
 #include "qgemv.cuh"
 #include "dora.cuh"
+#include "mxfp4.cuh"
+#include "act8.cuh"
+#include "mx_gemm.cuh"
 
 using namespace qlora;
 
@@ -982,6 +985,8 @@ qlora_status bwd_bf16(const qlora_nf4* w, const void* X, const void* dH, int64_t
     return QLORA_OK;
 }
 
+size_t mx_workspace_bytes(int op, qlora_dtype dtype, int64_t T, int64_t d_out, int64_t d_in, int32_t r);
+
 }  // namespace
 
 // ======================================================================= C ABI
@@ -1022,6 +1027,8 @@ qlora_status qlora_nf4_levels(float* out) {
 
 size_t qlora_workspace_bytes(int op, qlora_dtype dtype, int64_t T, int64_t d_out, int64_t d_in,
                              int32_t r_total) {
+    if (op >= QLORA_OP_FWD_MXFP4 && op <= QLORA_OP_BWD_ACT8)
+        return mx_workspace_bytes(op, dtype, T, d_out, d_in, r_total);
     if (op < QLORA_OP_FWD || op > QLORA_OP_DORA_BWD) return 0;
     if ((op == QLORA_OP_FWD_MULTI || op == QLORA_OP_DORA_FWD || op == QLORA_OP_FWD_FP8 ||
          op == QLORA_OP_FP8_QUANT || op == QLORA_OP_BWD_FP8 || op == QLORA_OP_DORA_BWD) &&
@@ -1725,3 +1732,5 @@ qlora_status qlora_set_gemm_events(cudaEvent_t start, cudaEvent_t stop) {
 }
 
 }  // extern "C"
+
+#include "mx_api.cuh"
