@@ -579,49 +579,63 @@ def qlora_linear_fwd_multi(w: NF4Weight, X, adapter_id, table: AdapterTable, H=N
 # given back on return is only reused behind the call's kernels).
 
 def _need(name, t, dtype, shape, dev):
-    if t.dtype != dtype:
+    if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+        return
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _need_cuda(name, t):
-    if t.device.type != "cuda":
+    dev = t.device
+    if dev.type != "cuda":
         raise ValueError(f"{name} must be a CUDA tensor")
-    return t.device
+    return dev
+
+
+_HERE = contextlib.nullcontext()
 
 
 def _run_on(dev, stream):
-    torch = _torch()
+    """Context in which a call on tensors of `dev` runs and allocates."""
+    cuda = _torch().cuda
     if stream is not None:
         if stream.device != dev:
             raise ValueError(f"stream is on {stream.device}, the tensors are on {dev}")
-        return torch.cuda.stream(stream)
-    if torch.cuda.current_device() == dev.index:
-        return contextlib.nullcontext()
-    return torch.cuda.device(dev)
+        return cuda.stream(stream)
+    return _HERE if cuda.current_device() == dev.index else cuda.device(dev)
+
+
+def _raw_stream(dev, stream):
+    """Stream handle; of the device's current stream without building a Stream object (3 us)."""
+    return stream.cuda_stream if stream is not None else _torch()._C._cuda_getCurrentRawStream(dev.index)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _need_ws(op, T, d_out, d_in, r, dev, ws):
-    torch = _torch()
-    need = workspace_bytes(op, BF16, T, d_out, d_in, r)
-    if need == 0:
-        raise ValueError(f"unsupported shape: T={T}, d_out={d_out}, d_in={d_in}, r={r} "
-                         "(d_in % 64 == 0, 1 <= r <= 128)")
     if ws is None:
+        need = workspace_bytes(op, BF16, T, d_out, d_in, r)
+        if need == 0:
+            raise ValueError(f"unsupported shape: T={T}, d_out={d_out}, d_in={d_in}, r={r} "
+                             "(d_in % 64 == 0, 1 <= r <= 128)")
+        torch = _torch()
         return torch.empty(need, dtype=torch.uint8, device=dev)
-    if ws.device != dev or not ws.is_contiguous() or ws.numel() * ws.element_size() < need:
-        raise ValueError(f"ws must be a contiguous buffer of at least {need} bytes on {dev}")
-    return ws
+    if ws.device != dev or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous buffer on {dev}")
+    return ws           # its size is checked by the library
 
 
-@dataclass
+@dataclass(frozen=True)
 class MXFP4Weight:
-    """Device buffers of an MXFP4 matrix: packed E2M1 codes and the tiled E8M0 scales."""
+    """Device buffers of an MXFP4 matrix: packed E2M1 codes and the tiled E8M0 scales (checked when
+    the handle is made)."""
     codes: object      # uint8 [d_out, d_in/2]
     scales: object     # uint8 [512 * ceil(d_out/128) * ceil(d_in/128)]
     d_out: int
@@ -630,32 +644,32 @@ class MXFP4Weight:
     def _c(self):
         return _MXFP4(self.codes.data_ptr(), self.scales.data_ptr(), self.d_out, self.d_in)
 
-    def _check(self):
+    def __post_init__(self):
         torch = _torch()
         dev = _need_cuda("codes", self.codes)
+        mxfp4_sizes(self.d_out, self.d_in)
         _need("codes", self.codes, torch.uint8, (self.d_out, self.d_in // 2), dev)
         _need("scales", self.scales, torch.uint8, (512 * -(-self.d_out // 128) * -(-self.d_in // 128),), dev)
-        return dev
 
 
-@dataclass
+@dataclass(frozen=True)
 class Act8:
-    """8-bit checkpoint of an activation [T, d_in]: int8 values and one E8M0 scale per 32 of them."""
+    """8-bit checkpoint of an activation [T, d_in]: int8 values and one E8M0 scale per 32 of them
+    (checked when the handle is made)."""
     q: object          # int8 [T, d_in]
     scales: object     # uint8 [T, d_in/32]
 
     def _c(self):
         return _ACT8(self.q.data_ptr(), self.scales.data_ptr())
 
-    def _check(self):
+    def __post_init__(self):
         torch = _torch()
         dev = _need_cuda("q", self.q)
-        if self.q.dim() != 2:
-            raise ValueError("q must be [T, d_in]")
+        if self.q.dim() != 2 or self.q.shape[1] % 64:
+            raise ValueError(f"q must be [T, d_in] with d_in % 64 == 0, got {tuple(self.q.shape)}")
         T, d_in = self.q.shape
         _need("q", self.q, torch.int8, (T, d_in), dev)
         _need("scales", self.scales, torch.uint8, (T, d_in // 32), dev)
-        return dev
 
 
 def mxfp4_sizes(rows, cols):
@@ -680,22 +694,23 @@ def mxfp4_quantize(W, codes=None, scales=None, stream=None) -> MXFP4Weight:
         if scales is None:
             scales = torch.empty(ns, dtype=torch.uint8, device=dev)
         w = MXFP4Weight(codes, scales, rows, cols)
-        w._check()
-        _check("mxfp4_quantize", load().mxfp4_quantize(_ptr(W), dt, rows, cols, _ptr(codes), _ptr(scales),
-                                                       _stream(stream)))
+        if codes.device != dev:
+            raise ValueError(f"codes is on {codes.device}, expected {dev}")
+        _check("mxfp4_quantize", load().mxfp4_quantize(_addr(W), dt, rows, cols, _addr(codes), _addr(scales),
+                                                       _raw_stream(dev, stream)))
     return w
 
 
 def mxfp4_dequantize(w: MXFP4Weight, dtype, out=None, stream=None):
     torch = _torch()
-    dev = w._check()
+    dev = w.codes.device
     dt = _dtype_code(dtype)
     with _run_on(dev, stream):
         if out is None:
             out = torch.empty((w.d_out, w.d_in), dtype=dtype, device=dev)
         else:
             _need("out", out, dtype, (w.d_out, w.d_in), dev)
-        _check("mxfp4_dequantize", load().mxfp4_dequantize(ctypes.byref(w._c()), _ptr(out), dt, _stream(stream)))
+        _check("mxfp4_dequantize", load().mxfp4_dequantize(ctypes.byref(w._c()), _addr(out), dt, _raw_stream(dev, stream)))
     return out
 
 
@@ -705,7 +720,7 @@ def qlora_linear_fwd_mxfp4(w: MXFP4Weight, X, A, B, alpha, H=None, U_save=None, 
     call for the base product.  Returns (H, U_save)."""
     torch = _torch()
     bf = torch.bfloat16
-    dev = w._check()
+    dev = w.codes.device
     T, r = X.shape[0], A.shape[0]
     _need("X", X, bf, (T, w.d_in), dev)
     _need("A", A, bf, (r, w.d_in), dev)
@@ -713,17 +728,17 @@ def qlora_linear_fwd_mxfp4(w: MXFP4Weight, X, A, B, alpha, H=None, U_save=None, 
     with _run_on(dev, stream):
         ws = _need_ws(OP_FWD_MXFP4, T, w.d_out, w.d_in, r, dev, ws)
         if H is None:
-            H = torch.empty((T, w.d_out), dtype=bf, device=dev)
+            H = X.new_empty((T, w.d_out))
         else:
             _need("H", H, bf, (T, w.d_out), dev)
         if U_save is None:
             if save_u:
-                U_save = torch.empty((T, r), dtype=bf, device=dev)
+                U_save = X.new_empty((T, r))
         else:
             _need("U_save", U_save, bf, (T, r), dev)
         _check("qlora_linear_fwd_mxfp4", load().qlora_linear_fwd_mxfp4(
-            ctypes.byref(w._c()), _ptr(X), T, _ptr(A), _ptr(B), r, float(alpha), _ptr(H), _ptr(U_save),
-            _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+            ctypes.byref(w._c()), _addr(X), T, _addr(A), _addr(B), r, float(alpha), _addr(H), _addr(U_save),
+            _addr(ws), ws.nbytes, _raw_stream(dev, stream)))
     return H, U_save
 
 
@@ -742,17 +757,16 @@ def act8_quantize(X, q=None, scales=None, stream=None) -> Act8:
         if scales is None:
             scales = torch.empty((T, d_in // 32), dtype=torch.uint8, device=dev)
         a = Act8(q, scales)
-        a._check()
         _need("q", q, torch.int8, (T, d_in), dev)
-        _check("qlora_act8_quantize", load().qlora_act8_quantize(_ptr(X), dt, T, d_in, _ptr(q), _ptr(scales),
-                                                                 _stream(stream)))
+        _check("qlora_act8_quantize", load().qlora_act8_quantize(_addr(X), dt, T, d_in, _addr(q), _addr(scales),
+                                                                 _raw_stream(dev, stream)))
     return a
 
 
 def act8_dequantize(a: Act8, dtype, out=None, stream=None):
     """The checkpoint's values (exact in bf16 and fp32)."""
     torch = _torch()
-    dev = a._check()
+    dev = a.q.device
     dt = _dtype_code(dtype)
     T, d_in = a.q.shape
     with _run_on(dev, stream):
@@ -760,8 +774,8 @@ def act8_dequantize(a: Act8, dtype, out=None, stream=None):
             out = torch.empty((T, d_in), dtype=dtype, device=dev)
         else:
             _need("out", out, dtype, (T, d_in), dev)
-        _check("qlora_act8_dequantize", load().qlora_act8_dequantize(ctypes.byref(a._c()), T, d_in, _ptr(out), dt,
-                                                                     _stream(stream)))
+        _check("qlora_act8_dequantize", load().qlora_act8_dequantize(ctypes.byref(a._c()), T, d_in, _addr(out), dt,
+                                                                     _raw_stream(dev, stream)))
     return out
 
 
@@ -777,8 +791,6 @@ def _bwd_act(fn, op, w, dev, X, dH, A, B, alpha, U_saved, dX, dA, dB, ws, want_d
     T, r = dH.shape[0], A.shape[0]
     x8 = None
     if isinstance(X, Act8):
-        if X._check() != dev:
-            raise ValueError(f"the checkpoint is on {X.q.device}, expected {dev}")
         _need("X.q", X.q, torch.int8, (T, w.d_in), dev)
         x8 = X._c()
     else:
@@ -793,7 +805,7 @@ def _bwd_act(fn, op, w, dev, X, dH, A, B, alpha, U_saved, dX, dA, dB, ws, want_d
     with _run_on(dev, stream):
         ws = _need_ws(op, T, w.d_out, w.d_in, r, dev, ws)
         if dX is None and want_dx and phase != "grads":
-            dX = torch.empty((T, w.d_in), dtype=bf, device=dev)
+            dX = dH.new_empty((T, w.d_in))
         if phase != "dx":
             if dA is None:
                 dA = torch.empty((r, w.d_in), dtype=f32, device=dev)
@@ -801,10 +813,10 @@ def _bwd_act(fn, op, w, dev, X, dH, A, B, alpha, U_saved, dX, dA, dB, ws, want_d
                 dB = torch.empty((w.d_out, r), dtype=f32, device=dev)
         flags = _BWD_PHASES[phase] | (BWD_ACCUMULATE if accumulate else 0)
         p8 = ctypes.byref(x8) if x8 is not None else None
-        act = (p8,) if op == OP_BWD_ACT8 else (None if x8 is not None else _ptr(X), p8)
+        act = (p8,) if op == OP_BWD_ACT8 else (None if x8 is not None else _addr(X), p8)
         _check(fn, getattr(load(), fn)(
-            ctypes.byref(w._c()), *act, _ptr(dH), T, _ptr(A), _ptr(B), r, float(alpha), _ptr(U_saved), _ptr(dX),
-            _ptr(dA), _ptr(dB), _ptr(ws), ws.numel() * ws.element_size(), flags, _stream(stream)))
+            ctypes.byref(w._c()), *act, _addr(dH), T, _addr(A), _addr(B), r, float(alpha), _addr(U_saved), _addr(dX),
+            _addr(dA), _addr(dB), _addr(ws), ws.nbytes, flags, _raw_stream(dev, stream)))
     return dX, dA, dB
 
 
@@ -812,7 +824,7 @@ def qlora_linear_bwd_mxfp4(w: MXFP4Weight, X, dH, A, B, alpha, U_saved=None, dX=
                            ws=None, stream=None, want_dx=True, accumulate=False, phase="all"):
     """Backward of qlora_linear_fwd_mxfp4 from X, a bf16 tensor or the Act8 checkpoint of one.
     Returns (dX, dA, dB); dA, dB fp32.  accumulate and phase as in qlora_linear_bwd."""
-    return _bwd_act("qlora_linear_bwd_mxfp4", OP_BWD_MXFP4, w, w._check(), X, dH, A, B, alpha, U_saved, dX, dA, dB,
+    return _bwd_act("qlora_linear_bwd_mxfp4", OP_BWD_MXFP4, w, w.codes.device, X, dH, A, B, alpha, U_saved, dX, dA, dB,
                     ws, want_dx, accumulate, phase, stream)
 
 

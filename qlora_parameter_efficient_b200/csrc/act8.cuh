@@ -11,13 +11,11 @@
 // the stored values exactly.  A block with a NaN or an infinity gets e = 255 and decodes to NaN.
 // q [T, d_in] int8 and scales [T, d_in / 32], both row-major.
 //
-// Adapter gradients from it (k_act_gemm): the int8 tile is brought to shared memory by TMA and
-// turned into the swizzled bf16 operand there, so no bf16 copy of X is ever in HBM:
+// The adapter products of a backward that reads it (k_act_gemm): the int8 tile is brought to shared
+// memory by TMA and turned into the swizzled bf16 operand there, so no bf16 copy of X is ever in HBM:
 //   dA^T[d_in, r] = X~^T (s G)       A operand MN-major (the tokens are K)
 //   U[T, r]       = X~ A^T           A operand K-major
-// The other operand comes as one or two bf16 matrices hi + lo (a value's bf16 rounding and the
-// rounding of what is left: 16 significant bits), accumulated in the same fp32 tile, so that
-// rounding G (or U) to the tensor cores' type costs 2^-18 of a gradient and not 2^-9.
+// and with bf16 operands G = dH B, dB = s dH^T U, and both of the above from a bf16 X.
 #pragma once
 
 #include "common.cuh"
@@ -105,20 +103,12 @@ __global__ void __launch_bounds__(256) k_act8_dequant(const int8_t* __restrict__
 
 // ------------------------------------------------------------------ adapter products
 
-// How the A operand of k_act_gemm is stored.
-enum : int {
-    kActBf16Mn = 0,   // bf16 [K, M] (tokens are K): TMA straight into the MN-major operand
-    kActInt8Mn = 1,   // int8 [K, M] with scales [K, M / 32]: decoded into the MN-major operand
-    kActInt8K = 2     // int8 [M, K] with scales [M, K / 32]: decoded into the K-major operand
-};
-
 struct ActGemmArgs {
     int M, N;                // output rows (channels or tokens) and valid columns (the rank)
     int64_t K;               // contraction length
     int k_steps;             // ceil(K / 64)
-    int split;               // split-K over grid.z
-    int nb;                  // B matrices: 1, or 2 for hi + lo
-    const uint8_t* scales;   // E8M0 bytes of the int8 operand
+    int split;               // split-K over grid.y
+    const uint8_t* scales;   // E8M0 bytes of the int8 operand, row-major
     int64_t ld_scales;       // blocks per stored row
     float* part;             // fp32 partials: [split][M][ldp], or transposed [split][N][M]
     int64_t ldp;
@@ -127,41 +117,53 @@ struct ActGemmArgs {
     uint64_t wait_ns;
 };
 
-// RPT: the padded rank (B tile columns), 64 or 128.
-template <int MODE, int RPT>
+// RPT: the padded rank, 64 or 128 (B tile rows); NB: bf16 matrices whose sum B is, 1 or 3.
+template <bool INT8, int RPT, int NB>
 struct ActGemmSmem {
     static constexpr int kA = 128 * 64 * 2;                     // bf16 operand tile
-    static constexpr int kRaw = MODE == kActBf16Mn ? 0 : 128 * 64;
+    static constexpr int kRaw = INT8 ? 128 * 64 : 0;
     static constexpr int kB = RPT * 64 * 2;                     // one B matrix's tile
-    static constexpr int kStage = kA + kRaw + 2 * kB;
-    static constexpr int kStages = 4;
-    static constexpr int kTotal = 1024 + kStages * kStage + 256;
-    static_assert(kTotal <= 232448, "shared memory budget");
+    static constexpr int kStage = kA + kRaw + NB * kB;
+    static constexpr int kStages = 221184 / kStage < 6 ? 221184 / kStage : 6;
+    static constexpr int kTotal = 1024 + kStages * kStage + 512;
+    // K steps of 64 per accumulator segment (see the kernel)
+    static constexpr int kSeg = NB == 1 ? 4 : 2;
+    static_assert(kTotal <= 232448 && kStages >= 3, "shared memory budget");
 };
 
-// D[M, RPT] = sum over K of A[M, K] (B0 + B1)[RPT, K], fp32 split-K partials.  Warp 0: TMA; warp 1:
-// MMA; warps 2..9: int8 decode (one 32-element block per thread and stage), then the epilogue.
-// B is MN-major ([K, rank] rows) for the Mn modes and K-major ([rank, K]) for kActInt8K.
-// Memory-bound: per K step of 64 a tile reads 8 KB of int8 and 2 to 4 B tiles that stay in L2.
-template <int MODE, int RPT>
+// D[M, N] = sum over K of A[M, K] B[N, K], B the sum of NB bf16 matrices; fp32 split-K partials.
+//   INT8   A is int8 with E8M0 scales, decoded to bf16 in shared memory (else bf16)
+//   AMN    A is stored [K, M] (tokens are K) and consumed MN-major, else [M, K]
+//   BMN    B is stored [K, N], else [N, K]; B's tensor map is three-dimensional, matrix outermost
+// Warp 0: TMA; warp 1: MMA; warps 2..9: int8 decode (one 32-element block per thread and stage),
+// accumulator drains, partials.
+//
+// Precision: the results are fp32 gradients.  (1) A value that was computed here (s G, a recomputed U)
+// is given to the bf16 tensor cores as the three bf16 numbers that make up its 24 bits, so nothing is
+// rounded off it.  (2) The tensor core's running fp32 sum is truncated at every MMA -- a bias that
+// grows with the chain: 9e-6 of a gradient over 8192 tokens.  So the chain is cut into segments of
+// 16 or 24 MMAs, whose sums warps 2..9 add up in registers, rounding to nearest, from two
+// accumulator tiles in turn.
+// Bound by memory: a K step of 64 reads 8 KB of int8 (or 16 KB of bf16) from HBM and the B tiles from
+// L2; N is the rank rounded up to 16, so that the MMAs stay below that.
+template <bool INT8, bool AMN, bool BMN, int RPT, int NB>
 __global__ void __launch_bounds__(320, 1)
-    k_act_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB0,
-               const __grid_constant__ CUtensorMap tmB1, const ActGemmArgs args) {
-    using L = ActGemmSmem<MODE, RPT>;
-    constexpr int S = L::kStages;
-    constexpr bool kMn = MODE != kActInt8K;
-    constexpr bool kDecode = MODE != kActBf16Mn;
+    k_act_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+               const ActGemmArgs args) {
+    using L = ActGemmSmem<INT8, RPT, NB>;
+    constexpr int S = L::kStages, kSeg = L::kSeg;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
     uint8_t* sA = smem;
     uint8_t* sB = sA + S * L::kA;
-    uint8_t* sR = sB + S * 2 * L::kB;
+    uint8_t* sR = sB + S * NB * L::kB;
     uint64_t* full = reinterpret_cast<uint64_t*>(sR + S * L::kRaw);
     uint64_t* empty = full + S;
     uint64_t* decoded = empty + S;
-    uint64_t* accf = decoded + S;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(accf + 1);
+    uint64_t* accf = decoded + S;         // [2] segment complete
+    uint64_t* acc_free = accf + 2;        // [2] segment drained (8 warp arrivals)
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_free + 2);
     volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -170,6 +172,8 @@ __global__ void __launch_bounds__(320, 1)
     const int per = (args.k_steps + args.split - 1) / args.split;
     const int k_begin = z * per;
     const int n_iters = max(0, min(args.k_steps, k_begin + per) - k_begin);
+    const int n_seg = (n_iters + kSeg - 1) / kSeg;
+    const int n_mma = (args.N + 15) & ~15;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
@@ -177,24 +181,31 @@ __global__ void __launch_bounds__(320, 1)
             mbar_init(&empty[s], 1);
             mbar_init(&decoded[s], 8);
         }
-        mbar_init(accf, 1);
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&accf[b], 1);
+            mbar_init(&acc_free[b], 8);
+        }
         *abort = 0;
         fence_mbar_init();
     }
     if (warp == 0 && lane == 0) {
         tma_prefetch_desc(&tmA);
-        tma_prefetch_desc(&tmB0);
-        if (args.nb > 1) tma_prefetch_desc(&tmB1);
+        tma_prefetch_desc(&tmB);
     }
     if (warp == 1) {
-        tmem_alloc(tmem_slot, RPT);
+        tmem_alloc(tmem_slot, 2 * RPT);
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem_acc = *tmem_slot;
+    const uint32_t tmem = *tmem_slot;
     griddep_enter();
+
+    auto fail = [&]() {
+        set_error(args.err, kErrTimeout);
+        *abort = 1;
+    };
 
     if (warp == 0) {
         if (lane == 0) {
@@ -202,28 +213,26 @@ __global__ void __launch_bounds__(320, 1)
             for (int it = 0; it < n_iters; ++it) {
                 const int s = it % S;
                 if (!mbar_wait(&empty[s], ((it / S) & 1) ^ 1, abort, args.wait_ns)) {
-                    set_error(args.err, kErrTimeout);
-                    *abort = 1;
+                    fail();
                     break;
                 }
                 const int kx = (k_begin + it) * 64;
-                mbar_arrive_expect_tx(&full[s], (kDecode ? L::kRaw : L::kA) + args.nb * L::kB);
-                if (MODE == kActBf16Mn) {
-                    tma_load_2d(sA + s * L::kA, &tmA, &full[s], m0, kx);
-                    tma_load_2d(sA + s * L::kA + 8192, &tmA, &full[s], m0 + 64, kx);
-                } else if (MODE == kActInt8Mn) {
-                    tma_load_2d(sR + s * L::kRaw, &tmA, &full[s], m0, kx);
+                mbar_arrive_expect_tx(&full[s], (INT8 ? L::kRaw : L::kA) + NB * L::kB);
+                uint8_t* a = INT8 ? sR + s * L::kRaw : sA + s * L::kA;
+                if (AMN) {
+                    tma_load_2d(a, &tmA, &full[s], m0, kx);
+                    if (!INT8) tma_load_2d(a + 8192, &tmA, &full[s], m0 + 64, kx);
                 } else {
-                    tma_load_2d(sR + s * L::kRaw, &tmA, &full[s], kx, m0);
+                    tma_load_2d(a, &tmA, &full[s], kx, m0);
                 }
-                for (int b = 0; b < args.nb; ++b) {
-                    const CUtensorMap* mb = b ? &tmB1 : &tmB0;
-                    uint8_t* dst = sB + (s * 2 + b) * L::kB;
-                    if (kMn) {
 #pragma unroll
-                        for (int c = 0; c < RPT / 64; ++c) tma_load_2d(dst + c * 8192, mb, &full[s], c * 64, kx);
+                for (int b = 0; b < NB; ++b) {
+                    uint8_t* dst = sB + (s * NB + b) * L::kB;
+                    if (BMN) {
+#pragma unroll
+                        for (int c = 0; c < RPT / 64; ++c) tma_load_3d(dst + c * 8192, &tmB, &full[s], c * 64, kx, b);
                     } else {
-                        tma_load_2d(dst, mb, &full[s], kx, 0);
+                        tma_load_3d(dst, &tmB, &full[s], kx, 0, b);
                     }
                 }
                 issued = it + 1;
@@ -234,132 +243,148 @@ __global__ void __launch_bounds__(320, 1)
         }
     } else if (warp == 1) {
         if (lane == 0) {
-            const uint32_t idesc = make_idesc_bf16(128, RPT, kMn, kMn);
+            const uint32_t idesc = make_idesc_bf16(128, n_mma, AMN, BMN);
             for (int it = 0; it < n_iters; ++it) {
-                const int s = it % S;
+                const int s = it % S, seg = it / kSeg;
                 const uint32_t ph = (it / S) & 1;
-                bool ok = mbar_wait(&full[s], ph, abort, args.wait_ns);
-                if (ok && kDecode) ok = mbar_wait(&decoded[s], ph, abort, args.wait_ns);
+                bool ok = true;
+                if (it % kSeg == 0 && seg >= 2)
+                    ok = mbar_wait(&acc_free[seg & 1], ((seg >> 1) & 1) ^ 1, abort, args.wait_ns);
+                if (ok) ok = mbar_wait(&full[s], ph, abort, args.wait_ns);
+                if (ok && INT8) ok = mbar_wait(&decoded[s], ph, abort, args.wait_ns);
                 if (!ok) {
-                    set_error(args.err, kErrTimeout);
-                    *abort = 1;
+                    fail();
                     break;
                 }
                 tc_fence_after();
+                const uint32_t d = tmem + static_cast<uint32_t>((seg & 1) * RPT);
                 const uint32_t a = smem_u32(sA + s * L::kA);
-                for (int b = 0; b < args.nb; ++b) {
-                    const uint32_t bb = smem_u32(sB + (s * 2 + b) * L::kB);
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    const uint32_t bb = smem_u32(sB + (s * NB + b) * L::kB);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        umma_bf16_ss(tmem_acc,
-                                     kMn ? make_sw128_desc(a + k * 2048, 8192, 1024) : make_sw128_desc(a + k * 32, 16, 1024),
-                                     kMn ? make_sw128_desc(bb + k * 2048, 8192, 1024) : make_sw128_desc(bb + k * 32, 16, 1024),
-                                     idesc, (it > 0 || b > 0 || k > 0) ? 1u : 0u);
+                        umma_bf16_ss(d, AMN ? make_sw128_desc(a + k * 2048, 8192, 1024) : make_sw128_desc(a + k * 32, 16, 1024),
+                                     BMN ? make_sw128_desc(bb + k * 2048, 8192, 1024) : make_sw128_desc(bb + k * 32, 16, 1024),
+                                     idesc, (it % kSeg > 0 || b > 0 || k > 0) ? 1u : 0u);
                 }
                 umma_commit(&empty[s]);
+                if (it % kSeg == kSeg - 1 || it == n_iters - 1) umma_commit(&accf[seg & 1]);
             }
-            umma_commit(accf);
         }
     } else {
-        if (kDecode) {
-            const int td = threadIdx.x - 64;                     // 0..255: the block of this thread
-            const int row = kMn ? td >> 2 : td >> 1;              // row of the int8 tile
-            const int b = kMn ? td & 3 : td & 1;                  // block within the row
-            auto scale_at = [&](int it) -> uint32_t {
-                const int64_t kx = static_cast<int64_t>(k_begin + it) * 64;
-                const int64_t srow = kMn ? kx + row : m0 + row;
-                const int64_t blk = (kMn ? m0 / 32 : kx / 32) + b;
-                const int64_t rows = kMn ? args.K : args.M;
-                if (it >= n_iters || srow >= rows || blk >= args.ld_scales) return 0u;
-                return __ldg(args.scales + srow * args.ld_scales + blk);
-            };
-            uint32_t e_nxt = scale_at(0);
-            for (int it = 0; it < n_iters; ++it) {
-                const int s = it % S;
-                const uint32_t e = e_nxt;
-                e_nxt = scale_at(it + 1);
-                if (!mbar_wait(&full[s], (it / S) & 1, abort, args.wait_ns)) {
-                    set_error(args.err, kErrTimeout);
-                    *abort = 1;
-                    break;
+        const int q = warp & 3, half = (warp - 2) >> 2;      // lane quarter, half of the columns
+        constexpr int kHalf = RPT / 2;
+        float acc[kHalf];
+#pragma unroll
+        for (int j = 0; j < kHalf; ++j) acc[j] = 0.f;
+        bool ok = true;
+        auto drain = [&](int seg) {
+            ok = mbar_wait_warp(&accf[seg & 1], (seg >> 1) & 1, abort, args.wait_ns);
+            if (!ok) return;
+            tc_fence_after();
+            const uint32_t t = tmem + (static_cast<uint32_t>(q * 32) << 16) + (seg & 1) * RPT + half * kHalf;
+#pragma unroll
+            for (int c = 0; c < kHalf; c += 32)
+                if (half * kHalf + c < args.N) {
+                    uint32_t r[32];
+                    tmem_ld_32x32b_x32(t + c, r);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) acc[c + j] += __uint_as_float(r[j]);
                 }
-                // (elements outside the matrix were filled with 0 by the copy)
-                const uint4* src = reinterpret_cast<const uint4*>(sR + s * L::kRaw + td * 32);
-                const uint4 v0 = src[0], v1 = src[1];
-                const float st = act8_step(e);
-                uint8_t* dst = sA + s * L::kA + (kMn ? (b >> 1) * 8192 + row * 128 : row * 128);
-                const int c0 = kMn ? (b & 1) * 4 : b * 4, sw = row & 7;
-                *reinterpret_cast<uint4*>(dst + (((c0 + 0) ^ sw) << 4)) = act8_decode8(v0.x, v0.y, st);
-                *reinterpret_cast<uint4*>(dst + (((c0 + 1) ^ sw) << 4)) = act8_decode8(v0.z, v0.w, st);
-                *reinterpret_cast<uint4*>(dst + (((c0 + 2) ^ sw) << 4)) = act8_decode8(v1.x, v1.y, st);
-                *reinterpret_cast<uint4*>(dst + (((c0 + 3) ^ sw) << 4)) = act8_decode8(v1.z, v1.w, st);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&decoded[s]);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&acc_free[seg & 1]);
+        };
+        const int td = threadIdx.x - 64;                      // 0..255: the int8 block of this thread
+        const int row = AMN ? td >> 2 : td >> 1;              // row of the int8 tile
+        const int blk_in = AMN ? td & 3 : td & 1;             // block within the row
+        auto scale_at = [&](int it) -> uint32_t {
+            const int64_t kx = static_cast<int64_t>(k_begin + it) * 64;
+            const int64_t srow = AMN ? kx + row : m0 + row;
+            const int64_t blk = (AMN ? m0 / 32 : kx / 32) + blk_in;
+            const int64_t rows = AMN ? args.K : args.M;
+            if (it >= n_iters || srow >= rows || blk >= args.ld_scales) return 0u;
+            return __ldg(args.scales + srow * args.ld_scales + blk);
+        };
+        uint32_t e_nxt = INT8 ? scale_at(0) : 0u;
+        for (int seg = 0; ok && seg < n_seg; ++seg) {
+            if (INT8) {
+                for (int it = seg * kSeg; it < min(n_iters, (seg + 1) * kSeg); ++it) {
+                    const int s = it % S;
+                    const uint32_t e = e_nxt;
+                    e_nxt = scale_at(it + 1);
+                    ok = mbar_wait_warp(&full[s], (it / S) & 1, abort, args.wait_ns);
+                    if (!ok) break;
+                    // (elements outside the matrix were filled with 0 by the copy)
+                    const uint4* src = reinterpret_cast<const uint4*>(sR + s * L::kRaw + td * 32);
+                    const uint4 v0 = src[0], v1 = src[1];
+                    const float st = act8_step(e);
+                    uint8_t* dst = sA + s * L::kA + (AMN ? (blk_in >> 1) * 8192 + row * 128 : row * 128);
+                    const int c0 = AMN ? (blk_in & 1) * 4 : blk_in * 4, sw = row & 7;
+                    *reinterpret_cast<uint4*>(dst + (((c0 + 0) ^ sw) << 4)) = act8_decode8(v0.x, v0.y, st);
+                    *reinterpret_cast<uint4*>(dst + (((c0 + 1) ^ sw) << 4)) = act8_decode8(v0.z, v0.w, st);
+                    *reinterpret_cast<uint4*>(dst + (((c0 + 2) ^ sw) << 4)) = act8_decode8(v1.x, v1.y, st);
+                    *reinterpret_cast<uint4*>(dst + (((c0 + 3) ^ sw) << 4)) = act8_decode8(v1.z, v1.w, st);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&decoded[s]);
+                }
             }
+            // one segment behind the decode, so that the MMAs of this one run meanwhile
+            if (ok && seg >= 1) drain(seg - 1);
         }
-        if (!mbar_wait(accf, 0, nullptr, args.wait_ns)) {
-            set_error(args.err, kErrTimeout);
-            *abort = 1;
-        }
-        tc_fence_after();
-        if (!*abort) {
-            const int q = warp & 3, half = (warp - 2) >> 2;
-            const int64_t grow = static_cast<int64_t>(m0) + q * 32 + lane;
-            float* out = args.part + static_cast<int64_t>(z) * (args.transposed ? args.N : args.M) *
-                                         (args.transposed ? static_cast<int64_t>(args.M) : args.ldp);
-#pragma unroll 1
-            for (int c0 = half * (RPT / 2); c0 < (half + 1) * (RPT / 2) && c0 < args.N; c0 += 32) {
-                uint32_t r[32];
-                tmem_ld_32x32b_x32(tmem_acc + (static_cast<uint32_t>(q * 32) << 16) + c0, r);
-                tmem_ld_wait();
-                if (grow < args.M) {
-                    if (args.transposed) {
+        if (ok && n_seg > 0) drain(n_seg - 1);
+        if (!ok) fail();
+        const int64_t grow = static_cast<int64_t>(m0) + q * 32 + lane;
+        if (ok && grow < args.M) {
+            const int c0 = half * kHalf;
+            if (args.transposed) {
+                float* out = args.part + static_cast<int64_t>(z) * args.N * args.M + grow;
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (c0 + j < args.N) out[static_cast<int64_t>(c0 + j) * args.M + grow] = __uint_as_float(r[j]);
-                    } else {
-                        // rows of ldp floats, ldp a multiple of 4: 16-byte stores up to the rank
-                        float* o = out + grow * args.ldp + c0;
+                for (int j = 0; j < kHalf; ++j)
+                    if (c0 + j < args.N) out[static_cast<int64_t>(c0 + j) * args.M] = acc[j];
+            } else {
+                // rows of ldp floats (a multiple of 4): 16-byte stores up to the rank
+                float* out = args.part + (static_cast<int64_t>(z) * args.M + grow) * args.ldp + c0;
 #pragma unroll
-                        for (int g = 0; g < 8; ++g)
-                            if (c0 + 4 * g < args.N)
-                                *reinterpret_cast<uint4*>(o + 4 * g) =
-                                    make_uint4(r[4 * g], r[4 * g + 1], r[4 * g + 2], r[4 * g + 3]);
-                    }
-                }
+                for (int j = 0; j < kHalf; j += 4)
+                    if (c0 + j < args.N)
+                        *reinterpret_cast<float4*>(out + j) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
             }
         }
     }
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem_acc, RPT);
+        tmem_dealloc(tmem, 2 * RPT);
     }
 }
 
-// Sum split-K partials P[z][t][j] (row stride ldp) in z order and write v = scale sum as the bf16 pair
-// hi = bf16(v), lo = bf16(v - hi), each [T, ld] (columns j >= r are zero).
-__global__ void __launch_bounds__(256) k_finalize_pair(const float* __restrict__ P, int split, int64_t T, int r,
-                                                       int ldp, float scale, int ld,
-                                                       __nv_bfloat16* __restrict__ hi,
-                                                       __nv_bfloat16* __restrict__ lo) {
+// Sum split-K partials P[z][t][j] (row stride ld) in z order; v = scale sum is written as the three bf16
+// numbers out[0] + out[1] + out[2] = v (8 significant bits each), matrices [T, ld], columns
+// j >= r zero.  An infinite or NaN v is carried by the first alone (inf - inf would make it NaN).
+__global__ void __launch_bounds__(256) k_finalize_triple(const float* __restrict__ P, int split, int64_t T, int r,
+                                                         int ld, float scale, __nv_bfloat16* __restrict__ out) {
     griddep_enter();
-    const int64_t n = T * ld, stride = T * ldp;
+    const int64_t n = T * ld;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
          i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-        const int64_t t = i / ld;
-        const int j = static_cast<int>(i - t * ld);
+        const int j = static_cast<int>(i % ld);
         float acc = 0.f;
         if (j < r)
-            for (int z = 0; z < split; ++z) acc += P[z * stride + t * ldp + j];
-        const float v = scale * acc;
-        const __nv_bfloat16 h = __float2bfloat16_rn(v);
-        const float rest = v - __bfloat162float(h);
-        hi[i] = h;
-        // an infinite or NaN v is carried by hi alone (inf - inf would turn it into NaN)
-        lo[i] = __float2bfloat16_rn(fabsf(rest) < __int_as_float(0x7F800000) ? rest : 0.f);
+            for (int z = 0; z < split; ++z) acc += P[z * n + i];
+        float v = scale * acc;
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            const __nv_bfloat16 h = __float2bfloat16_rn(v);
+            out[k * n + i] = h;
+            const float rest = v - __bfloat162float(h);
+            v = fabsf(rest) < __int_as_float(0x7F800000) ? rest : 0.f;
+        }
     }
 }
 

@@ -65,7 +65,7 @@ MxFwdPlan mx_fwd_plan(int64_t T, int64_t d_out, int64_t d_in, int r) {
 // The backward of an MXFP4 or NF4 base from a bf16 activation or an 8-bit checkpoint.
 struct MxBwdPlan {
     int RP = 0, split_u = 1, split_g = 1, split_da = 1, split_db = 1;
-    size_t b_pad = 0, dh_pad = 0, u_hi = 0, u_lo = 0, g_hi = 0, g_lo = 0, part = 0, g2 = 0, total = 0;
+    size_t b_pad = 0, dh_pad = 0, u3 = 0, g3 = 0, part = 0, g2 = 0, total = 0;
 };
 // k_act_gemm runs one CTA per SM: one wave of them.
 int act_split(int64_t tiles, int64_t k_steps) {
@@ -85,12 +85,10 @@ MxBwdPlan mx_bwd_plan(int64_t T, int64_t d_out, int64_t d_in, int r) {
     const size_t rp = static_cast<size_t>(p.RP), row = static_cast<size_t>(T) * rp;
     if (r % 8) p.b_pad = take(static_cast<size_t>(d_out) * rp * 2);
     if (d_out % 8) p.dh_pad = take(static_cast<size_t>(T) * ((d_out + 7) / 8 * 8) * 2);
-    p.u_hi = take(row * 2);
-    p.u_lo = take(row * 2);
-    p.g_hi = take(row * 2);
-    p.g_lo = take(row * 2);
-    p.split_u = choose_split(cdiv(T, kBM), cdiv(d_in, kBK));
-    p.split_g = choose_split(cdiv(T, kBM), cdiv(d_out, kBK));
+    p.u3 = take(3 * row * 2);      // U and s G as three bf16 matrices each
+    p.g3 = take(3 * row * 2);
+    p.split_u = act_split(cdiv(T, 128), cdiv(d_in, 64));
+    p.split_g = act_split(cdiv(T, 128), cdiv(d_out, 64));
     p.split_da = act_split(cdiv(d_in, 128), cdiv(T, 64));
     p.split_db = act_split(cdiv(d_out, 128), cdiv(T, 64));
     size_t part = static_cast<size_t>(std::max(p.split_u, p.split_g)) * row * 4;
@@ -153,28 +151,37 @@ qlora_status launch_mx_stream(const CUtensorMap& tw, const CUtensorMap& tx, cons
     return QLORA_OK;
 }
 
-template <int MODE, int RPT>
-qlora_status launch_act_gemm(const CUtensorMap& ta, const CUtensorMap& tb0, const CUtensorMap& tb1,
-                             const ActGemmArgs& g, cudaStream_t st) {
-    using L = ActGemmSmem<MODE, RPT>;
+// bf16 [nb][rows, cols] with row stride ld and matrix stride rows * ld, 128-byte swizzle, boxes of 64
+// columns x box_rows; rows and columns outside a matrix are filled with 0 (cols need not be whole
+// 16-byte units, ld does).
+qlora_status tmap_bf16_3d(CUtensorMap* m, const void* base, int nb, int64_t rows, int64_t cols, int64_t ld,
+                          uint32_t box_rows) {
+    QL_TRY(get_encoder());
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(nb)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld * 2), static_cast<cuuint64_t>(rows * ld * 2)};
+    cuuint32_t box[3] = {64, box_rows, 1};
+    cuuint32_t es[3] = {1, 1, 1};
+    CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? QLORA_OK : QLORA_ERR_CUDA;
+}
+
+template <bool INT8, bool AMN, bool BMN, int RPT, int NB>
+qlora_status launch_act_gemm(const CUtensorMap& ta, const CUtensorMap& tb, const ActGemmArgs& g, cudaStream_t st) {
+    using L = ActGemmSmem<INT8, RPT, NB>;
+    auto kern = k_act_gemm<INT8, AMN, BMN, RPT, NB>;
     static std::atomic<uint64_t> configured{0};
-    QL_TRY(allow_smem(k_act_gemm<MODE, RPT>, L::kTotal, configured));
+    QL_TRY(allow_smem(kern, L::kTotal, configured));
     const dim3 grid(static_cast<unsigned>(cdiv(g.M, 128)), static_cast<unsigned>(g.split));
-    if (launch_pdl(k_act_gemm<MODE, RPT>, grid, dim3(320), L::kTotal, st, ta, tb0, tb1, g) != cudaSuccess)
-        return QLORA_ERR_CUDA;
+    if (launch_pdl(kern, grid, dim3(320), L::kTotal, st, ta, tb, g) != cudaSuccess) return QLORA_ERR_CUDA;
     QL_LAUNCH_CHECK();
     return QLORA_OK;
 }
-template <int MODE>
-qlora_status act_gemm(int RP, const CUtensorMap& ta, const CUtensorMap& tb0, const CUtensorMap& tb1,
-                      const ActGemmArgs& g, cudaStream_t st) {
-    return RP == 64 ? launch_act_gemm<MODE, 64>(ta, tb0, tb1, g, st) : launch_act_gemm<MODE, 128>(ta, tb0, tb1, g, st);
-}
-
-// bf16 [rows, cols] with row stride ld, 128-byte swizzle, 64 columns x box_rows; columns past
-// `cols` are filled with 0 (cols need not be whole 16-byte units, ld does).
-qlora_status tmap_rank(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld, uint32_t box_rows) {
-    return tmap_bf16(m, base, rows, cols, ld, box_rows);
+template <bool INT8, bool AMN, bool BMN, int NB>
+qlora_status act_gemm(int RP, const CUtensorMap& ta, const CUtensorMap& tb, const ActGemmArgs& g, cudaStream_t st) {
+    return RP == 64 ? launch_act_gemm<INT8, AMN, BMN, 64, NB>(ta, tb, g, st)
+                    : launch_act_gemm<INT8, AMN, BMN, 128, NB>(ta, tb, g, st);
 }
 
 // dX = dH W4 + (sG) A: the fused decode GEMM with its decoders reading MXFP4.
@@ -272,8 +279,8 @@ qlora_status mx_fwd(const qlora_mxfp4* w, const void* X, int64_t T, const void* 
     const uint32_t nt = route == kMxDecode ? 16 : (route == kMxStream64 ? 64 : 128);
     QL_TRY(tmap_u8_sw128(&tw, w->codes, d_out, d_in / 2, d_in / 2, 128));
     QL_TRY(tmap_u8_sw128(&tx, codes, T, d_in / 2, d_in / 2, nt));
-    QL_TRY(tmap_rank(&tb, b_src, d_out, r, b_ld, 128));
-    QL_TRY(tmap_rank(&tu, us, T, r, RP, nt));
+    QL_TRY(tmap_bf16(&tb, b_src, d_out, r, b_ld, 128));
+    QL_TRY(tmap_bf16(&tu, us, T, r, RP, nt));
     MxStreamArgs g{};
     g.T = static_cast<int>(T);
     g.d_out = static_cast<int>(d_out);
@@ -307,18 +314,16 @@ qlora_status mx_bwd(MxBase base, const void* X, const qlora_act8* X8, const void
     const MxBwdPlan p = mx_bwd_plan(T, d_out, d_in, r);
     const int RP = p.RP;
     auto* part = at<float>(ws, p.part);
-    auto* u_hi = at<bf>(ws, p.u_hi);
-    auto* u_lo = at<bf>(ws, p.u_lo);
-    auto* g_hi = at<bf>(ws, p.g_hi);
-    auto* g_lo = at<bf>(ws, p.g_lo);
+    auto* u3 = at<bf>(ws, p.u3);
+    auto* g3 = at<bf>(ws, p.g3);
     int64_t dh_ld = d_out;
     if (d_out % 8) {          // rows that are no whole 16-byte units cannot be read by a tensor map
         dh_ld = (d_out + 7) / 8 * 8;
         QL_TRY(pad_bf16(static_cast<const bf*>(dH), T, d_out, d_out, at<bf>(ws, p.dh_pad), T, dh_ld, 0, dh_ld, st));
         dH = at<void>(ws, p.dh_pad);
     }
-    auto pair = [&](int split, float scale, bf* hi, bf* lo) -> qlora_status {
-        if (launch_pdl(k_finalize_pair, grid1d(T * RP), dim3(256), 0, st, part, split, T, r, RP, scale, RP, hi, lo) !=
+    auto triple = [&](int split, float scale, bf* out) -> qlora_status {
+        if (launch_pdl(k_finalize_triple, grid1d(T * RP), dim3(256), 0, st, part, split, T, r, RP, scale, out) !=
             cudaSuccess)
             return QLORA_ERR_CUDA;
         QL_LAUNCH_CHECK();
@@ -329,9 +334,14 @@ qlora_status mx_bwd(MxBase base, const void* X, const qlora_act8* X8, const void
     g.err = err;
     g.wait_ns = kWaitNs;
     g.part = part;
-    int u_nb = 2;                 // matrices that make up U
-    const void* u_src = u_hi;
-    int u_ld = RP;
+    g.ldp = RP;
+    if (X8) {
+        g.scales = X8->scales;
+        g.ld_scales = d_in / 32;
+    }
+    CUtensorMap ta, tb;
+    int u_nb = 3, u_ld = RP;      // the matrices that make up U
+    const void* u_src = u3;
     if (phase != kBwdDx) {
         // U = X~ A^T, unless the forward kept it
         if (U_saved) {
@@ -340,28 +350,22 @@ qlora_status mx_bwd(MxBase base, const void* X, const qlora_act8* X8, const void
                 u_src = U_saved;
                 u_ld = r;
             } else {
-                QL_TRY(pad_bf16(static_cast<const bf*>(U_saved), T, r, r, u_hi, T, RP, 0, RP, st));
+                QL_TRY(pad_bf16(static_cast<const bf*>(U_saved), T, r, r, u3, T, RP, 0, RP, st));
             }
-        } else if (X8) {
-            CUtensorMap ta, tb;
-            QL_TRY(tmap_u8(&ta, X8->q, T, d_in, d_in, 64, 128));
-            QL_TRY(tmap_bf16(&tb, A, r, d_in, d_in, static_cast<uint32_t>(RP)));
+        } else {
+            QL_TRY(tmap_bf16_3d(&tb, A, 1, r, d_in, d_in, static_cast<uint32_t>(RP)));
             g.M = static_cast<int>(T);
             g.K = d_in;
             g.k_steps = static_cast<int>(d_in / 64);
             g.split = p.split_u;
-            g.nb = 1;
-            g.scales = X8->scales;
-            g.ld_scales = d_in / 32;
-            g.ldp = RP;
-            QL_TRY((act_gemm<kActInt8K>(RP, ta, tb, tb, g, st)));
-            QL_TRY(pair(p.split_u, 1.f, u_hi, u_lo));
-        } else {
-            CUtensorMap ta, tb;
-            QL_TRY(tmap_bf16(&ta, X, T, d_in, d_in, kBM));
-            QL_TRY(tmap_bf16(&tb, A, r, d_in, d_in, RP));
-            QL_TRY(skinny_gemm(false, false, RP, r, ta, tb, T, cdiv(d_in, kBK), p.split_u, part, err, st));
-            QL_TRY(pair(p.split_u, 1.f, u_hi, u_lo));
+            if (X8) {
+                QL_TRY(tmap_u8(&ta, X8->q, T, d_in, d_in, 64, 128));
+                QL_TRY((act_gemm<true, false, false, 1>(RP, ta, tb, g, st)));
+            } else {
+                QL_TRY(tmap_bf16(&ta, X, T, d_in, d_in, 128));
+                QL_TRY((act_gemm<false, false, false, 1>(RP, ta, tb, g, st)));
+            }
+            QL_TRY(triple(p.split_u, 1.f, u3));
         }
         // s G = s dH B
         const void* b_src = B;
@@ -371,63 +375,54 @@ qlora_status mx_bwd(MxBase base, const void* X, const qlora_act8* X8, const void
             b_src = at<void>(ws, p.b_pad);
             b_ld = RP;
         }
-        CUtensorMap ta, tb;
-        QL_TRY(tmap_bf16(&ta, dH, T, d_out, dh_ld, kBM));
-        QL_TRY(tmap_bf16(&tb, b_src, d_out, b_ld, b_ld, 64));
-        QL_TRY(skinny_gemm(false, true, RP, r, ta, tb, T, cdiv(d_out, kBK), p.split_g, part, err, st));
-        QL_TRY(pair(p.split_g, s, g_hi, g_lo));
+        QL_TRY(tmap_bf16(&ta, dH, T, d_out, dh_ld, 128));
+        QL_TRY(tmap_bf16_3d(&tb, b_src, 1, d_out, r, b_ld, 64));
+        g.M = static_cast<int>(T);
+        g.K = d_out;
+        g.k_steps = static_cast<int>(cdiv(d_out, 64));
+        g.split = p.split_g;
+        QL_TRY((act_gemm<false, false, true, 1>(RP, ta, tb, g, st)));
+        QL_TRY(triple(p.split_g, s, g3));
     }
     // dX = dH W + (sG) A; the adapter term's s G is rounded to bf16 (2^-9 of that term, as dX itself is)
     if (dX && phase != kBwdGrads) {
         if (base.mx)
-            QL_TRY(mx_dx_gemm(base.mx, dH, dh_ld, T, g_hi, A, RP, r, dX, at<void>(ws, p.g2), err, st));
+            QL_TRY(mx_dx_gemm(base.mx, dH, dh_ld, T, g3, A, RP, r, dX, at<void>(ws, p.g2), err, st));
         else
-            QL_TRY(nf4_gemm(true, base.nf4, dH, T, g_hi, A, RP, r, r, dX, at<void>(ws, p.g2), err, st, nullptr, nullptr,
+            QL_TRY(nf4_gemm(true, base.nf4, dH, T, g3, A, RP, r, r, dX, at<void>(ws, p.g2), err, st, nullptr, nullptr,
                             nullptr, dh_ld));
     }
     if (phase == kBwdDx) return QLORA_OK;
     // dA^T[d_in, r] = X~^T (s G), partials stored as [split][r][d_in]
-    {
-        CUtensorMap ta, t0, t1;
-        QL_TRY(tmap_bf16(&t0, g_hi, T, r, RP, 64));
-        QL_TRY(tmap_bf16(&t1, g_lo, T, r, RP, 64));
-        g.M = static_cast<int>(d_in);
-        g.K = T;
-        g.k_steps = static_cast<int>(cdiv(T, 64));
-        g.split = p.split_da;
-        g.nb = 2;
-        g.transposed = 1;
-        if (X8) {
-            QL_TRY(tmap_u8(&ta, X8->q, T, d_in, d_in, 128, 64));
-            g.scales = X8->scales;
-            g.ld_scales = d_in / 32;
-            QL_TRY((act_gemm<kActInt8Mn>(RP, ta, t0, t1, g, st)));
-        } else {
-            QL_TRY(tmap_bf16(&ta, X, T, d_in, d_in, 64));
-            QL_TRY((act_gemm<kActBf16Mn>(RP, ta, t0, t1, g, st)));
-        }
-        const int64_t n = static_cast<int64_t>(r) * d_in;
-        if (launch_pdl(k_finalize_flat, grid1d(n), dim3(256), 0, st, part, p.split_da, n, 1.f, dA, acc) != cudaSuccess)
-            return QLORA_ERR_CUDA;
-        QL_LAUNCH_CHECK();
+    QL_TRY(tmap_bf16_3d(&tb, g3, 3, T, r, RP, 64));
+    g.M = static_cast<int>(d_in);
+    g.K = T;
+    g.k_steps = static_cast<int>(cdiv(T, 64));
+    g.split = p.split_da;
+    g.transposed = 1;
+    if (X8) {
+        QL_TRY(tmap_u8(&ta, X8->q, T, d_in, d_in, 128, 64));
+        QL_TRY((act_gemm<true, true, true, 3>(RP, ta, tb, g, st)));
+    } else {
+        QL_TRY(tmap_bf16(&ta, X, T, d_in, d_in, 64));
+        QL_TRY((act_gemm<false, true, true, 3>(RP, ta, tb, g, st)));
     }
+    const int64_t n_da = static_cast<int64_t>(r) * d_in;
+    if (launch_pdl(k_finalize_flat, grid1d(n_da), dim3(256), 0, st, part, p.split_da, n_da, 1.f, dA, acc) != cudaSuccess)
+        return QLORA_ERR_CUDA;
+    QL_LAUNCH_CHECK();
     // dB[d_out, r] = s dH^T U
-    {
-        CUtensorMap ta, t0, t1;
-        QL_TRY(tmap_bf16(&ta, dH, T, d_out, dh_ld, 64));
-        QL_TRY(tmap_bf16(&t0, u_src, T, r, u_ld, 64));
-        QL_TRY(tmap_bf16(&t1, u_nb > 1 ? u_lo : u_src, T, r, u_ld, 64));
-        g.M = static_cast<int>(d_out);
-        g.split = p.split_db;
-        g.nb = u_nb;
-        g.transposed = 0;
-        g.ldp = RP;
-        QL_TRY((act_gemm<kActBf16Mn>(RP, ta, t0, t1, g, st)));
-        if (launch_pdl(k_finalize_strided, grid1d(d_out * r), dim3(256), 0, st, part, p.split_db, d_out, r, RP, s, dB,
-                       acc) != cudaSuccess)
-            return QLORA_ERR_CUDA;
-        QL_LAUNCH_CHECK();
-    }
+    QL_TRY(tmap_bf16(&ta, dH, T, d_out, dh_ld, 64));
+    QL_TRY(tmap_bf16_3d(&tb, u_src, u_nb, T, r, u_ld, 64));
+    g.M = static_cast<int>(d_out);
+    g.split = p.split_db;
+    g.transposed = 0;
+    if (u_nb == 1) QL_TRY((act_gemm<false, true, true, 1>(RP, ta, tb, g, st)));
+    else QL_TRY((act_gemm<false, true, true, 3>(RP, ta, tb, g, st)));
+    if (launch_pdl(k_finalize_strided, grid1d(d_out * r), dim3(256), 0, st, part, p.split_db, d_out, r, RP, s, dB,
+                   acc) != cudaSuccess)
+        return QLORA_ERR_CUDA;
+    QL_LAUNCH_CHECK();
     return QLORA_OK;
 }
 
