@@ -632,6 +632,17 @@ def _need_ws(op, T, d_out, d_in, r, dev, ws):
     return ws           # its size is checked by the library
 
 
+def _mx_scale_bytes(rows, cols):
+    return 512 * -(-rows // 128) * -(-cols // 128)
+
+
+def _made(cls, **fields):
+    """A handle of buffers that were allocated here (nothing left to check)."""
+    h = object.__new__(cls)
+    h.__dict__.update(fields)
+    return h
+
+
 @dataclass(frozen=True)
 class MXFP4Weight:
     """Device buffers of an MXFP4 matrix: packed E2M1 codes and the tiled E8M0 scales (checked when
@@ -649,7 +660,7 @@ class MXFP4Weight:
         dev = _need_cuda("codes", self.codes)
         mxfp4_sizes(self.d_out, self.d_in)
         _need("codes", self.codes, torch.uint8, (self.d_out, self.d_in // 2), dev)
-        _need("scales", self.scales, torch.uint8, (512 * -(-self.d_out // 128) * -(-self.d_in // 128),), dev)
+        _need("scales", self.scales, torch.uint8, (_mx_scale_bytes(self.d_out, self.d_in),), dev)
 
 
 @dataclass(frozen=True)
@@ -687,15 +698,19 @@ def mxfp4_quantize(W, codes=None, scales=None, stream=None) -> MXFP4Weight:
     _contig(W)
     rows, cols = W.shape
     dt = _dtype_code(W.dtype)
-    _, ns = mxfp4_sizes(rows, cols)
+    if rows < 1 or cols < 64 or cols % 64:
+        raise QloraError("mxfp4_quantize", 2)
     with _run_on(dev, stream):
+        u8 = torch.uint8
         if codes is None:
-            codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=dev)
+            codes = W.new_empty((rows, cols // 2), dtype=u8)
+        else:
+            _need("codes", codes, u8, (rows, cols // 2), dev)
         if scales is None:
-            scales = torch.empty(ns, dtype=torch.uint8, device=dev)
-        w = MXFP4Weight(codes, scales, rows, cols)
-        if codes.device != dev:
-            raise ValueError(f"codes is on {codes.device}, expected {dev}")
+            scales = W.new_empty((_mx_scale_bytes(rows, cols),), dtype=u8)
+        else:
+            _need("scales", scales, u8, (_mx_scale_bytes(rows, cols),), dev)
+        w = _made(MXFP4Weight, codes=codes, scales=scales, d_out=rows, d_in=cols)
         _check("mxfp4_quantize", load().mxfp4_quantize(_addr(W), dt, rows, cols, _addr(codes), _addr(scales),
                                                        _raw_stream(dev, stream)))
     return w
@@ -751,13 +766,18 @@ def act8_quantize(X, q=None, scales=None, stream=None) -> Act8:
     _contig(X)
     T, d_in = X.shape
     dt = _dtype_code(X.dtype)
+    if T < 1 or d_in < 64 or d_in % 64:
+        raise QloraError("qlora_act8_quantize", 2)
     with _run_on(dev, stream):
         if q is None:
-            q = torch.empty((T, d_in), dtype=torch.int8, device=dev)
+            q = X.new_empty((T, d_in), dtype=torch.int8)
+        else:
+            _need("q", q, torch.int8, (T, d_in), dev)
         if scales is None:
-            scales = torch.empty((T, d_in // 32), dtype=torch.uint8, device=dev)
-        a = Act8(q, scales)
-        _need("q", q, torch.int8, (T, d_in), dev)
+            scales = X.new_empty((T, d_in // 32), dtype=torch.uint8)
+        else:
+            _need("scales", scales, torch.uint8, (T, d_in // 32), dev)
+        a = _made(Act8, q=q, scales=scales)
         _check("qlora_act8_quantize", load().qlora_act8_quantize(_addr(X), dt, T, d_in, _addr(q), _addr(scales),
                                                                  _raw_stream(dev, stream)))
     return a

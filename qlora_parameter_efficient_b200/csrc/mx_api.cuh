@@ -8,6 +8,7 @@ namespace {
 // ======================================================================= planning
 
 constexpr int64_t kMaxDim = 1LL << 30;
+constexpr int64_t kMxStreamMaxT = 512;
 
 qlora_status mx_check_dims(int64_t rows, int64_t cols) {
     if (rows < 1 || rows > kMaxDim || cols < 64 || cols % 64 || cols > kMaxDim) return QLORA_ERR_UNSUPPORTED;
@@ -23,10 +24,35 @@ qlora_status check_mxfp4(const qlora_mxfp4* w) {
 }
 
 // Routes of the MXFP4 forward by the number of tokens.
-enum MxRoute { kMxDecode, kMxStream64, kMxStream128 };
+enum MxRoute { kMxDecode, kMxStream64, kMxStream128, kMxPair };
 MxRoute mx_route(int64_t T) {
     if (T <= kMxDecodeT) return kMxDecode;
-    return T <= 64 ? kMxStream64 : kMxStream128;
+    if (T <= 64) return kMxStream64;
+    return T <= kMxStreamMaxT ? kMxStream128 : kMxPair;
+}
+
+// Schedule of k_pair_gemm: pairs of SMs; the tiles of an incomplete last wave are split along K over
+// as many pairs as the wave has for each, up to 8 and with at least min_steps stages a part.
+struct PairSched {
+    int pairs = 1, tail = 0, split = 1;
+    size_t part_bytes = 0;
+    int n_cnt = 0;
+    size_t bytes() const { return part_bytes + align256(static_cast<size_t>(n_cnt) * sizeof(int)); }
+};
+PairSched pair_schedule(int64_t M, int64_t N, int64_t k_steps, int64_t min_steps) {
+    PairSched g;
+    const int64_t tiles = cdiv(M, 256) * cdiv(N, 256), slots = kSmsForSplit / 2;
+    const int64_t rem = tiles % slots;
+    int64_t split = rem ? std::min<int64_t>(8, std::min(slots / rem, k_steps / min_steps)) : 1;
+    if (split < 1) split = 1;
+    g.split = static_cast<int>(split);
+    g.tail = split > 1 ? static_cast<int>(rem) : 0;
+    g.pairs = static_cast<int>(tiles >= slots ? slots : rem * split);
+    if (split > 1) {
+        g.part_bytes = static_cast<size_t>(rem) * 8 * split * 2048 * 16;
+        g.n_cnt = static_cast<int>(rem) * 8;
+    }
+    return g;
 }
 
 // Ranks of a weight-stream cluster: as many of 8, 4, 2, 1 as K has stages for and the resident CTAs
@@ -39,7 +65,8 @@ int mx_ranks(int64_t tiles, int64_t chunks, int64_t slots) {
 
 struct MxFwdPlan {
     int RP = 0, split_u = 1;
-    size_t codes = 0, scales = 0, us = 0, b_pad = 0, part = 0, total = 0;
+    size_t codes = 0, scales = 0, us = 0, b_pad = 0, part = 0, pair = 0, total = 0;
+    PairSched sched;
 };
 MxFwdPlan mx_fwd_plan(int64_t T, int64_t d_out, int64_t d_in, int r) {
     MxFwdPlan p;
@@ -58,6 +85,10 @@ MxFwdPlan mx_fwd_plan(int64_t T, int64_t d_out, int64_t d_in, int r) {
         p.split_u = choose_split(cdiv(T, kBM), cdiv(d_in, kBK));
         p.part = take(static_cast<size_t>(p.split_u) * T * p.RP * 4);
     }
+    if (mx_route(T) == kMxPair) {
+        p.sched = pair_schedule(T, d_out, cdiv(d_in, 256), 2);
+        p.pair = take(p.sched.bytes());
+    }
     p.total = off;
     return p;
 }
@@ -65,7 +96,8 @@ MxFwdPlan mx_fwd_plan(int64_t T, int64_t d_out, int64_t d_in, int r) {
 // The backward of an MXFP4 or NF4 base from a bf16 activation or an 8-bit checkpoint.
 struct MxBwdPlan {
     int RP = 0, split_u = 1, split_g = 1, split_da = 1, split_db = 1;
-    size_t b_pad = 0, dh_pad = 0, u3 = 0, g3 = 0, part = 0, g2 = 0, total = 0;
+    size_t b_pad = 0, dh_pad = 0, u3 = 0, g3 = 0, part = 0, w = 0, pair = 0, total = 0;
+    PairSched sched;
 };
 // k_act_gemm runs one CTA per SM: one wave of them.
 int act_split(int64_t tiles, int64_t k_steps) {
@@ -95,7 +127,9 @@ MxBwdPlan mx_bwd_plan(int64_t T, int64_t d_out, int64_t d_in, int r) {
     part = std::max(part, static_cast<size_t>(p.split_da) * d_in * r * 4);
     part = std::max(part, static_cast<size_t>(p.split_db) * d_out * rp * 4);
     p.part = take(part);
-    p.g2 = take(g2_schedule(T, d_in, d_out).bytes());
+    p.w = take(static_cast<size_t>(d_out) * d_in * 2);      // the decoded weight
+    p.sched = pair_schedule(T, d_in, cdiv(d_out, 64), 8);
+    p.pair = take(p.sched.bytes());
     p.total = off;
     return p;
 }
@@ -184,46 +218,60 @@ qlora_status act_gemm(int RP, const CUtensorMap& ta, const CUtensorMap& tb, cons
                     : launch_act_gemm<INT8, AMN, BMN, 128, NB>(ta, tb, g, st);
 }
 
-// dX = dH W4 + (sG) A: the fused decode GEMM with its decoders reading MXFP4.
-qlora_status mx_dx_gemm(const qlora_mxfp4* w, const void* dH, int64_t dh_ld, int64_t T, const void* g_hi,
-                        const void* A, int RP, int r, void* dX, void* g2ws, int* err, cudaStream_t st) {
-    const int64_t d_out = w->d_out, d_in = w->d_in;
-    CUtensorMap ta, tc, tax, tbx;
-    QL_TRY(tmap_bf16(&ta, dH, T, d_out, dh_ld, 128));
-    QL_TRY(tmap_u8(&tc, w->codes, d_out, d_in / 2, d_in / 2, 64, 64));
-    QL_TRY(tmap_bf16(&tax, g_hi, T, RP, RP, 128));
-    QL_TRY(tmap_bf16(&tbx, A, r, d_in, d_in, 64));
-    Gemm2Args g{};
-    g.M = static_cast<int>(T);
-    g.N = static_cast<int>(d_in);
-    g.k_steps = static_cast<int>(cdiv(d_out, 64));
-    g.ext_steps = RP / 64;
-    g.ext_k16_last = static_cast<int>(std::min<int64_t>(4, cdiv(r - 64 * (g.ext_steps - 1), 16)));
-    g.m_tiles = static_cast<int>(cdiv(T, 256));
-    g.n_tiles = static_cast<int>(cdiv(d_in, 256));
-    g.mx_scales = w->scales;
-    g.mx_col_tiles = static_cast<int>(mx_col_tiles(d_in));
-    g.nf4_rows = static_cast<int>(d_out);
-    g.nf4_bpr = static_cast<int>(d_in / 64);
-    g.out = static_cast<__nv_bfloat16*>(dX);
-    g.ld_out = d_in;
+template <bool MX>
+qlora_status launch_pair_gemm(const CUtensorMap (&t)[6], PairGemmArgs g, const PairSched& sch, void* ws, int* err,
+                              cudaStream_t st) {
+    using L = PairGemmSmem<MX>;
+    g.split = sch.split;
+    g.tail_tiles = sch.tail;
+    g.part = static_cast<float*>(ws);
+    g.cnt = reinterpret_cast<int*>(static_cast<uint8_t*>(ws) + sch.part_bytes);
     g.err = err;
     g.wait_ns = kWaitNs;
-    const G2Sched sch = g2_schedule(T, d_in, d_out);
-    g.split_tiles = sch.split_tiles;
-    if (sch.split_tiles > 0) {
-        g.part = static_cast<float*>(g2ws);
-        g.cnt = reinterpret_cast<int*>(static_cast<uint8_t*>(g2ws) + sch.part_bytes);
-        if (cudaMemsetAsync(g.cnt, 0, sch.cnt_bytes, st) != cudaSuccess) return QLORA_ERR_CUDA;
-    }
-    auto kern = k_nf4_gemm2<true, false, kWMxfp4>;
     static std::atomic<uint64_t> configured{0};
-    QL_TRY(allow_smem(kern, G2Smem<false>::kTotal, configured));
-    if (launch_pdl(kern, dim3(2 * sch.pairs), dim3(G2Smem<false>::kThreads), G2Smem<false>::kTotal, st, ta, tc, tax,
-                   tbx, g) != cudaSuccess)
+    QL_TRY(allow_smem(k_pair_gemm<MX>, L::kTotal, configured));
+    if (launch_pdl(k_pair_gemm<MX>, dim3(2 * sch.pairs), dim3(L::kThreads), L::kTotal, st, t[0], t[1], t[2], t[3], t[4],
+                   t[5], g) != cudaSuccess)
         return QLORA_ERR_CUDA;
     QL_LAUNCH_CHECK();
     return QLORA_OK;
+}
+
+// Scale tiles as rows of 128 words, two tiles (256 elements of K) per box.
+qlora_status tmap_scales(CUtensorMap* m, const void* base, int64_t rows, int64_t cols) {
+    QL_TRY(get_encoder());
+    cuuint64_t dims[2] = {128, static_cast<cuuint64_t>(cdiv(rows, 128) * mx_col_tiles(cols))};
+    cuuint64_t strides[1] = {kMxTileBytes};
+    cuuint32_t box[2] = {128, 2};
+    cuuint32_t es[2] = {1, 1};
+    CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), dims, strides, box, es,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? QLORA_OK : QLORA_ERR_CUDA;
+}
+
+// dX = dH W + (sG) A over the weight decoded to bf16 in the workspace.
+qlora_status dx_gemm(const void* W, const void* dH, int64_t dh_ld, int64_t T, int64_t d_out, int64_t d_in,
+                     const void* sG, const void* A, int RP, int r, void* dX, const PairSched& sch, void* pair_ws,
+                     int* err, cudaStream_t st) {
+    CUtensorMap t[6];
+    QL_TRY(tmap_bf16(&t[0], dH, T, d_out, dh_ld, 128));
+    QL_TRY(tmap_bf16(&t[1], W, d_out, d_in, d_in, 64));
+    QL_TRY(tmap_bf16(&t[4], sG, T, r, RP, 128));
+    QL_TRY(tmap_bf16(&t[5], A, r, d_in, d_in, 64));
+    t[2] = t[3] = t[0];
+    PairGemmArgs g{};
+    g.M = static_cast<int>(T);
+    g.N = static_cast<int>(d_in);
+    g.k_steps = static_cast<int>(cdiv(d_out, 64));
+    g.k_mma_last = static_cast<int>(cdiv(d_out - 64 * (g.k_steps - 1), 16));
+    g.ext_steps = RP / 64;
+    g.ext_k16_last = static_cast<int>(cdiv(r - 64 * (g.ext_steps - 1), 16));
+    g.m_tiles = static_cast<int>(cdiv(T, 256));
+    g.n_tiles = static_cast<int>(cdiv(d_in, 256));
+    g.out = static_cast<__nv_bfloat16*>(dX);
+    g.ld_out = d_in;
+    return launch_pair_gemm<false>(t, g, sch, pair_ws, err, st);
 }
 
 // ======================================================================= sequences
@@ -268,12 +316,34 @@ qlora_status mx_fwd(const qlora_mxfp4* w, const void* X, int64_t T, const void* 
         QL_LAUNCH_CHECK();
     } else {
         k_mxfp4_quantize<bf><<<static_cast<unsigned>(cdiv(T, 128) * mx_col_tiles(d_in)), 256, 0, st>>>(
-            static_cast<const bf*>(X), T, d_in, codes, scales);
+            static_cast<const bf*>(X), T, d_in, codes, scales, at<int>(ws, p.pair + p.sched.part_bytes), p.sched.n_cnt);
         QL_LAUNCH_CHECK();
         if (!direct)
             QL_TRY(pad_bf16(static_cast<const bf*>(B), d_out, r, r, at<bf>(ws, p.b_pad), d_out, RP, 0, RP, st));
         QL_TRY(compute_u_bf16(X, T, d_in, A, r, RP, r, s, p.split_u, at<float>(ws, p.part), static_cast<bf*>(U_save),
                               nullptr, us, err, st));
+    }
+    if (route == kMxPair) {
+        CUtensorMap t[6];
+        QL_TRY(tmap_u8_sw128(&t[0], codes, T, d_in / 2, d_in / 2, 128));
+        QL_TRY(tmap_u8_sw128(&t[1], w->codes, d_out, d_in / 2, d_in / 2, 128));
+        QL_TRY(tmap_scales(&t[2], scales, T, d_in));
+        QL_TRY(tmap_scales(&t[3], w->scales, d_out, d_in));
+        QL_TRY(tmap_bf16(&t[4], us, T, r, RP, 128));
+        QL_TRY(tmap_bf16(&t[5], b_src, d_out, r, b_ld, 128));
+        PairGemmArgs g{};
+        g.M = static_cast<int>(T);
+        g.N = static_cast<int>(d_out);
+        g.k_steps = static_cast<int>(cdiv(d_in, 256));
+        g.k_mma_last = static_cast<int>(d_in / 64 - 4 * (g.k_steps - 1));
+        g.ext_steps = RP / 64;
+        g.ext_k16_last = static_cast<int>(cdiv(r - 64 * (g.ext_steps - 1), 16));
+        g.m_tiles = static_cast<int>(cdiv(T, 256));
+        g.n_tiles = static_cast<int>(cdiv(d_out, 256));
+        g.a_sf_tiles = g.b_sf_tiles = static_cast<int>(mx_col_tiles(d_in));
+        g.out = static_cast<bf*>(H);
+        g.ld_out = d_out;
+        return launch_pair_gemm<true>(t, g, p.sched, at<void>(ws, p.pair), err, st);
     }
     CUtensorMap tw, tx, tb, tu;
     const uint32_t nt = route == kMxDecode ? 16 : (route == kMxStream64 ? 64 : 128);
@@ -386,11 +456,22 @@ qlora_status mx_bwd(MxBase base, const void* X, const qlora_act8* X8, const void
     }
     // dX = dH W + (sG) A; the adapter term's s G is rounded to bf16 (2^-9 of that term, as dX itself is)
     if (dX && phase != kBwdGrads) {
-        if (base.mx)
-            QL_TRY(mx_dx_gemm(base.mx, dH, dh_ld, T, g3, A, RP, r, dX, at<void>(ws, p.g2), err, st));
-        else
-            QL_TRY(nf4_gemm(true, base.nf4, dH, T, g3, A, RP, r, r, dX, at<void>(ws, p.g2), err, st, nullptr, nullptr,
-                            nullptr, dh_ld));
+        auto* W = at<bf>(ws, p.w);
+        int* zero = at<int>(ws, p.pair + p.sched.part_bytes);
+        const int64_t n = d_out * d_in;
+        if (base.mx) {
+            if (launch_pdl(k_mxfp4_dequant<bf>, grid1d(n / 8), dim3(256), 0, st, base.mx->codes, base.mx->scales, d_out,
+                           d_in, W, zero, p.sched.n_cnt) != cudaSuccess)
+                return QLORA_ERR_CUDA;
+        } else {
+            if (p.sched.n_cnt &&
+                cudaMemsetAsync(zero, 0, static_cast<size_t>(p.sched.n_cnt) * sizeof(int), st) != cudaSuccess)
+                return QLORA_ERR_CUDA;
+            k_nf4_dequant_bf16<<<static_cast<unsigned>(cdiv(n / 64, 256)), 256, 0, st>>>(
+                base.nf4->codes, base.nf4->absmax_q, base.nf4->c2, n / 64, W);
+        }
+        QL_LAUNCH_CHECK();
+        QL_TRY(dx_gemm(W, dH, dh_ld, T, d_out, d_in, g3, A, RP, r, dX, p.sched, at<void>(ws, p.pair), err, st));
     }
     if (phase == kBwdDx) return QLORA_OK;
     // dA^T[d_in, r] = X~^T (s G), partials stored as [split][r][d_in]
@@ -471,10 +552,11 @@ qlora_status mxfp4_quantize(const void* W, qlora_dtype w_dtype, int64_t rows, in
     QL_TRY(mx_check_dims(rows, cols));
     const unsigned tiles = static_cast<unsigned>(cdiv(rows, 128) * mx_col_tiles(cols));
     if (w_dtype == QLORA_F32)
-        k_mxfp4_quantize<float><<<tiles, 256, 0, stream>>>(static_cast<const float*>(W), rows, cols, codes, scales);
+        k_mxfp4_quantize<float><<<tiles, 256, 0, stream>>>(static_cast<const float*>(W), rows, cols, codes, scales,
+                                                         nullptr, 0);
     else
         k_mxfp4_quantize<__nv_bfloat16><<<tiles, 256, 0, stream>>>(static_cast<const __nv_bfloat16*>(W), rows, cols,
-                                                                   codes, scales);
+                                                                   codes, scales, nullptr, 0);
     QL_LAUNCH_CHECK();
     return QLORA_OK;
 }
@@ -485,10 +567,10 @@ qlora_status mxfp4_dequantize(const qlora_mxfp4* w, void* W_out, qlora_dtype out
     const dim3 grid = grid1d(w->d_out * w->d_in / 8);
     if (out_dtype == QLORA_F32)
         k_mxfp4_dequant<float><<<grid, 256, 0, stream>>>(w->codes, w->scales, w->d_out, w->d_in,
-                                                         static_cast<float*>(W_out));
+                                                         static_cast<float*>(W_out), nullptr, 0);
     else
         k_mxfp4_dequant<__nv_bfloat16><<<grid, 256, 0, stream>>>(w->codes, w->scales, w->d_out, w->d_in,
-                                                                 static_cast<__nv_bfloat16*>(W_out));
+                                                                 static_cast<__nv_bfloat16*>(W_out), nullptr, 0);
     QL_LAUNCH_CHECK();
     return QLORA_OK;
 }

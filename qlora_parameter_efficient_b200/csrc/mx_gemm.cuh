@@ -13,7 +13,8 @@
 // k_mx_stream: one CTA per 128 weight rows, the tokens as the (narrow) N operand, K split over the
 //   ranks of a cluster whose partials meet in shared memory.  For token counts whose time is the
 //   weight stream.
-// k_mx_gemm: persistent pairs of CTAs (cta_group::2) on 256 x 256 tiles, for the rest.
+// k_pair_gemm: persistent pairs of CTAs (cta_group::2) on 256 x 256 tiles, for the rest; with bf16
+//   operands also the backward's dX over a decoded weight.
 #pragma once
 
 #include "common.cuh"
@@ -411,6 +412,378 @@ __global__ void __launch_bounds__(MxStreamCfg<NT>::kThreads)
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, L::kTmem);
+    }
+}
+
+// ------------------------------------------------------------------ persistent 2-SM kernel
+
+// 2-D tiled load into this CTA's shared memory that completes on a barrier of either CTA of the
+// pair (bar: cluster address).
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* m, uint32_t bar, int32_t x,
+                                                 int32_t y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y)
+        : "memory");
+}
+
+struct PairGemmArgs {
+    int M, N;                 // output rows (tokens) and columns
+    int k_steps;              // main stages: 256 MXFP4 or 64 bf16 elements of K
+    int k_mma_last;           // MMAs of the last main stage (1..4)
+    int ext_steps;            // adapter K stages of 64
+    int ext_k16_last;
+    int m_tiles, n_tiles;     // 256 x 256 tiles
+    int a_sf_tiles, b_sf_tiles;   // MXFP4: scale tiles per row of tiles (both operands share d_in)
+    int split;                // ways the tail tiles are split along K (1: not)
+    int tail_tiles;           // trailing tiles that are split
+    float* part;              // [tail_tiles][2 ranks][4 warps][split][2048 float4] fp32 partials
+    int* cnt;                 // [tail_tiles][2 ranks][4 warps] tickets, zero at launch
+    __nv_bfloat16* out;
+    int64_t ld_out;
+    int* err;
+    uint64_t wait_ns;
+};
+
+template <bool MX>
+struct PairGemmSmem {
+    static constexpr int kA = 128 * 128;               // this CTA's A half: 128 rows of 128 bytes
+    static constexpr int kB = 128 * 128;               // its B half
+    static constexpr int kSfA = MX ? 1024 : 0;         // scales of its 128 A rows
+    static constexpr int kSfB = MX ? 2048 : 0;         // scales of all 256 B rows
+    static constexpr int kStage = kA + kB + kSfA + kSfB;
+    static constexpr int kStages = MX ? 6 : 7;
+    static constexpr int kTotal = 1024 + kStages * kStage + 512;
+    static constexpr int kThreads = 192;
+    // Accumulator columns of the second buffer.  MXFP4 keeps the scales in columns 448..511, so its
+    // two accumulators share 64 columns, which the epilogue reads first.
+    static constexpr int kAcc1 = MX ? 192 : 256;
+    static constexpr int kSfCol = 448;
+    static_assert(kTotal <= 232448, "shared memory budget");
+};
+
+// MX:  out[T, d_out] = X4 W4^T + sU B^T   (kind::mxf4, all operands K-major)
+// !MX: out[T, d_in]  = dH W + sG A        (kind::f16, W bf16 [K, N] and A [r, N] consumed MN-major)
+//
+// A pair of CTAs computes 256 x 256 tiles with cta_group::2 MMAs of M = N = 256 issued by the leader;
+// each CTA loads half of both operands (and, for MXFP4, the scales of its own A rows and of all B
+// rows).  Both CTAs' copies complete on the leader's full[s], so one wait covers the pair; a stage
+// is released to both by the MMAs' commit.  Persistent: pair p takes tiles p, p + pairs, ...; the tiles
+// of an incomplete last wave (all of them when there are fewer tiles than pairs) are split along K
+// over `split` pairs each.  Every epilogue warp of a split tile writes its fp32 partial and takes a
+// ticket; the last adds all partials in K order, so the result does not depend on which is last,
+// and no CTA waits for another.
+// Bound (256 x 256 x 256 MXFP4 or x 64 bf16 per 512 tensor cycles): 32 to 35 KB per SM and stage
+// out of L2.
+template <bool MX>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGemmSmem<MX>::kThreads, 1)
+    k_pair_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                const __grid_constant__ CUtensorMap tmSa, const __grid_constant__ CUtensorMap tmSb,
+                const __grid_constant__ CUtensorMap tmAx, const __grid_constant__ CUtensorMap tmBx,
+                const PairGemmArgs args) {
+    using L = PairGemmSmem<MX>;
+    constexpr int S = L::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    uint8_t* sA = smem;
+    uint8_t* sB = sA + S * L::kA;
+    uint8_t* sSa = sB + S * L::kB;
+    uint8_t* sSb = sSa + S * L::kSfA;
+    uint64_t* full = reinterpret_cast<uint64_t*>(sSb + S * L::kSfB);   // leader: both halves landed
+    uint64_t* empty = full + S;             // both: stage consumed
+    uint64_t* accf = empty + S;             // [2] both: accumulator complete
+    uint64_t* acc_free = accf + 2;          // [2] leader: accumulator (MX: its shared columns) read
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_free + 2);
+    volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+    const int n_tiles_total = args.m_tiles * args.n_tiles;
+    const int iters_per_tile = args.k_steps + args.ext_steps;
+    const int tail_base = n_tiles_total - args.tail_tiles;
+    // this pair's units: whole tiles pair, pair + npairs, ... < tail_base, then at most one part of a
+    // tail tile (part p: main stages [p k / split, (p + 1) k / split), the last part also the adapter's)
+    const int n_full = pair < tail_base ? (tail_base - pair + npairs - 1) / npairs : 0;
+    const bool has_part = pair < args.tail_tiles * args.split;
+    const int part_tile = has_part ? pair / args.split : 0, part = has_part ? pair % args.split : 0;
+    const int n_units = n_full + (has_part ? 1 : 0);
+    auto unit = [&](int u, int& tile, int& k0, int& k1) {
+        if (u < n_full) {
+            tile = pair + u * npairs;
+            k0 = 0;
+            k1 = iters_per_tile;
+        } else {
+            tile = tail_base + part_tile;
+            k0 = args.k_steps * part / args.split;
+            k1 = part == args.split - 1 ? iters_per_tile : args.k_steps * (part + 1) / args.split;
+        }
+    };
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&accf[b], 1);
+            mbar_init(&acc_free[b], 8);
+        }
+        *abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&tmA);
+        tma_prefetch_desc(&tmB);
+        tma_prefetch_desc(&tmAx);
+        tma_prefetch_desc(&tmBx);
+        if (MX) {
+            tma_prefetch_desc(&tmSa);
+            tma_prefetch_desc(&tmSb);
+        }
+    }
+    if (warp == 1) {
+        tmem_alloc_2sm(tmem_slot, 512);
+        tmem_relinquish_2sm();
+    }
+    tc_fence_before();
+    cluster_barrier();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    griddep_enter();
+
+    auto fail = [&]() {
+        set_error(args.err, kErrTimeout);
+        *abort = 1;
+    };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            const uint32_t full_leader = mapa_shared(smem_u32(&full[0]), 0);
+            int git = 0;
+            for (int u = 0; u < n_units && !*abort; ++u) {
+                int tile, k0, k1;
+                unit(u, tile, k0, k1);
+                const int m0 = (tile % args.m_tiles) * 256 + static_cast<int>(rank) * 128;
+                const int nt = tile / args.m_tiles;
+                const int n0 = nt * 256 + static_cast<int>(rank) * 128;
+                for (int it = k0; it < k1; ++it, ++git) {
+                    const int s = git % S;
+                    if (!mbar_wait(&empty[s], ((git / S) & 1) ^ 1, abort, args.wait_ns)) {
+                        fail();
+                        break;
+                    }
+                    const uint32_t bar = full_leader + static_cast<uint32_t>(s * 8);
+                    uint8_t* a = sA + s * L::kA;
+                    uint8_t* b = sB + s * L::kB;
+                    const bool main_step = it < args.k_steps;
+                    if (rank == 0)
+                        mbar_arrive_expect_tx(&full[s], 2 * (main_step ? L::kStage : L::kA + L::kB));
+                    if (main_step) {
+                        if (MX) {
+                            tma_load_2d_pair(a, &tmA, bar, it * 128, m0);
+                            tma_load_2d_pair(b, &tmB, bar, it * 128, n0);
+                            tma_load_2d_pair(sSa + s * L::kSfA, &tmSa, bar, 0, (m0 >> 7) * args.a_sf_tiles + 2 * it);
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+                                tma_load_2d_pair(sSb + s * L::kSfB + h * 1024, &tmSb, bar, 0,
+                                                 (2 * nt + h) * args.b_sf_tiles + 2 * it);
+                        } else {
+                            tma_load_2d_pair(a, &tmA, bar, it * 64, m0);
+                            tma_load_2d_pair(b, &tmB, bar, n0, it * 64);
+                            tma_load_2d_pair(b + 8192, &tmB, bar, n0 + 64, it * 64);
+                        }
+                    } else {
+                        const int kx = (it - args.k_steps) * 64;
+                        tma_load_2d_pair(a, &tmAx, bar, kx, m0);
+                        if (MX) {
+                            tma_load_2d_pair(b, &tmBx, bar, kx, n0);
+                        } else {
+                            tma_load_2d_pair(b, &tmBx, bar, n0, kx);
+                            tma_load_2d_pair(b + 8192, &tmBx, bar, n0 + 64, kx);
+                        }
+                    }
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (rank == 0 && lane == 0) {
+            const uint32_t idesc = make_idesc_bf16(256, 256, false, !MX);
+            int git = 0;
+            bool ok = true;
+            for (int u = 0; ok && u < n_units; ++u) {
+                int tile, k0, k1;
+                unit(u, tile, k0, k1);
+                // MX: the shared columns of unit u - 1 have been read; else: all of unit u - 2
+                const int prev = u - (MX ? 1 : 2);
+                if (prev >= 0 && !mbar_wait_cluster(&acc_free[prev & 1], (prev >> 1) & 1, abort, args.wait_ns)) {
+                    fail();
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t d = tmem + static_cast<uint32_t>((u & 1) * L::kAcc1);
+                for (int it = k0; it < k1; ++it, ++git) {
+                    const int s = git % S;
+                    ok = mbar_wait_cluster(&full[s], (git / S) & 1, abort, args.wait_ns);
+                    // two sets of scale columns in turn: those of stage git - 2 are free once its MMAs are done
+                    if (MX && ok && git >= 2)
+                        ok = mbar_wait(&empty[(git - 2) % S], ((git - 2) / S) & 1, abort, args.wait_ns);
+                    if (!ok) {
+                        fail();
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t a = smem_u32(sA + s * L::kA), b = smem_u32(sB + s * L::kB);
+                    if (it < args.k_steps) {
+                        const int nk = it == args.k_steps - 1 ? args.k_mma_last : 4;
+                        if constexpr (MX) {
+                            const uint32_t sfa = tmem + L::kSfCol + (git & 1) * 24, sfb = sfa + 8;
+                            for (int h = 0; h < (nk + 1) / 2; ++h) {
+                                tmem_cp_scales<2>(sfa + 4 * h, smem_u32(sSa + s * L::kSfA + h * 512));
+                                tmem_cp_scales<2>(sfb + 8 * h, smem_u32(sSb + s * L::kSfB + h * 512));
+                                tmem_cp_scales<2>(sfb + 8 * h + 4, smem_u32(sSb + s * L::kSfB + 1024 + h * 512));
+                            }
+                            for (int k = 0; k < nk; ++k) {
+                                const uint32_t id = (k & 1) * 2;
+                                umma_mxf4_ss<2>(d, make_sw128_desc(a + k * 32, 16, 1024),
+                                                make_sw128_desc(b + k * 32, 16, 1024),
+                                                make_idesc_mxf4(256, 256, id, id), sfa + 4 * (k >> 1),
+                                                sfb + 8 * (k >> 1), (it > k0 || k > 0) ? 1u : 0u);
+                            }
+                        } else {
+                            for (int k = 0; k < nk; ++k)
+                                umma_bf16_ss_2sm(d, make_sw128_desc(a + k * 32, 16, 1024),
+                                                 make_sw128_desc(b + k * 2048, 8192, 1024), idesc,
+                                                 (it > k0 || k > 0) ? 1u : 0u);
+                        }
+                    } else {
+                        const int nk = it == iters_per_tile - 1 ? args.ext_k16_last : 4;
+                        for (int k = 0; k < nk; ++k)
+                            umma_bf16_ss_2sm(d, make_sw128_desc(a + k * 32, 16, 1024),
+                                             MX ? make_sw128_desc(b + k * 32, 16, 1024)
+                                                : make_sw128_desc(b + k * 2048, 8192, 1024),
+                                             idesc, (it > k0 || k > 0) ? 1u : 0u);
+                    }
+                    umma_commit_2sm_both(&empty[s]);
+                }
+                umma_commit_2sm_both(&accf[u & 1]);
+            }
+        }
+    } else {
+        // ---------------------------------------------------------------- epilogue
+        const int q = warp & 3;
+        const uint32_t free_leader = mapa_shared(smem_u32(&acc_free[0]), 0);
+        const bool vec_rows = (args.ld_out & 7) == 0;
+        for (int u = 0; u < n_units; ++u) {
+            int tile, k0, k1;
+            unit(u, tile, k0, k1);
+            const int buf = u & 1;
+            if (!mbar_wait_warp(&accf[buf], (u >> 1) & 1, abort, args.wait_ns)) {
+                fail();
+                break;
+            }
+            tc_fence_after();
+            const int64_t grow = static_cast<int64_t>(tile % args.m_tiles) * 256 + rank * 128 + q * 32 + lane;
+            const int gc0 = (tile / args.m_tiles) * 256;
+            const uint32_t tbase = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * L::kAcc1;
+            const bool split = u >= n_full && args.split > 1;
+            bool last = true;
+            const float4* parts = nullptr;
+            if (split) {
+                const int64_t slot = (static_cast<int64_t>(part_tile) * 2 + rank) * 4 + q;
+                float4* mine = reinterpret_cast<float4*>(args.part) + ((slot * args.split + part) << 11);
+#pragma unroll 1
+                for (int c = 0; c < 8; ++c) {
+                    uint32_t r[32];
+                    tmem_ld_32x32b_x32(tbase + c * 32, r);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int g = 0; g < 8; ++g)
+                        mine[g2_part_idx(c, g, lane)] =
+                            make_float4(__uint_as_float(r[4 * g]), __uint_as_float(r[4 * g + 1]),
+                                        __uint_as_float(r[4 * g + 2]), __uint_as_float(r[4 * g + 3]));
+                }
+                __threadfence();
+                __syncwarp();
+                int ticket = 0;
+                if (lane == 0) ticket = atomicAdd(args.cnt + slot, 1);
+                last = __shfl_sync(0xffffffffu, ticket, 0) == args.split - 1;
+                if (last) {
+                    __threadfence();
+                    parts = reinterpret_cast<const float4*>(args.part) + ((slot * args.split) << 11);
+                }
+            }
+            // MX: the columns that the other accumulator shares come first (the last 64 of
+            // buffer 0, the first 64 of buffer 1)
+            const int rot = (MX && buf == 0) ? 6 : 0;
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i) {
+                const int c = (i + rot) & 7;
+                uint32_t r[32];
+                if (last) {
+                    if (parts) {
+                        float4 v[8];
+#pragma unroll
+                        for (int g = 0; g < 8; ++g) v[g] = __ldcg(parts + g2_part_idx(c, g, lane));
+                        for (int p = 1; p < args.split; ++p) {
+#pragma unroll
+                            for (int g = 0; g < 8; ++g) {
+                                const float4 o = __ldcg(parts + (static_cast<int64_t>(p) << 11) + g2_part_idx(c, g, lane));
+                                v[g].x += o.x;
+                                v[g].y += o.y;
+                                v[g].z += o.z;
+                                v[g].w += o.w;
+                            }
+                        }
+#pragma unroll
+                        for (int g = 0; g < 8; ++g) {
+                            r[4 * g] = __float_as_uint(v[g].x);
+                            r[4 * g + 1] = __float_as_uint(v[g].y);
+                            r[4 * g + 2] = __float_as_uint(v[g].z);
+                            r[4 * g + 3] = __float_as_uint(v[g].w);
+                        }
+                    } else {
+                        tmem_ld_32x32b_x32(tbase + c * 32, r);
+                        tmem_ld_wait();
+                    }
+                    const int gc = gc0 + c * 32;
+                    if (grow < args.M) {
+                        __nv_bfloat16* o = args.out + grow * args.ld_out + gc;
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) {
+                            if (gc + 8 * g + 8 <= args.N && vec_rows) {
+                                uint4 v;
+                                v.x = pack_bf16x2(__uint_as_float(r[8 * g + 0]), __uint_as_float(r[8 * g + 1]));
+                                v.y = pack_bf16x2(__uint_as_float(r[8 * g + 2]), __uint_as_float(r[8 * g + 3]));
+                                v.z = pack_bf16x2(__uint_as_float(r[8 * g + 4]), __uint_as_float(r[8 * g + 5]));
+                                v.w = pack_bf16x2(__uint_as_float(r[8 * g + 6]), __uint_as_float(r[8 * g + 7]));
+                                *reinterpret_cast<uint4*>(o + 8 * g) = v;
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < 8; ++e)
+                                    if (gc + 8 * g + e < args.N) o[8 * g + e] = __float2bfloat16_rn(__uint_as_float(r[8 * g + e]));
+                            }
+                        }
+                    }
+                }
+                if (i == (MX ? 1 : 7)) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_remote_async_payload(free_leader + static_cast<uint32_t>(buf * 8));
+                }
+            }
+        }
+    }
+
+    __syncwarp();
+    if (*abort) __nanosleep(100000);   // copies in flight land before shared memory is released
+    tc_fence_before();
+    cluster_barrier();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_2sm(tmem, 512);
     }
 }
 

@@ -17,9 +17,6 @@
 // the matrix are 0.
 #pragma once
 
-#include <cuda_fp16.h>
-#include <cuda_fp4.h>
-
 #include "common.cuh"
 
 namespace qlora {
@@ -69,6 +66,20 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t m) {
     return max(m, __shfl_xor_sync(0xffffffffu, m, 2));
 }
 
+// Eight fp32 values to packed E2M1 codes, round to nearest even, saturating at 6.
+__device__ __forceinline__ uint32_t e2m1x8(const float (&x)[8]) {
+    uint32_t q;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+        : "=r"(q)
+        : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+    return q;
+}
+
 // One 128 x 128 scale tile of a matrix: 256 threads, sixteen lanes per row (8 elements each, four
 // lanes per block), 8 passes of 16 rows.  The tile's scales are gathered in shared memory
 // and written once, 512 contiguous bytes.
@@ -97,14 +108,9 @@ __device__ __forceinline__ void mxfp4_quantize_tile(const T* __restrict__ X, int
         const uint32_t e = ef == 255u ? 255u : (ef > 2u ? ef - 2u : 0u);
         // 2^(127 - e); 0 for a NaN block, whose codes are 0
         const float inv = __uint_as_float(e == 255u ? 0u : (254u - e) << 23);
-        uint32_t q = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            q |= static_cast<uint32_t>(__nv_cvt_float2_to_fp4x2(
-                     make_float2(__fmul_rn(x[p][2 * i], inv), __fmul_rn(x[p][2 * i + 1], inv)), __NV_E2M1,
-                     cudaRoundNearest))
-                 << (8 * i);
-        if (e == 255u) q = 0;
+        for (int i = 0; i < 8; ++i) x[p][i] = __fmul_rn(x[p][i], inv);
+        const uint32_t q = e == 255u ? 0u : e2m1x8(x[p]);
         if (row < rows && col < cols) *reinterpret_cast<uint32_t*>(codes + (row * cols + col) / 2) = q;
         if ((seg & 3) == 0)
             s_sc[(lr & 31) * 16 + (lr >> 5) * 4 + (seg >> 2)] =
@@ -117,12 +123,16 @@ __device__ __forceinline__ void mxfp4_quantize_tile(const T* __restrict__ X, int
 }
 
 // grid: one CTA per scale tile, column tiles fastest.
+// zero[0, n_zero): ticket counters of a later kernel of the call, cleared on the way.
 template <typename T>
 __global__ void __launch_bounds__(256) k_mxfp4_quantize(const T* __restrict__ X, int64_t rows, int64_t cols,
                                                         uint8_t* __restrict__ codes,
-                                                        uint8_t* __restrict__ scales) {
+                                                        uint8_t* __restrict__ scales, int* __restrict__ zero,
+                                                        int n_zero) {
     __shared__ __align__(16) uint8_t s_sc[kMxTileBytes];
     griddep_enter();
+    if (blockIdx.x == 0)
+        for (int i = threadIdx.x; i < n_zero; i += 256) zero[i] = 0;
     const int64_t kts = mx_col_tiles(cols);
     mxfp4_quantize_tile(X, rows, cols, blockIdx.x / kts, blockIdx.x % kts, codes, scales, s_sc);
 }
@@ -145,23 +155,15 @@ __device__ __forceinline__ uint4 e2m1_decode8_bf16(uint32_t q) {
                       prmt(lo_b, hi_b, 0x7362));
 }
 
-// bf16 of 2^(e - 127), twice; exact (e = 0 is a bf16 subnormal), NaN for 255.
-__device__ __forceinline__ uint32_t e8m0_bf16x2(uint32_t e) {
-    const uint32_t b = e == 255u ? 0x7FFFu : (e == 0u ? 0x0040u : e << 7);
-    return b | (b << 16);
-}
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-    const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a),
-                                     *reinterpret_cast<const __nv_bfloat162*>(&b));
-    return *reinterpret_cast<const uint32_t*>(&r);
-}
-
 // One thread per 8 elements: 4 code bytes in, 16 (bf16) or 32 (fp32) bytes out.
 template <typename T>
 __global__ void __launch_bounds__(256) k_mxfp4_dequant(const uint8_t* __restrict__ codes,
                                                        const uint8_t* __restrict__ scales, int64_t rows,
-                                                       int64_t cols, T* __restrict__ out) {
+                                                       int64_t cols, T* __restrict__ out, int* __restrict__ zero,
+                                                       int n_zero) {
     griddep_enter();
+    if (blockIdx.x == 0)
+        for (int i = threadIdx.x; i < n_zero; i += 256) zero[i] = 0;
     const int64_t n8 = rows * cols / 8, per_row = cols / 8, kts = mx_col_tiles(cols);
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n8;
          i += static_cast<int64_t>(gridDim.x) * blockDim.x) {

@@ -49,10 +49,7 @@
 // Every wait is bounded (QLORA_ERR_TIMEOUT on expiry); all TMA loads are plain local loads.
 #pragma once
 
-#include <type_traits>
-
 #include "common.cuh"
-#include "mxfp4.cuh"
 #include "nf4.cuh"
 
 namespace qlora {
@@ -187,8 +184,6 @@ struct Gemm2Args {
     int* cnt;              // [split_tiles][2 ranks][4 warps] tickets, zero at launch
     const float* x_scale;  // FP8: sigma_x (device scalar)
     const float* w_scale;  // FP8: sigma_w (device scalar)
-    const uint8_t* mx_scales;  // MXFP4 weight: tiled E8M0 scales
-    int mx_col_tiles;          // MXFP4 weight: scale tiles along d_in
     int* err;
     uint64_t wait_ns;
 };
@@ -197,15 +192,7 @@ struct Gemm2Args {
 // consecutive lanes of one store are consecutive 16-byte words.
 __device__ __forceinline__ int g2_part_idx(int c, int g, int lane) { return (c * 8 + g) * 32 + lane; }
 
-// Stored format of the weight the decoders read.
-enum : int { kWNf4 = 0, kWMxfp4 = 1 };
-
-// Decode table of one 64-column chunk of an MXFP4 row: its two block scales as bf16x2 factors.
-struct MxScalePair {
-    uint32_t s0, s1;
-};
-
-template <bool B_MN, bool FP8 = false, int FMT = kWNf4>
+template <bool B_MN, bool FP8 = false>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G2Smem<FP8>::kThreads, 1)
     k_nf4_gemm2(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmC,
                 const __grid_constant__ CUtensorMap tmAx, const __grid_constant__ CUtensorMap tmBx,
@@ -667,11 +654,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G2Smem<FP8>::kThread
             mc = nc;
         }
     } else {
-        // -------------------------------------------------------------- NF4 / MXFP4 decoders
-        // (MXFP4: a thread's 64 columns are two blocks of 32; an E2M1 value times a power of two is
-        // a bf16 value, so the decode is a table of eight magnitudes and one bf16x2 product)
-        constexpr bool kMx = FMT == kWMxfp4;
-        using Table = typename std::conditional<kMx, MxScalePair, Nf4Planes>::type;
+        // -------------------------------------------------------------- NF4 decoders
         const int grp = (warp - 6) >> 2;
         const int j = ((warp - 6) & 3) * 32 + lane;      // 0..127: block of this thread
         int row_in_tile, blk_col_off;
@@ -704,56 +687,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G2Smem<FP8>::kThread
             }
             if (wrow >= args.nf4_rows || wblk >= args.nf4_bpr) return -1;
             const int64_t blk = wrow * args.nf4_bpr + wblk;
-            if (!dcheck(blk < static_cast<int64_t>(args.nf4_rows) * args.nf4_bpr, args.err)) return -1;
-            if constexpr (kMx) return mx_scale_offset(wrow, 2 * wblk, args.mx_col_tiles);
-            return blk;
+            return dcheck(blk < static_cast<int64_t>(args.nf4_rows) * args.nf4_bpr, args.err) ? blk : -1;
         };
         uint64_t* arrive_bar = rank == 0 ? ready : dec_done;   // local arrive either way
-        uint32_t q8_nxt = 0;
-        float c2_nxt = 0.f;
-        auto load_scale = [&](int64_t blk) {
-            if (blk < 0) return;
-            if constexpr (kMx) {
-                q8_nxt = __ldg(reinterpret_cast<const uint16_t*>(args.mx_scales + blk));
-            } else {
-                q8_nxt = __ldg(args.absmax_q + blk);
-                c2_nxt = __ldg(args.c2 + (blk >> 8));
-            }
-        };
-        auto make_table = [&]() -> Table {
-            if constexpr (kMx) return MxScalePair{e8m0_bf16x2(q8_nxt & 255u), e8m0_bf16x2(q8_nxt >> 8)};
-            else return nf4_make_planes(nf4_block_scale(q8_nxt, c2_nxt));
-        };
         // Software pipeline per handled step: the step's 64 weights are decoded into registers
         // as soon as its code tile has landed -- before its decoded-B slot is free -- so the
         // slot is held only for the stores; the next block's tables are built after that.
         uint4 dec[8];
-        auto decode_into_regs = [&](int git, int64_t blk, const Table& p) {
+        auto decode_into_regs = [&](int git, int64_t blk, const Nf4Planes& p) {
             const int s = git % SA;
             const uint8_t* c = sC + s * L::kC;
             const uint8_t* src = B_MN ? c + row_in_tile * 64 + blk_col_off * 32 : c + row_in_tile * 32;
             if (blk >= 0) {
                 const uint4 q0 = *reinterpret_cast<const uint4*>(src);
                 const uint4 q1 = *reinterpret_cast<const uint4*>(src + 16);
-                const uint32_t qs[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
-#pragma unroll
-                for (int ch = 0; ch < 8; ++ch) {
-                    if constexpr (kMx) {
-                        const uint32_t f = ch < 4 ? p.s0 : p.s1;
-                        const uint4 v = e2m1_decode8_bf16(qs[ch]);
-                        dec[ch] = make_uint4(mul_bf16x2(v.x, f), mul_bf16x2(v.y, f), mul_bf16x2(v.z, f),
-                                             mul_bf16x2(v.w, f));
-                    } else {
-                        dec[ch] = nf4_decode8(qs[ch], p);
-                    }
-                }
+                dec[0] = nf4_decode8(q0.x, p);
+                dec[1] = nf4_decode8(q0.y, p);
+                dec[2] = nf4_decode8(q0.z, p);
+                dec[3] = nf4_decode8(q0.w, p);
+                dec[4] = nf4_decode8(q1.x, p);
+                dec[5] = nf4_decode8(q1.y, p);
+                dec[6] = nf4_decode8(q1.z, p);
+                dec[7] = nf4_decode8(q1.w, p);
             } else {
 #pragma unroll
                 for (int ch = 0; ch < 8; ++ch) dec[ch] = make_uint4(0, 0, 0, 0);
             }
         };
         int64_t blk_nxt = next_block();
-        load_scale(blk_nxt);
+        uint32_t q8_nxt = 0;
+        float c2_nxt = 0.f;
+        if (blk_nxt >= 0) {
+            q8_nxt = __ldg(args.absmax_q + blk_nxt);
+            c2_nxt = __ldg(args.c2 + (blk_nxt >> 8));
+        }
         bool have = false;          // dec[] holds step `git` (decoded ahead)
         Cur mc = cur_at(grp);
         for (int git = grp; git < total_iters; git += NG) {
@@ -764,10 +731,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G2Smem<FP8>::kThread
             if (!have) {
                 // (first step, or after an adapter step) decode now
                 const int64_t blk = blk_nxt;
-                Table p{};
-                if (blk >= 0) p = make_table();
+                Nf4Planes p{};
+                if (blk >= 0) p = nf4_make_planes(nf4_block_scale(q8_nxt, c2_nxt));
                 blk_nxt = next_block();
-                load_scale(blk_nxt);
+                if (blk_nxt >= 0) {
+                    q8_nxt = __ldg(args.absmax_q + blk_nxt);
+                    c2_nxt = __ldg(args.c2 + (blk_nxt >> 8));
+                }
                 if (!mbar_wait_warp(&full[s], (git / SA) & 1, abort, args.wait_ns)) {
                     fail();
                     break;
@@ -794,10 +764,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G2Smem<FP8>::kThread
             const int gn = git + NG;
             if (gn < total_iters && nc.it < args.k_steps) {
                 const int64_t blk = blk_nxt;
-                Table p{};
-                if (blk >= 0) p = make_table();
+                Nf4Planes p{};
+                if (blk >= 0) p = nf4_make_planes(nf4_block_scale(q8_nxt, c2_nxt));
                 blk_nxt = next_block();
-                load_scale(blk_nxt);
+                if (blk_nxt >= 0) {
+                    q8_nxt = __ldg(args.absmax_q + blk_nxt);
+                    c2_nxt = __ldg(args.c2 + (blk_nxt >> 8));
+                }
                 if (!mbar_wait_warp(&full[gn % SA], (gn / SA) & 1, abort, args.wait_ns)) {
                     fail();
                     break;

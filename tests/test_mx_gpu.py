@@ -172,7 +172,9 @@ def check_forward(q, T, d_out, d_in, r, seed=0):
 
 FWD = [(1, 64, 64, 1), (1, 256, 256, 16), (1, 1000, 4096, 16), (2, 130, 192, 5), (7, 77, 320, 8), (16, 513, 1088, 64),
        (17, 128, 256, 33), (40, 300, 576, 100), (64, 129, 2048, 128), (65, 64, 64, 8), (127, 200, 448, 12),
-       (128, 256, 512, 16), (200, 1001, 1024, 7), (300, 384, 704, 64), (513, 520, 960, 128)]
+       (128, 256, 512, 16), (200, 1001, 1024, 7), (300, 384, 704, 64), (513, 520, 960, 128),
+       # 256 x 256 tiles: fewer than the pairs of SMs (split along K), more (a split last wave), whole
+       (600, 513, 1088, 64), (1000, 300, 320, 5), (1025, 1000, 2048, 16), (2600, 2100, 1088, 8), (700, 77, 64, 16)]
 
 
 @pytest.mark.parametrize("T,d_out,d_in,r", FWD)
@@ -215,7 +217,8 @@ def check_backward(q, T, d_out, d_in, r, base, ckpt, keep_u, seed=0):
 
 
 BWD = [(1, 64, 64, 1), (3, 77, 128, 5), (64, 200, 192, 8), (65, 256, 320, 16), (130, 513, 448, 33),
-       (257, 128, 1088, 64), (300, 1001, 512, 100), (513, 300, 704, 128)]
+       (257, 128, 1088, 64), (300, 1001, 512, 100), (513, 300, 704, 128), (1100, 2000, 576, 16),
+       (2600, 1100, 2112, 8)]
 
 
 @pytest.mark.parametrize("keep_u", [True, False])
