@@ -20,6 +20,7 @@
 
 #include "common.cuh"
 #include "mxfp4.cuh"
+#include "nf4.cuh"
 
 namespace qlora {
 
@@ -28,35 +29,40 @@ __device__ __forceinline__ float act8_step(uint32_t e) {
     return __uint_as_float(e == 255u ? 0x7FFFFFFFu : (e >= 7u ? (e - 6u) << 23 : 1u << (e + 16u)));
 }
 
-// Four lanes per block of 32, eight elements per lane.
+// Four lanes per block of 32, eight elements per lane, kAct8Unroll chunks of 256 lanes per CTA whose
+// loads are issued together.  n8 (elements / 8) is a multiple of 8, so a block is never split.
+constexpr int kAct8Unroll = 4;
 template <typename T>
 __global__ void __launch_bounds__(256) k_act8_quantize(const T* __restrict__ X, int64_t n8,
                                                        int8_t* __restrict__ q, uint8_t* __restrict__ scales) {
     griddep_enter();
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
-    // n8 is a multiple of 4 (whole blocks) and blockDim of 32: a quad is never split
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i - (threadIdx.x & 31) < n8;
-         i += stride) {
+    const int64_t i0 = static_cast<int64_t>(blockIdx.x) * (256 * kAct8Unroll) + threadIdx.x;
+    Raw8<T> raw[kAct8Unroll];
+#pragma unroll
+    for (int u = 0; u < kAct8Unroll; ++u) {
+        if (i0 + u * 256 < n8) raw[u].load(X + (i0 + u * 256) * 8);
+        else raw[u].zero();
+    }
+#pragma unroll
+    for (int u = 0; u < kAct8Unroll; ++u) {
+        const int64_t i = i0 + u * 256;
         float x[8];
-        uint32_t m = 0;
-        const bool in = i < n8;
-        if (in) m = load8(X + i * 8, x);
-        const uint32_t e = quad_max(m) >> 23;
-        if (!in) continue;
+        const uint32_t e = quad_max(raw[u].values(x)) >> 23;
         // x 2^(133 - e) in two exact steps (2^133 is no fp32 value)
         const uint32_t ec = max(e, 6u);
         const float f = __uint_as_float((260u - ec) << 23);
         const float g = static_cast<float>(1u << (ec - e));
         uint32_t w[2] = {0, 0};
-        if (e != 255u) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float y = fminf(fmaxf(rintf(__fmul_rn(__fmul_rn(x[k], f), g)), -127.f), 127.f);
-                w[k >> 2] |= (static_cast<uint32_t>(static_cast<int>(y)) & 255u) << (8 * (k & 3));
-            }
+        for (int k = 0; k < 8; ++k) {
+            // rounded by adding 1.5 2^23 (to nearest even, the integer in the low bits)
+            const float y = fminf(fmaxf(__fmul_rn(__fmul_rn(x[k], f), g), -127.f), 127.f) + 12582912.f;
+            w[k >> 2] |= (__float_as_uint(y) & 255u) << (8 * (k & 3));
         }
-        reinterpret_cast<uint2*>(q)[i] = make_uint2(w[0], w[1]);
-        if ((i & 3) == 0) scales[i >> 2] = static_cast<uint8_t>(e);
+        if (i < n8) {
+            reinterpret_cast<uint2*>(q)[i] = e == 255u ? make_uint2(0, 0) : make_uint2(w[0], w[1]);
+            if ((i & 3) == 0) scales[i >> 2] = static_cast<uint8_t>(e);
+        }
     }
 }
 
@@ -84,104 +90,166 @@ __global__ void __launch_bounds__(256) k_act8_dequant(const int8_t* __restrict__
                                                       const uint8_t* __restrict__ scales, int64_t n8,
                                                       T* __restrict__ out) {
     griddep_enter();
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n8;
-         i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-        const uint2 v = __ldg(reinterpret_cast<const uint2*>(q) + i);
-        const float s = act8_step(__ldg(scales + (i >> 2)));
+    const int64_t i0 = static_cast<int64_t>(blockIdx.x) * (256 * kAct8Unroll) + threadIdx.x;
+    uint2 v[kAct8Unroll];
+    uint32_t e[kAct8Unroll];
+#pragma unroll
+    for (int u = 0; u < kAct8Unroll; ++u) {
+        const int64_t i = i0 + u * 256;
+        v[u] = make_uint2(0, 0);
+        e[u] = 0;
+        if (i < n8) {
+            v[u] = __ldg(reinterpret_cast<const uint2*>(q) + i);
+            e[u] = __ldg(scales + (i >> 2));
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < kAct8Unroll; ++u) {
+        const int64_t i = i0 + u * 256;
+        if (i >= n8) break;
+        const float s = act8_step(e[u]);
         if constexpr (sizeof(T) == 4) {
             float a[4], b[4];
-            int8x4_to_f32(v.x, a);
-            int8x4_to_f32(v.y, b);
+            int8x4_to_f32(v[u].x, a);
+            int8x4_to_f32(v[u].y, b);
             float4* o = reinterpret_cast<float4*>(out) + 2 * i;
             o[0] = make_float4(a[0] * s, a[1] * s, a[2] * s, a[3] * s);
             o[1] = make_float4(b[0] * s, b[1] * s, b[2] * s, b[3] * s);
         } else {
-            reinterpret_cast<uint4*>(out)[i] = act8_decode8(v.x, v.y, s);
+            reinterpret_cast<uint4*>(out)[i] = act8_decode8(v[u].x, v[u].y, s);
         }
     }
 }
 
 // ------------------------------------------------------------------ adapter products
 
-struct ActGemmArgs {
-    int M, N;                // output rows (channels or tokens) and valid columns (the rank)
+// A matrix of fp32 values [T, r] as a tensor-core operand: three bf16 terms per value, whose sum is the
+// value (8 significant bits each), as column groups of one matrix.  Up to rank 64 the groups are
+// `stride` = the rank rounded up to 16 apart, so that one MMA takes all three (N = 3 stride, each
+// group with accumulator columns of its own); above, 128 apart, one MMA each into the same columns.
+struct ActTriple {
+    int stride, ld;
+};
+__host__ __device__ __forceinline__ ActTriple act_triple(int r) {
+    ActTriple t;
+    t.stride = r <= 64 ? (r + 15) & ~15 : 128;
+    t.ld = (3 * t.stride + 63) & ~63;
+    return t;
+}
+
+// What becomes of the sum D[M, N] of a product.
+enum : int {
+    kActTriple = 0,   // scale D as three bf16 terms (ActTriple layout)
+    kActCols = 1,     // fp32 out[j, m] = scale D[m, j]  (dA)
+    kActRows = 2      // fp32 out[m, j] = scale D[m, j]  (dB)
+};
+
+// One product of a launch: D[M, N] = sum over K of A[M, K] B[N, K], B bf16 or a bf16 triple.
+struct ActJob {
+    int M, N;                // output rows (channels or tokens) and columns (the rank)
     int64_t K;               // contraction length
     int k_steps;             // ceil(K / 64)
-    int split;               // split-K over grid.y
+    int int8;                // A is int8 with E8M0 scales, decoded to bf16 in shared memory (else bf16)
+    int amn;                 // A is stored [K, M] (tokens are K) and consumed MN-major, else [M, K]
+    int bmn;                 // B is stored [K, N], else [N, K]
+    int triple;              // B is an ActTriple (bmn only)
     const uint8_t* scales;   // E8M0 bytes of the int8 operand, row-major
     int64_t ld_scales;       // blocks per stored row
-    float* part;             // fp32 partials: [split][M][ldp], or transposed [split][N][M]
-    int64_t ldp;
-    int transposed;
+    int mode;
+    float scale;
+    int accumulate;          // kActCols, kActRows: add to out
+    void* out;
+};
+struct ActGemmArgs {
+    ActJob job[2];
+    int tiles0;              // M tiles of job 0; tiles above belong to job 1
+    int ranks;               // CTAs per cluster, K split over them
     int* err;
     uint64_t wait_ns;
 };
 
-// RPT: the padded rank, 64 or 128 (B tile rows); NB: bf16 matrices whose sum B is, 1 or 3.
-template <bool INT8, int RPT, int NB>
+// RPT: the padded rank, 64 or 128 (B tile rows).
+template <int RPT>
 struct ActGemmSmem {
     static constexpr int kA = 128 * 64 * 2;                     // bf16 operand tile
-    static constexpr int kRaw = INT8 ? 128 * 64 : 0;
-    static constexpr int kB = RPT * 64 * 2;                     // one B matrix's tile
-    static constexpr int kStage = kA + kRaw + NB * kB;
-    static constexpr int kStages = 221184 / kStage < 6 ? 221184 / kStage : 6;
-    static constexpr int kTotal = 1024 + kStages * kStage + 512;
-    // K steps of 64 per accumulator segment (see the kernel)
-    static constexpr int kSeg = NB == 1 ? 4 : 2;
-    static_assert(kTotal <= 232448 && kStages >= 3, "shared memory budget");
+    static constexpr int kRaw = 128 * 64;                       // int8 tile
+    static constexpr int kChunk = 64 * 64 * 2;                  // 64 columns (or rows) of the B tile
+    static constexpr int kRing = 221184;
+    static constexpr int kMaxStages = 6;
+    static constexpr int kAcc = 4;                              // accumulator tiles, at most
+    static constexpr int kTotal = 1024 + kRing + 512;
+    static constexpr int kLdRed = RPT + 4;                      // floats per row of the joining buffer
+    static_assert(kTotal <= 232448 && 128 * kLdRed * 4 <= kRing, "shared memory budget");
+    static_assert(3 * (kA + kRaw + 3 * RPT / 64 * kChunk) <= kRing, "three stages at least");
 };
 
-// D[M, N] = sum over K of A[M, K] B[N, K], B the sum of NB bf16 matrices; fp32 split-K partials.
-//   INT8   A is int8 with E8M0 scales, decoded to bf16 in shared memory (else bf16)
-//   AMN    A is stored [K, M] (tokens are K) and consumed MN-major, else [M, K]
-//   BMN    B is stored [K, N], else [N, K]; B's tensor map is three-dimensional, matrix outermost
-// Warp 0: TMA; warp 1: MMA; warps 2..9: int8 decode (one 32-element block per thread and stage),
-// accumulator drains, partials.
+// Warp 0: TMA; warp 1: MMA; warps 2..9: int8 decode (one 32-element block per thread and stage) and
+// accumulator drains.  A cluster's ranks split K; their sums meet in shared memory, each rank adding and
+// writing 128 / ranks rows in rank order, so no partial goes through memory.  Up to two products share
+// a launch (U and G; dA and dB).
 //
 // Precision: the results are fp32 gradients.  (1) A value that was computed here (s G, a recomputed U)
 // is given to the bf16 tensor cores as the three bf16 numbers that make up its 24 bits, so nothing is
 // rounded off it.  (2) The tensor core's running fp32 sum is truncated at every MMA -- a bias that
 // grows with the chain: 9e-6 of a gradient over 8192 tokens.  So the chain is cut into segments of
-// 16 or 24 MMAs, whose sums warps 2..9 add up in registers, rounding to nearest, from two
+// 16 or 24 MMAs, whose sums warps 2..9 add up in registers, rounding to nearest, from two to four
 // accumulator tiles in turn.
 // Bound by memory: a K step of 64 reads 8 KB of int8 (or 16 KB of bf16) from HBM and the B tiles from
-// L2; N is the rank rounded up to 16, so that the MMAs stay below that.
-template <bool INT8, bool AMN, bool BMN, int RPT, int NB>
+// L2.  An MMA of M = 128 takes about 75 cycles however small N is (it reads its A tile), hence one of
+// N = 3 stride for a triple and not three.
+template <int RPT>
 __global__ void __launch_bounds__(320, 1)
-    k_act_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-               const ActGemmArgs args) {
-    using L = ActGemmSmem<INT8, RPT, NB>;
-    constexpr int S = L::kStages, kSeg = L::kSeg;
+    k_act_gemm(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmB0,
+               const __grid_constant__ CUtensorMap tmA1, const __grid_constant__ CUtensorMap tmB1,
+               const __grid_constant__ ActGemmArgs args) {
+    using L = ActGemmSmem<RPT>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
-    uint8_t* sA = smem;
-    uint8_t* sB = sA + S * L::kA;
-    uint8_t* sR = sB + S * NB * L::kB;
-    uint64_t* full = reinterpret_cast<uint64_t*>(sR + S * L::kRaw);
-    uint64_t* empty = full + S;
-    uint64_t* decoded = empty + S;
-    uint64_t* accf = decoded + S;         // [2] segment complete
-    uint64_t* acc_free = accf + 2;        // [2] segment drained (8 warp arrivals)
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_free + 2);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kRing);
+    uint64_t* empty = full + L::kMaxStages;
+    uint64_t* decoded = empty + L::kMaxStages;
+    uint64_t* accf = decoded + L::kMaxStages;   // [kAcc] segment complete
+    uint64_t* acc_free = accf + L::kAcc;        // [kAcc] segment drained (8 warp arrivals)
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_free + L::kAcc);
     volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int m0 = blockIdx.x * 128;
-    const int z = blockIdx.y;
-    const int per = (args.k_steps + args.split - 1) / args.split;
-    const int k_begin = z * per;
-    const int n_iters = max(0, min(args.k_steps, k_begin + per) - k_begin);
-    const int n_seg = (n_iters + kSeg - 1) / kSeg;
-    const int n_mma = (args.N + 15) & ~15;
+    const int C = args.ranks;
+    const int rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int tile = blockIdx.x / C;
+    const int ji = tile >= args.tiles0 ? 1 : 0;
+    const ActJob& job = args.job[ji];
+    const CUtensorMap* tmA = ji ? &tmA1 : &tmA0;
+    const CUtensorMap* tmB = ji ? &tmB1 : &tmB0;
+    const int m0 = (tile - (ji ? args.tiles0 : 0)) * 128;
+    const bool int8 = job.int8, amn = job.amn, bmn = job.bmn;
+    const int k_begin = static_cast<int>(static_cast<int64_t>(job.k_steps) * rank / C);
+    const int n_iters = static_cast<int>(static_cast<int64_t>(job.k_steps) * (rank + 1) / C) - k_begin;
+    const ActTriple tr = act_triple(job.N);
+    const int terms = RPT == 64 && job.triple ? 3 : 1;         // column groups of an accumulator tile
+    const int groups = RPT == 128 && job.triple ? 3 : 1;       // MMAs per 16 of K
+    const int n_mma = terms == 3 ? 3 * tr.stride : (job.N + 15) & ~15;
+    const int chunks = job.triple ? tr.ld / 64 : RPT / 64;     // of the B tile
+    const int acc_cols = terms == 3 ? tr.ld : RPT;
+    const int NA = min(L::kAcc, 512 / acc_cols);               // accumulator tiles
+    const int seg_len = groups == 3 ? 2 : 4;                   // K steps of 64 per accumulator segment
+    const int n_seg = (n_iters + seg_len - 1) / seg_len;
+    // ring: A tiles, B tiles, int8 tiles
+    const int b_bytes = chunks * L::kChunk;
+    const int stage = L::kA + b_bytes + (int8 ? L::kRaw : 0);
+    const int S = min(L::kMaxStages, L::kRing / stage);
+    uint8_t* sA = smem;
+    uint8_t* sB = sA + S * L::kA;
+    uint8_t* sR = sB + S * b_bytes;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < S; ++s) {
+        for (int s = 0; s < L::kMaxStages; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
             mbar_init(&decoded[s], 8);
         }
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < L::kAcc; ++b) {
             mbar_init(&accf[b], 1);
             mbar_init(&acc_free[b], 8);
         }
@@ -189,11 +257,11 @@ __global__ void __launch_bounds__(320, 1)
         fence_mbar_init();
     }
     if (warp == 0 && lane == 0) {
-        tma_prefetch_desc(&tmA);
-        tma_prefetch_desc(&tmB);
+        tma_prefetch_desc(tmA);
+        tma_prefetch_desc(tmB);
     }
     if (warp == 1) {
-        tmem_alloc(tmem_slot, 2 * RPT);
+        tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -206,36 +274,38 @@ __global__ void __launch_bounds__(320, 1)
         set_error(args.err, kErrTimeout);
         *abort = 1;
     };
+    // warps 2..9: this thread's row and half of the columns
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    constexpr int kHalf = RPT / 2;
+    float acc[kHalf];
+#pragma unroll
+    for (int j = 0; j < kHalf; ++j) acc[j] = 0.f;
 
     if (warp == 0) {
         if (lane == 0) {
             int issued = 0;
-            for (int it = 0; it < n_iters; ++it) {
-                const int s = it % S;
-                if (!mbar_wait(&empty[s], ((it / S) & 1) ^ 1, abort, args.wait_ns)) {
+            for (int it = 0, s = 0, ph = 0; it < n_iters; ++it) {
+                if (!mbar_wait(&empty[s], ph ^ 1, abort, args.wait_ns)) {
                     fail();
                     break;
                 }
                 const int kx = (k_begin + it) * 64;
-                mbar_arrive_expect_tx(&full[s], (INT8 ? L::kRaw : L::kA) + NB * L::kB);
-                uint8_t* a = INT8 ? sR + s * L::kRaw : sA + s * L::kA;
-                if (AMN) {
-                    tma_load_2d(a, &tmA, &full[s], m0, kx);
-                    if (!INT8) tma_load_2d(a + 8192, &tmA, &full[s], m0 + 64, kx);
+                mbar_arrive_expect_tx(&full[s], (int8 ? L::kRaw : L::kA) + b_bytes);
+                uint8_t* a = int8 ? sR + s * L::kRaw : sA + s * L::kA;
+                if (amn) {
+                    tma_load_2d(a, tmA, &full[s], m0, kx);
+                    if (!int8) tma_load_2d(a + 8192, tmA, &full[s], m0 + 64, kx);
                 } else {
-                    tma_load_2d(a, &tmA, &full[s], kx, m0);
+                    tma_load_2d(a, tmA, &full[s], kx, m0);
                 }
-#pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    uint8_t* dst = sB + (s * NB + b) * L::kB;
-                    if (BMN) {
-#pragma unroll
-                        for (int c = 0; c < RPT / 64; ++c) tma_load_3d(dst + c * 8192, &tmB, &full[s], c * 64, kx, b);
-                    } else {
-                        tma_load_3d(dst, &tmB, &full[s], kx, 0, b);
-                    }
+                uint8_t* dst = sB + s * b_bytes;
+                if (bmn) {
+                    for (int c = 0; c < chunks; ++c) tma_load_2d(dst + c * L::kChunk, tmB, &full[s], c * 64, kx);
+                } else {
+                    tma_load_2d(dst, tmB, &full[s], kx, 0);
                 }
                 issued = it + 1;
+                if (++s == S) s = 0, ph ^= 1;
             }
             if (*abort)
                 for (int it = max(0, issued - S); it < issued; ++it)
@@ -243,86 +313,94 @@ __global__ void __launch_bounds__(320, 1)
         }
     } else if (warp == 1) {
         if (lane == 0) {
-            const uint32_t idesc = make_idesc_bf16(128, n_mma, AMN, BMN);
-            for (int it = 0; it < n_iters; ++it) {
-                const int s = it % S, seg = it / kSeg;
-                const uint32_t ph = (it / S) & 1;
+            const uint32_t idesc = make_idesc_bf16(128, n_mma, amn, bmn);
+            const uint32_t a_step = amn ? 2048 : 32, a_lbo = amn ? 8192 : 16;
+            const uint32_t b_step = bmn ? 2048 : 32, b_lbo = bmn ? 8192 : 16;
+            int seg = 0, in_seg = 0;
+            for (int it = 0, s = 0, ph = 0; it < n_iters; ++it) {
                 bool ok = true;
-                if (it % kSeg == 0 && seg >= 2)
-                    ok = mbar_wait(&acc_free[seg & 1], ((seg >> 1) & 1) ^ 1, abort, args.wait_ns);
+                if (in_seg == 0 && seg >= NA)
+                    ok = mbar_wait(&acc_free[seg % NA], ((seg / NA) & 1) ^ 1, abort, args.wait_ns);
                 if (ok) ok = mbar_wait(&full[s], ph, abort, args.wait_ns);
-                if (ok && INT8) ok = mbar_wait(&decoded[s], ph, abort, args.wait_ns);
+                if (ok && int8) ok = mbar_wait(&decoded[s], ph, abort, args.wait_ns);
                 if (!ok) {
                     fail();
                     break;
                 }
                 tc_fence_after();
-                const uint32_t d = tmem + static_cast<uint32_t>((seg & 1) * RPT);
+                const uint32_t d = tmem + static_cast<uint32_t>((seg % NA) * acc_cols);
                 const uint32_t a = smem_u32(sA + s * L::kA);
-#pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    const uint32_t bb = smem_u32(sB + (s * NB + b) * L::kB);
+                for (int b = 0; b < groups; ++b) {
+                    const uint32_t bb = smem_u32(sB + s * b_bytes + b * 2 * L::kChunk);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        umma_bf16_ss(d, AMN ? make_sw128_desc(a + k * 2048, 8192, 1024) : make_sw128_desc(a + k * 32, 16, 1024),
-                                     BMN ? make_sw128_desc(bb + k * 2048, 8192, 1024) : make_sw128_desc(bb + k * 32, 16, 1024),
-                                     idesc, (it % kSeg > 0 || b > 0 || k > 0) ? 1u : 0u);
+                        umma_bf16_ss(d, make_sw128_desc(a + k * a_step, a_lbo, 1024),
+                                     make_sw128_desc(bb + k * b_step, b_lbo, 1024), idesc,
+                                     (in_seg > 0 || b > 0 || k > 0) ? 1u : 0u);
                 }
                 umma_commit(&empty[s]);
-                if (it % kSeg == kSeg - 1 || it == n_iters - 1) umma_commit(&accf[seg & 1]);
+                if (++in_seg == seg_len || it == n_iters - 1) {
+                    umma_commit(&accf[seg % NA]);
+                    in_seg = 0;
+                    ++seg;
+                }
+                if (++s == S) s = 0, ph ^= 1;
             }
         }
     } else {
-        const int q = warp & 3, half = (warp - 2) >> 2;      // lane quarter, half of the columns
-        constexpr int kHalf = RPT / 2;
-        float acc[kHalf];
-#pragma unroll
-        for (int j = 0; j < kHalf; ++j) acc[j] = 0.f;
         bool ok = true;
         auto drain = [&](int seg) {
-            ok = mbar_wait_warp(&accf[seg & 1], (seg >> 1) & 1, abort, args.wait_ns);
+            ok = mbar_wait_warp(&accf[seg % NA], (seg / NA) & 1, abort, args.wait_ns);
             if (!ok) return;
             tc_fence_after();
-            const uint32_t t = tmem + (static_cast<uint32_t>(q * 32) << 16) + (seg & 1) * RPT + half * kHalf;
+            const uint32_t t = tmem + (static_cast<uint32_t>(q * 32) << 16) + (seg % NA) * acc_cols + half * kHalf;
 #pragma unroll
             for (int c = 0; c < kHalf; c += 32)
-                if (half * kHalf + c < args.N) {
-                    uint32_t r[32];
-                    tmem_ld_32x32b_x32(t + c, r);
-                    tmem_ld_wait();
+                if (half * kHalf + c < job.N) {
+                    // the smallest terms first (columns past a group are the next one's: never used)
+                    for (int k = terms - 1; k >= 0; --k) {
+                        uint32_t r[32];
+                        tmem_ld_32x32b_x32(t + c + k * tr.stride, r);
+                        tmem_ld_wait();
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) acc[c + j] += __uint_as_float(r[j]);
+                        for (int j = 0; j < 32; ++j) acc[c + j] += __uint_as_float(r[j]);
+                    }
                 }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&acc_free[seg & 1]);
+            if (lane == 0) mbar_arrive(&acc_free[seg % NA]);
         };
-        const int td = threadIdx.x - 64;                      // 0..255: the int8 block of this thread
-        const int row = AMN ? td >> 2 : td >> 1;              // row of the int8 tile
-        const int blk_in = AMN ? td & 3 : td & 1;             // block within the row
-        auto scale_at = [&](int it) -> uint32_t {
-            const int64_t kx = static_cast<int64_t>(k_begin + it) * 64;
-            const int64_t srow = AMN ? kx + row : m0 + row;
-            const int64_t blk = (AMN ? m0 / 32 : kx / 32) + blk_in;
-            const int64_t rows = AMN ? args.K : args.M;
-            if (it >= n_iters || srow >= rows || blk >= args.ld_scales) return 0u;
-            return __ldg(args.scales + srow * args.ld_scales + blk);
-        };
-        uint32_t e_nxt = INT8 ? scale_at(0) : 0u;
-        for (int seg = 0; ok && seg < n_seg; ++seg) {
-            if (INT8) {
-                for (int it = seg * kSeg; it < min(n_iters, (seg + 1) * kSeg); ++it) {
-                    const int s = it % S;
-                    const uint32_t e = e_nxt;
-                    e_nxt = scale_at(it + 1);
-                    ok = mbar_wait_warp(&full[s], (it / S) & 1, abort, args.wait_ns);
+        if (int8) {
+            const int td = threadIdx.x - 64;                      // 0..255: the int8 block of this thread
+            const int row = amn ? td >> 2 : td >> 1;              // row of the int8 tile
+            const int blk_in = amn ? td & 3 : td & 1;             // block within the row
+            auto scale_at = [&](int it) -> uint32_t {
+                const int64_t kx = static_cast<int64_t>(k_begin + it) * 64;
+                const int64_t srow = amn ? kx + row : m0 + row;
+                const int64_t blk = (amn ? m0 / 32 : kx / 32) + blk_in;
+                const int64_t rows = amn ? job.K : job.M;
+                if (it >= n_iters || srow >= rows || blk >= job.ld_scales) return 0u;
+                return __ldg(job.scales + srow * job.ld_scales + blk);
+            };
+            const int dst_off = amn ? (blk_in >> 1) * 8192 + row * 128 : row * 128;
+            const int c0 = amn ? (blk_in & 1) * 4 : blk_in * 4, sw = row & 7;
+            // four steps' scales are in flight (a load takes longer than a step)
+            uint32_t e[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) e[u] = scale_at(u);
+            int drained = 0;
+            for (int it0 = 0, s = 0, ph = 0; ok && it0 < n_iters; it0 += 4) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    if (!ok || it0 + u >= n_iters) break;
+                    const float st = act8_step(e[u]);
+                    e[u] = scale_at(it0 + u + 4);
+                    ok = mbar_wait_warp(&full[s], ph, abort, args.wait_ns);
                     if (!ok) break;
                     // (elements outside the matrix were filled with 0 by the copy)
                     const uint4* src = reinterpret_cast<const uint4*>(sR + s * L::kRaw + td * 32);
                     const uint4 v0 = src[0], v1 = src[1];
-                    const float st = act8_step(e);
-                    uint8_t* dst = sA + s * L::kA + (AMN ? (blk_in >> 1) * 8192 + row * 128 : row * 128);
-                    const int c0 = AMN ? (blk_in & 1) * 4 : blk_in * 4, sw = row & 7;
+                    uint8_t* dst = sA + s * L::kA + dst_off;
                     *reinterpret_cast<uint4*>(dst + (((c0 + 0) ^ sw) << 4)) = act8_decode8(v0.x, v0.y, st);
                     *reinterpret_cast<uint4*>(dst + (((c0 + 1) ^ sw) << 4)) = act8_decode8(v0.z, v0.w, st);
                     *reinterpret_cast<uint4*>(dst + (((c0 + 2) ^ sw) << 4)) = act8_decode8(v1.x, v1.y, st);
@@ -330,89 +408,157 @@ __global__ void __launch_bounds__(320, 1)
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&decoded[s]);
+                    if (++s == S) s = 0, ph ^= 1;
                 }
+                // one or two segments behind the decode, so that a drain does not wait for MMAs in flight
+                // and the segments of the next round find their accumulator tiles free
+                for (const int end = (it0 + 4) / seg_len - NA / 2; ok && drained < end && drained < n_seg;) drain(drained++);
             }
-            // one segment behind the decode, so that the MMAs of this one run meanwhile
-            if (ok && seg >= 1) drain(seg - 1);
+            while (ok && drained < n_seg) drain(drained++);
+        } else {
+            for (int g = 0; ok && g < n_seg; ++g) drain(g);
         }
-        if (ok && n_seg > 0) drain(n_seg - 1);
         if (!ok) fail();
-        const int64_t grow = static_cast<int64_t>(m0) + q * 32 + lane;
-        if (ok && grow < args.M) {
-            const int c0 = half * kHalf;
-            if (args.transposed) {
-                float* out = args.part + static_cast<int64_t>(z) * args.N * args.M + grow;
-#pragma unroll
-                for (int j = 0; j < kHalf; ++j)
-                    if (c0 + j < args.N) out[static_cast<int64_t>(c0 + j) * args.M] = acc[j];
-            } else {
-                // rows of ldp floats (a multiple of 4): 16-byte stores up to the rank
-                float* out = args.part + (static_cast<int64_t>(z) * args.M + grow) * args.ldp + c0;
-#pragma unroll
-                for (int j = 0; j < kHalf; j += 4)
-                    if (c0 + j < args.N)
-                        *reinterpret_cast<float4*>(out + j) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
-            }
-        }
     }
     __syncwarp();
+
+    // ------------------------------------------------------------ join the ranks, write
+    // The ring becomes red[source rank][row of this rank's share][kLdRed]: every MMA of every rank is
+    // done before a rank writes into another's.
+    const int R = 128 / C;
+    if (C > 1) cluster_barrier();
+    else __syncthreads();
+    const bool dead = *abort != 0;
+    if (warp >= 2 && !dead) {
+        const int row = q * 32 + lane;
+        const uint32_t dst = mapa_shared(smem_u32(smem), static_cast<uint32_t>(C > 1 ? row / R : 0)) +
+                             static_cast<uint32_t>(((rank * R + row % R) * L::kLdRed + half * kHalf) * 4);
+#pragma unroll
+        for (int j = 0; j < kHalf; j += 4)
+            if (half * kHalf + j < job.N)
+                asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(dst + j * 4), "f"(acc[j]),
+                             "f"(acc[j + 1]), "f"(acc[j + 2]), "f"(acc[j + 3])
+                             : "memory");
+    }
+    if (C > 1) cluster_barrier();
+    else __syncthreads();
+    if (warp >= 2 && !dead) {
+        const float* red = reinterpret_cast<const float*>(smem);
+        const int row0 = m0 + rank * R;
+        const int rows = min(R, job.M - row0);
+        const int N = job.N;
+        auto total = [&](int rl, int j) {
+            float v = 0.f;
+            for (int c = 0; c < C; ++c) v += red[(c * R + rl) * L::kLdRed + j];
+            return job.scale * v;
+        };
+        const int td = threadIdx.x - 64;
+        if (job.mode == kActTriple) {
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(job.out) + static_cast<int64_t>(row0) * tr.ld;
+            for (int i = td; i < rows * tr.stride; i += 256) {
+                const int rl = i / tr.stride, j = i % tr.stride;
+                float v = j < N ? total(rl, j) : 0.f;
+#pragma unroll
+                for (int k = 0; k < 3; ++k) {
+                    const __nv_bfloat16 h = __float2bfloat16_rn(v);
+                    out[rl * tr.ld + k * tr.stride + j] = h;
+                    // an infinite or NaN v is carried by the first alone (inf - inf would make it NaN)
+                    const float rest = v - __bfloat162float(h);
+                    v = fabsf(rest) < __int_as_float(0x7F800000) ? rest : 0.f;
+                }
+            }
+        } else if (job.mode == kActCols) {
+            float* out = static_cast<float*>(job.out);
+            for (int i = td; i < R * N; i += 256) {
+                const int j = i / R, rl = i % R;
+                if (rl >= rows) continue;
+                float* o = out + static_cast<int64_t>(j) * job.M + row0 + rl;
+                *o = job.accumulate ? *o + total(rl, j) : total(rl, j);
+            }
+        } else {
+            float* out = static_cast<float*>(job.out) + static_cast<int64_t>(row0) * N;
+            for (int i = td; i < rows * N; i += 256)
+                out[i] = job.accumulate ? out[i] + total(i / N, i % N) : total(i / N, i % N);
+        }
+    }
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, 2 * RPT);
+        tmem_dealloc(tmem, 512);
     }
 }
 
-// Sum split-K partials P[z][t][j] (row stride ld) in z order; v = scale sum is written as the three bf16
-// numbers out[0] + out[1] + out[2] = v (8 significant bits each), matrices [T, ld], columns
-// j >= r zero.  An infinite or NaN v is carried by the first alone (inf - inf would make it NaN).
-__global__ void __launch_bounds__(256) k_finalize_triple(const float* __restrict__ P, int split, int64_t T, int r,
-                                                         int ld, float scale, __nv_bfloat16* __restrict__ out) {
-    griddep_enter();
-    const int64_t n = T * ld;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
-         i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-        const int j = static_cast<int>(i % ld);
-        float acc = 0.f;
-        if (j < r)
-            for (int z = 0; z < split; ++z) acc += P[z * n + i];
-        float v = scale * acc;
+// Everything a backward has to lay out before its products, in one launch: the weight decoded to bf16
+// (MXFP4 or NF4, eight elements per thread), and copies of matrices whose rows are no whole 16-byte
+// units to zero-padded rows (dH, B, a given U); the last CTA clears the ticket counters.  Each part
+// has its own range of CTAs.
+struct BwdPrepArgs {
+    const uint8_t* codes;
+    const uint8_t* mx_scales;     // MXFP4 weight, or
+    const uint8_t* absmax_q;      // NF4 weight
+    const float* c2;
+    int64_t n8, col_tiles;        // weight elements / 8
+    uint32_t per_row;             // d_in / 8
+    __nv_bfloat16* w;
+    int ctas_w;
+    struct Pad {
+        const __nv_bfloat16* src;
+        __nv_bfloat16* dst;
+        int64_t rows;
+        int cols, ld, ctas;
+    } pad[3];
+    int* zero;
+    int n_zero;
+};
+constexpr int kPrepUnroll = 4;
+__global__ void __launch_bounds__(256) k_bwd_prepare(const __grid_constant__ BwdPrepArgs a) {
+    griddep_launch_dependents();
+    int b = blockIdx.x;
+    if (b < a.ctas_w) {
+        const int64_t i0 = static_cast<int64_t>(b) * (256 * kPrepUnroll) + threadIdx.x;
+        uint32_t q[kPrepUnroll], e[kPrepUnroll];
+        float c[kPrepUnroll];
 #pragma unroll
-        for (int k = 0; k < 3; ++k) {
-            const __nv_bfloat16 h = __float2bfloat16_rn(v);
-            out[k * n + i] = h;
-            const float rest = v - __bfloat162float(h);
-            v = fabsf(rest) < __int_as_float(0x7F800000) ? rest : 0.f;
+        for (int u = 0; u < kPrepUnroll; ++u) {
+            const int64_t i = i0 + u * 256;
+            if (i < a.n8) {
+                q[u] = __ldg(reinterpret_cast<const uint32_t*>(a.codes) + i);
+                if (a.mx_scales) {
+                    const int64_t row = a.n8 >> 32 ? i / a.per_row : static_cast<uint32_t>(i) / a.per_row;
+                    e[u] = __ldg(a.mx_scales + mx_scale_offset(row, (i - row * a.per_row) >> 2, a.col_tiles));
+                } else {
+                    e[u] = __ldg(a.absmax_q + (i >> 3));
+                    c[u] = __ldg(a.c2 + (i >> 3) / kGroup);
+                }
+            }
         }
+#pragma unroll
+        for (int u = 0; u < kPrepUnroll; ++u) {
+            const int64_t i = i0 + u * 256;
+            if (i < a.n8)
+                reinterpret_cast<uint4*>(a.w)[i] = a.mx_scales
+                                                       ? e2m1_scale8_bf16(q[u], e8m0_value(e[u]))
+                                                       : nf4_decode8(q[u], nf4_make_planes(nf4_block_scale(e[u], c[u])));
+        }
+        return;
     }
-}
-
-// out[i] = scale sum_z P[z][i] over n elements (partials of out's own layout), or added to out.
-__global__ void __launch_bounds__(256) k_finalize_flat(const float* __restrict__ P, int split, int64_t n,
-                                                       float scale, float* __restrict__ out, int accumulate) {
-    griddep_enter();
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
-         i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-        float acc = 0.f;
-        for (int z = 0; z < split; ++z) acc += P[z * n + i];
-        out[i] = accumulate ? out[i] + scale * acc : scale * acc;
+    b -= a.ctas_w;
+#pragma unroll
+    for (int p = 0; p < 3; ++p) {
+        if (b >= 0 && b < a.pad[p].ctas) {
+            const int64_t n = a.pad[p].rows * a.pad[p].ld;
+            for (int64_t i = static_cast<int64_t>(b) * 256 + threadIdx.x; i < n;
+                 i += static_cast<int64_t>(a.pad[p].ctas) * 256) {
+                const int64_t row = i / a.pad[p].ld;
+                const int col = static_cast<int>(i - row * a.pad[p].ld);
+                a.pad[p].dst[i] = col < a.pad[p].cols ? a.pad[p].src[row * a.pad[p].cols + col] : __float2bfloat16_rn(0.f);
+            }
+        }
+        b -= a.pad[p].ctas;
     }
-}
-
-// out[m, j] = scale sum_z P[z][m][j] (row stride ldp), j < r, or added to out.
-__global__ void __launch_bounds__(256) k_finalize_strided(const float* __restrict__ P, int split, int64_t M, int r,
-                                                          int ldp, float scale, float* __restrict__ out,
-                                                          int accumulate) {
-    griddep_enter();
-    const int64_t n = M * r, stride = M * ldp;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
-         i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-        const int64_t m = i / r;
-        float acc = 0.f;
-        for (int z = 0; z < split; ++z) acc += P[z * stride + m * ldp + (i - m * r)];
-        out[i] = accumulate ? out[i] + scale * acc : scale * acc;
-    }
+    if (b == 0)
+        for (int i = threadIdx.x; i < a.n_zero; i += 256) a.zero[i] = 0;
 }
 
 }  // namespace qlora

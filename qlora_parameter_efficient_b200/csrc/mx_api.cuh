@@ -12,7 +12,7 @@ constexpr int64_t kMxStreamMaxT = 512;
 
 qlora_status mx_check_dims(int64_t rows, int64_t cols) {
     if (rows < 1 || rows > kMaxDim || cols < 64 || cols % 64 || cols > kMaxDim) return QLORA_ERR_UNSUPPORTED;
-    if (cdiv(rows, 128) * mx_col_tiles(cols) > 0x7FFFFFFFLL) return QLORA_ERR_UNSUPPORTED;
+    if (cdiv(rows, 128) * mx_col_tiles(cols) > (1LL << 28)) return QLORA_ERR_UNSUPPORTED;   // grids
     return QLORA_OK;
 }
 inline size_t mx_scale_bytes(int64_t rows, int64_t cols) {
@@ -22,6 +22,10 @@ qlora_status check_mxfp4(const qlora_mxfp4* w) {
     if (!w || !aligned16(w->codes) || !aligned16(w->scales)) return QLORA_ERR_INVALID_ARG;
     return mx_check_dims(w->d_out, w->d_in);
 }
+
+// CTAs of the stand-alone format kernels: 256 threads, four steps of 8 elements each.
+static_assert(kMxUnroll == 4 && kAct8Unroll == 4, "mx_ctas");
+unsigned mx_ctas(int64_t n8) { return static_cast<unsigned>(cdiv(n8, 1024)); }
 
 // Routes of the MXFP4 forward by the number of tokens.
 enum MxRoute { kMxDecode, kMxStream64, kMxStream128, kMxPair };
@@ -95,16 +99,10 @@ MxFwdPlan mx_fwd_plan(int64_t T, int64_t d_out, int64_t d_in, int r) {
 
 // The backward of an MXFP4 or NF4 base from a bf16 activation or an 8-bit checkpoint.
 struct MxBwdPlan {
-    int RP = 0, split_u = 1, split_g = 1, split_da = 1, split_db = 1;
-    size_t b_pad = 0, dh_pad = 0, u3 = 0, g3 = 0, part = 0, w = 0, pair = 0, total = 0;
+    int RP = 0;
+    size_t b_pad = 0, dh_pad = 0, u3 = 0, g3 = 0, w = 0, pair = 0, total = 0;
     PairSched sched;
 };
-// k_act_gemm runs one CTA per SM: one wave of them.
-int act_split(int64_t tiles, int64_t k_steps) {
-    int64_t s = std::max<int64_t>(1, kSmsForSplit / tiles);
-    s = std::min<int64_t>(s, std::max<int64_t>(1, k_steps / 4));
-    return static_cast<int>(cdiv(k_steps, cdiv(k_steps, s)));
-}
 MxBwdPlan mx_bwd_plan(int64_t T, int64_t d_out, int64_t d_in, int r) {
     MxBwdPlan p;
     size_t off = 0;
@@ -117,16 +115,9 @@ MxBwdPlan mx_bwd_plan(int64_t T, int64_t d_out, int64_t d_in, int r) {
     const size_t rp = static_cast<size_t>(p.RP), row = static_cast<size_t>(T) * rp;
     if (r % 8) p.b_pad = take(static_cast<size_t>(d_out) * rp * 2);
     if (d_out % 8) p.dh_pad = take(static_cast<size_t>(T) * ((d_out + 7) / 8 * 8) * 2);
-    p.u3 = take(3 * row * 2);      // U and s G as three bf16 matrices each
-    p.g3 = take(3 * row * 2);
-    p.split_u = act_split(cdiv(T, 128), cdiv(d_in, 64));
-    p.split_g = act_split(cdiv(T, 128), cdiv(d_out, 64));
-    p.split_da = act_split(cdiv(d_in, 128), cdiv(T, 64));
-    p.split_db = act_split(cdiv(d_out, 128), cdiv(T, 64));
-    size_t part = static_cast<size_t>(std::max(p.split_u, p.split_g)) * row * 4;
-    part = std::max(part, static_cast<size_t>(p.split_da) * d_in * r * 4);
-    part = std::max(part, static_cast<size_t>(p.split_db) * d_out * rp * 4);
-    p.part = take(part);
+    const size_t triple = static_cast<size_t>(T) * act_triple(r).ld * 2;
+    p.u3 = take(std::max(triple, row * 2));   // U and s G, three bf16 terms each
+    p.g3 = take(triple);
     p.w = take(static_cast<size_t>(d_out) * d_in * 2);      // the decoded weight
     p.sched = pair_schedule(T, d_in, cdiv(d_out, 64), 8);
     p.pair = take(p.sched.bytes());
@@ -185,37 +176,71 @@ qlora_status launch_mx_stream(const CUtensorMap& tw, const CUtensorMap& tx, cons
     return QLORA_OK;
 }
 
-// bf16 [nb][rows, cols] with row stride ld and matrix stride rows * ld, 128-byte swizzle, boxes of 64
-// columns x box_rows; rows and columns outside a matrix are filled with 0 (cols need not be whole
-// 16-byte units, ld does).
-qlora_status tmap_bf16_3d(CUtensorMap* m, const void* base, int nb, int64_t rows, int64_t cols, int64_t ld,
-                          uint32_t box_rows) {
-    QL_TRY(get_encoder());
-    cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(nb)};
-    cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld * 2), static_cast<cuuint64_t>(rows * ld * 2)};
-    cuuint32_t box[3] = {64, box_rows, 1};
-    cuuint32_t es[3] = {1, 1, 1};
-    CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? QLORA_OK : QLORA_ERR_CUDA;
-}
-
-template <bool INT8, bool AMN, bool BMN, int RPT, int NB>
-qlora_status launch_act_gemm(const CUtensorMap& ta, const CUtensorMap& tb, const ActGemmArgs& g, cudaStream_t st) {
-    using L = ActGemmSmem<INT8, RPT, NB>;
-    auto kern = k_act_gemm<INT8, AMN, BMN, RPT, NB>;
+// One launch of one or two adapter products.  The cluster size (K ranks) is the one with the shortest
+// schedule on 148 SMs, one CTA each: waves x (K steps of a rank + what a CTA costs besides, about
+// six K steps).
+struct ActLaunch {
+    ActGemmArgs g{};
+    CUtensorMap a[2], b[2];
+    int n = 0;
+    ActJob& add(int64_t M, int N, int64_t K) {
+        ActJob& j = g.job[n++];
+        j.M = static_cast<int>(M);
+        j.N = N;
+        j.K = K;
+        j.k_steps = static_cast<int>(cdiv(K, 64));
+        j.scale = 1.f;
+        return j;
+    }
+};
+template <int RPT>
+qlora_status launch_act_gemm(ActLaunch& l, int* err, cudaStream_t st) {
+    using L = ActGemmSmem<RPT>;
+    auto kern = k_act_gemm<RPT>;
     static std::atomic<uint64_t> configured{0};
     QL_TRY(allow_smem(kern, L::kTotal, configured));
-    const dim3 grid(static_cast<unsigned>(cdiv(g.M, 128)), static_cast<unsigned>(g.split));
-    if (launch_pdl(kern, grid, dim3(320), L::kTotal, st, ta, tb, g) != cudaSuccess) return QLORA_ERR_CUDA;
+    if (l.n == 1) {
+        l.a[1] = l.a[0];
+        l.b[1] = l.b[0];
+    }
+    int64_t tiles = 0;
+    int steps = 1 << 30, most = 0;
+    for (int i = 0; i < l.n; ++i) {
+        tiles += cdiv(l.g.job[i].M, 128);
+        steps = std::min(steps, l.g.job[i].k_steps);
+        most = std::max(most, l.g.job[i].k_steps);
+    }
+    int64_t best = 0;
+    for (int c = 1; c <= 8 && c <= steps; c *= 2) {
+        const int64_t cost = cdiv(tiles * c, kSmsForSplit) * (cdiv(most, c) + 6);
+        if (c == 1 || cost < best) {
+            best = cost;
+            l.g.ranks = c;
+        }
+    }
+    l.g.tiles0 = static_cast<int>(cdiv(l.g.job[0].M, 128));
+    l.g.err = err;
+    l.g.wait_ns = kWaitNs;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(l.g.ranks);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles * l.g.ranks));
+    cfg.blockDim = dim3(320);
+    cfg.dynamicSmemBytes = L::kTotal;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = l.g.ranks > 1 ? 2 : 1;
+    if (cudaLaunchKernelEx(&cfg, kern, l.a[0], l.b[0], l.a[1], l.b[1], l.g) != cudaSuccess) return QLORA_ERR_CUDA;
     QL_LAUNCH_CHECK();
     return QLORA_OK;
 }
-template <bool INT8, bool AMN, bool BMN, int NB>
-qlora_status act_gemm(int RP, const CUtensorMap& ta, const CUtensorMap& tb, const ActGemmArgs& g, cudaStream_t st) {
-    return RP == 64 ? launch_act_gemm<INT8, AMN, BMN, 64, NB>(ta, tb, g, st)
-                    : launch_act_gemm<INT8, AMN, BMN, 128, NB>(ta, tb, g, st);
+qlora_status act_gemm(int RP, ActLaunch& l, int* err, cudaStream_t st) {
+    return RP == 64 ? launch_act_gemm<64>(l, err, st) : launch_act_gemm<128>(l, err, st);
 }
 
 template <bool MX>
@@ -257,7 +282,7 @@ qlora_status dx_gemm(const void* W, const void* dH, int64_t dh_ld, int64_t T, in
     CUtensorMap t[6];
     QL_TRY(tmap_bf16(&t[0], dH, T, d_out, dh_ld, 128));
     QL_TRY(tmap_bf16(&t[1], W, d_out, d_in, d_in, 64));
-    QL_TRY(tmap_bf16(&t[4], sG, T, r, RP, 128));
+    QL_TRY(tmap_bf16(&t[4], sG, T, r, act_triple(r).ld, 128));
     QL_TRY(tmap_bf16(&t[5], A, r, d_in, d_in, 64));
     t[2] = t[3] = t[0];
     PairGemmArgs g{};
@@ -383,127 +408,121 @@ qlora_status mx_bwd(MxBase base, const void* X, const qlora_act8* X8, const void
     const int64_t d_in = base.mx ? base.mx->d_in : base.nf4->d_in;
     const MxBwdPlan p = mx_bwd_plan(T, d_out, d_in, r);
     const int RP = p.RP;
-    auto* part = at<float>(ws, p.part);
     auto* u3 = at<bf>(ws, p.u3);
     auto* g3 = at<bf>(ws, p.g3);
-    int64_t dh_ld = d_out;
-    if (d_out % 8) {          // rows that are no whole 16-byte units cannot be read by a tensor map
-        dh_ld = (d_out + 7) / 8 * 8;
-        QL_TRY(pad_bf16(static_cast<const bf*>(dH), T, d_out, d_out, at<bf>(ws, p.dh_pad), T, dh_ld, 0, dh_ld, st));
-        dH = at<void>(ws, p.dh_pad);
-    }
-    auto triple = [&](int split, float scale, bf* out) -> qlora_status {
-        if (launch_pdl(k_finalize_triple, grid1d(T * RP), dim3(256), 0, st, part, split, T, r, RP, scale, out) !=
-            cudaSuccess)
-            return QLORA_ERR_CUDA;
-        QL_LAUNCH_CHECK();
-        return QLORA_OK;
-    };
-    ActGemmArgs g{};
-    g.N = r;
-    g.err = err;
-    g.wait_ns = kWaitNs;
-    g.part = part;
-    g.ldp = RP;
-    if (X8) {
-        g.scales = X8->scales;
-        g.ld_scales = d_in / 32;
-    }
-    CUtensorMap ta, tb;
-    int u_nb = 3, u_ld = RP;      // the matrices that make up U
-    const void* u_src = u3;
-    if (phase != kBwdDx) {
-        // U = X~ A^T, unless the forward kept it
-        if (U_saved) {
-            u_nb = 1;
-            if (r % 8 == 0) {
-                u_src = U_saved;
-                u_ld = r;
+    auto* W = at<bf>(ws, p.w);
+    const bool grads = phase != kBwdDx, want_dx = dX && phase != kBwdGrads;
+    const int64_t dh_ld = (d_out + 7) / 8 * 8;
+    const void* b_src = B;
+    const void* u_src = U_saved ? U_saved : u3;
+    const ActTriple tr = act_triple(r);
+    int b_ld = r, u_ld = U_saved ? r : tr.ld;
+    // The first kernel is launched without programmatic dependent launch, so that whatever used the
+    // workspace before has ended.
+    {
+        BwdPrepArgs a{};
+        if (want_dx) {
+            a.codes = base.mx ? base.mx->codes : base.nf4->codes;
+            if (base.mx) {
+                a.mx_scales = base.mx->scales;
             } else {
-                QL_TRY(pad_bf16(static_cast<const bf*>(U_saved), T, r, r, u3, T, RP, 0, RP, st));
+                a.absmax_q = base.nf4->absmax_q;
+                a.c2 = base.nf4->c2;
             }
-        } else {
-            QL_TRY(tmap_bf16_3d(&tb, A, 1, r, d_in, d_in, static_cast<uint32_t>(RP)));
-            g.M = static_cast<int>(T);
-            g.K = d_in;
-            g.k_steps = static_cast<int>(d_in / 64);
-            g.split = p.split_u;
-            if (X8) {
-                QL_TRY(tmap_u8(&ta, X8->q, T, d_in, d_in, 64, 128));
-                QL_TRY((act_gemm<true, false, false, 1>(RP, ta, tb, g, st)));
-            } else {
-                QL_TRY(tmap_bf16(&ta, X, T, d_in, d_in, 128));
-                QL_TRY((act_gemm<false, false, false, 1>(RP, ta, tb, g, st)));
-            }
-            QL_TRY(triple(p.split_u, 1.f, u3));
+            a.n8 = d_out * d_in / 8;
+            a.col_tiles = mx_col_tiles(d_in);
+            a.per_row = static_cast<uint32_t>(d_in / 8);
+            a.w = W;
+            a.ctas_w = static_cast<int>(cdiv(a.n8, 256 * kPrepUnroll));
+            a.zero = at<int>(ws, p.pair + p.sched.part_bytes);
+            a.n_zero = p.sched.n_cnt;
         }
-        // s G = s dH B
-        const void* b_src = B;
-        int b_ld = r;
-        if (r % 8) {
-            QL_TRY(pad_bf16(static_cast<const bf*>(B), d_out, r, r, at<bf>(ws, p.b_pad), d_out, RP, 0, RP, st));
+        auto pad = [&](int i, const void* src, void* dst, int64_t rows, int64_t cols, int64_t ld) {
+            a.pad[i].src = static_cast<const bf*>(src);
+            a.pad[i].dst = static_cast<bf*>(dst);
+            a.pad[i].rows = rows;
+            a.pad[i].cols = static_cast<int>(cols);
+            a.pad[i].ld = static_cast<int>(ld);
+            a.pad[i].ctas = static_cast<int>(std::min<int64_t>(cdiv(rows * ld, 1024), 4 * kSmsForSplit));
+        };
+        // rows that are no whole 16-byte units cannot be read by a tensor map
+        if (d_out % 8) {
+            pad(0, dH, at<void>(ws, p.dh_pad), T, d_out, dh_ld);
+            dH = at<void>(ws, p.dh_pad);
+        }
+        if (r % 8 && grads) {
+            pad(1, B, at<void>(ws, p.b_pad), d_out, r, RP);
             b_src = at<void>(ws, p.b_pad);
             b_ld = RP;
+            if (U_saved) {
+                pad(2, U_saved, u3, T, r, RP);
+                u_src = u3;
+                u_ld = RP;
+            }
         }
-        QL_TRY(tmap_bf16(&ta, dH, T, d_out, dh_ld, 128));
-        QL_TRY(tmap_bf16_3d(&tb, b_src, 1, d_out, r, b_ld, 64));
-        g.M = static_cast<int>(T);
-        g.K = d_out;
-        g.k_steps = static_cast<int>(cdiv(d_out, 64));
-        g.split = p.split_g;
-        QL_TRY((act_gemm<false, false, true, 1>(RP, ta, tb, g, st)));
-        QL_TRY(triple(p.split_g, s, g3));
+        const int ctas = a.ctas_w + a.pad[0].ctas + a.pad[1].ctas + a.pad[2].ctas + (a.n_zero ? 1 : 0);
+        if (ctas) {
+            k_bwd_prepare<<<ctas, 256, 0, st>>>(a);
+            QL_LAUNCH_CHECK();
+        }
     }
-    // dX = dH W + (sG) A; the adapter term's s G is rounded to bf16 (2^-9 of that term, as dX itself is)
-    if (dX && phase != kBwdGrads) {
-        auto* W = at<bf>(ws, p.w);
-        int* zero = at<int>(ws, p.pair + p.sched.part_bytes);
-        const int64_t n = d_out * d_in;
-        if (base.mx) {
-            if (launch_pdl(k_mxfp4_dequant<bf>, grid1d(n / 8), dim3(256), 0, st, base.mx->codes, base.mx->scales, d_out,
-                           d_in, W, zero, p.sched.n_cnt) != cudaSuccess)
-                return QLORA_ERR_CUDA;
+    if (grads) {
+        // s G = s dH B, and U = X~ A^T unless the forward kept it
+        ActLaunch l;
+        ActJob& jg = l.add(T, r, d_out);
+        jg.bmn = 1;
+        jg.mode = kActTriple;
+        jg.scale = s;
+        jg.out = g3;
+        QL_TRY(tmap_bf16(&l.a[0], dH, T, d_out, dh_ld, 128));
+        QL_TRY(tmap_bf16(&l.b[0], b_src, d_out, r, b_ld, 64));
+        if (!U_saved) {
+            ActJob& ju = l.add(T, r, d_in);
+            ju.mode = kActTriple;
+            ju.out = u3;
+            if (X8) {
+                ju.int8 = 1;
+                ju.scales = X8->scales;
+                ju.ld_scales = d_in / 32;
+                QL_TRY(tmap_u8(&l.a[1], X8->q, T, d_in, d_in, 64, 128));
+            } else {
+                QL_TRY(tmap_bf16(&l.a[1], X, T, d_in, d_in, 128));
+            }
+            QL_TRY(tmap_bf16(&l.b[1], A, r, d_in, d_in, static_cast<uint32_t>(RP)));
+        }
+        QL_TRY(act_gemm(RP, l, err, st));
+    }
+    // dX = dH W + (sG) A; the adapter term's s G is rounded to bf16 (2^-8 of that term, as dX itself is)
+    if (want_dx) QL_TRY(dx_gemm(W, dH, dh_ld, T, d_out, d_in, g3, A, RP, r, dX, p.sched, at<void>(ws, p.pair), err, st));
+    if (grads) {
+        // dA^T[d_in, r] = X~^T (s G) and dB[d_out, r] = s dH^T U
+        ActLaunch l;
+        ActJob& ja = l.add(d_in, r, T);
+        ja.amn = ja.bmn = 1;
+        ja.triple = 1;
+        ja.mode = kActCols;
+        ja.accumulate = acc;
+        ja.out = dA;
+        if (X8) {
+            ja.int8 = 1;
+            ja.scales = X8->scales;
+            ja.ld_scales = d_in / 32;
+            QL_TRY(tmap_u8(&l.a[0], X8->q, T, d_in, d_in, 128, 64));
         } else {
-            if (p.sched.n_cnt &&
-                cudaMemsetAsync(zero, 0, static_cast<size_t>(p.sched.n_cnt) * sizeof(int), st) != cudaSuccess)
-                return QLORA_ERR_CUDA;
-            k_nf4_dequant_bf16<<<static_cast<unsigned>(cdiv(n / 64, 256)), 256, 0, st>>>(
-                base.nf4->codes, base.nf4->absmax_q, base.nf4->c2, n / 64, W);
+            QL_TRY(tmap_bf16(&l.a[0], X, T, d_in, d_in, 64));
         }
-        QL_LAUNCH_CHECK();
-        QL_TRY(dx_gemm(W, dH, dh_ld, T, d_out, d_in, g3, A, RP, r, dX, p.sched, at<void>(ws, p.pair), err, st));
+        QL_TRY(tmap_bf16(&l.b[0], g3, T, tr.ld, tr.ld, 64));
+        ActJob& jb = l.add(d_out, r, T);
+        jb.amn = jb.bmn = 1;
+        jb.triple = !U_saved;
+        jb.mode = kActRows;
+        jb.scale = s;
+        jb.accumulate = acc;
+        jb.out = dB;
+        QL_TRY(tmap_bf16(&l.a[1], dH, T, d_out, dh_ld, 64));
+        QL_TRY(tmap_bf16(&l.b[1], u_src, T, U_saved ? r : tr.ld, u_ld, 64));
+        QL_TRY(act_gemm(RP, l, err, st));
     }
-    if (phase == kBwdDx) return QLORA_OK;
-    // dA^T[d_in, r] = X~^T (s G), partials stored as [split][r][d_in]
-    QL_TRY(tmap_bf16_3d(&tb, g3, 3, T, r, RP, 64));
-    g.M = static_cast<int>(d_in);
-    g.K = T;
-    g.k_steps = static_cast<int>(cdiv(T, 64));
-    g.split = p.split_da;
-    g.transposed = 1;
-    if (X8) {
-        QL_TRY(tmap_u8(&ta, X8->q, T, d_in, d_in, 128, 64));
-        QL_TRY((act_gemm<true, true, true, 3>(RP, ta, tb, g, st)));
-    } else {
-        QL_TRY(tmap_bf16(&ta, X, T, d_in, d_in, 64));
-        QL_TRY((act_gemm<false, true, true, 3>(RP, ta, tb, g, st)));
-    }
-    const int64_t n_da = static_cast<int64_t>(r) * d_in;
-    if (launch_pdl(k_finalize_flat, grid1d(n_da), dim3(256), 0, st, part, p.split_da, n_da, 1.f, dA, acc) != cudaSuccess)
-        return QLORA_ERR_CUDA;
-    QL_LAUNCH_CHECK();
-    // dB[d_out, r] = s dH^T U
-    QL_TRY(tmap_bf16(&ta, dH, T, d_out, dh_ld, 64));
-    QL_TRY(tmap_bf16_3d(&tb, u_src, u_nb, T, r, u_ld, 64));
-    g.M = static_cast<int>(d_out);
-    g.split = p.split_db;
-    g.transposed = 0;
-    if (u_nb == 1) QL_TRY((act_gemm<false, true, true, 1>(RP, ta, tb, g, st)));
-    else QL_TRY((act_gemm<false, true, true, 3>(RP, ta, tb, g, st)));
-    if (launch_pdl(k_finalize_strided, grid1d(d_out * r), dim3(256), 0, st, part, p.split_db, d_out, r, RP, s, dB,
-                   acc) != cudaSuccess)
-        return QLORA_ERR_CUDA;
-    QL_LAUNCH_CHECK();
     return QLORA_OK;
 }
 
@@ -564,13 +583,13 @@ qlora_status mxfp4_quantize(const void* W, qlora_dtype w_dtype, int64_t rows, in
 qlora_status mxfp4_dequantize(const qlora_mxfp4* w, void* W_out, qlora_dtype out_dtype, cudaStream_t stream) {
     if (!aligned16(W_out) || (out_dtype != QLORA_F32 && out_dtype != QLORA_BF16)) return QLORA_ERR_INVALID_ARG;
     QL_TRY(check_mxfp4(w));
-    const dim3 grid = grid1d(w->d_out * w->d_in / 8);
+    const dim3 grid(mx_ctas(w->d_out * w->d_in / 8));
     if (out_dtype == QLORA_F32)
         k_mxfp4_dequant<float><<<grid, 256, 0, stream>>>(w->codes, w->scales, w->d_out, w->d_in,
-                                                         static_cast<float*>(W_out), nullptr, 0);
+                                                         static_cast<float*>(W_out));
     else
         k_mxfp4_dequant<__nv_bfloat16><<<grid, 256, 0, stream>>>(w->codes, w->scales, w->d_out, w->d_in,
-                                                                 static_cast<__nv_bfloat16*>(W_out), nullptr, 0);
+                                                                 static_cast<__nv_bfloat16*>(W_out));
     QL_LAUNCH_CHECK();
     return QLORA_OK;
 }
@@ -610,6 +629,7 @@ qlora_status qlora_linear_bwd_act8(const qlora_nf4* w, const qlora_act8* X8, con
 qlora_status qlora_act8_sizes(int64_t T, int64_t d_in, size_t* q_bytes, size_t* scale_bytes) {
     if (!q_bytes || !scale_bytes) return QLORA_ERR_INVALID_ARG;
     if (T < 1 || T > kMaxDim || d_in < 64 || d_in % 64 || d_in > kMaxDim) return QLORA_ERR_UNSUPPORTED;
+    if (cdiv(T * d_in, 8192) > 0x7FFFFFFFLL) return QLORA_ERR_UNSUPPORTED;                  // grids
     *q_bytes = static_cast<size_t>(T) * d_in;
     *scale_bytes = static_cast<size_t>(T) * d_in / 32;
     return QLORA_OK;
@@ -623,9 +643,9 @@ qlora_status qlora_act8_quantize(const void* X, qlora_dtype x_dtype, int64_t T, 
     QL_TRY(qlora_act8_sizes(T, d_in, &qb, &sb));
     const int64_t n8 = T * d_in / 8;
     if (x_dtype == QLORA_F32)
-        k_act8_quantize<float><<<grid1d(n8), 256, 0, stream>>>(static_cast<const float*>(X), n8, q, scales);
+        k_act8_quantize<float><<<mx_ctas(n8), 256, 0, stream>>>(static_cast<const float*>(X), n8, q, scales);
     else
-        k_act8_quantize<__nv_bfloat16><<<grid1d(n8), 256, 0, stream>>>(static_cast<const __nv_bfloat16*>(X), n8, q,
+        k_act8_quantize<__nv_bfloat16><<<mx_ctas(n8), 256, 0, stream>>>(static_cast<const __nv_bfloat16*>(X), n8, q,
                                                                        scales);
     QL_LAUNCH_CHECK();
     return QLORA_OK;
@@ -639,9 +659,9 @@ qlora_status qlora_act8_dequantize(const qlora_act8* a, int64_t T, int64_t d_in,
     QL_TRY(qlora_act8_sizes(T, d_in, &qb, &sb));
     const int64_t n8 = T * d_in / 8;
     if (out_dtype == QLORA_F32)
-        k_act8_dequant<float><<<grid1d(n8), 256, 0, stream>>>(a->q, a->scales, n8, static_cast<float*>(X_out));
+        k_act8_dequant<float><<<mx_ctas(n8), 256, 0, stream>>>(a->q, a->scales, n8, static_cast<float*>(X_out));
     else
-        k_act8_dequant<__nv_bfloat16><<<grid1d(n8), 256, 0, stream>>>(a->q, a->scales, n8,
+        k_act8_dequant<__nv_bfloat16><<<mx_ctas(n8), 256, 0, stream>>>(a->q, a->scales, n8,
                                                                       static_cast<__nv_bfloat16*>(X_out));
     QL_LAUNCH_CHECK();
     return QLORA_OK;

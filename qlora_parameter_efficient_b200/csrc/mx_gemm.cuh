@@ -626,7 +626,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGemmSmem<MX>::kT
                 const uint32_t d = tmem + static_cast<uint32_t>((u & 1) * L::kAcc1);
                 for (int it = k0; it < k1; ++it, ++git) {
                     const int s = git % S;
-                    ok = mbar_wait_cluster(&full[s], (git / S) & 1, abort, args.wait_ns);
+                    ok = mbar_wait(&full[s], (git / S) & 1, abort, args.wait_ns);
                     // two sets of scale columns in turn: those of stage git - 2 are free once its MMAs are done
                     if (MX && ok && git >= 2)
                         ok = mbar_wait(&empty[(git - 2) % S], ((git - 2) / S) & 1, abort, args.wait_ns);

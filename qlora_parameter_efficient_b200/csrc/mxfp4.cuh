@@ -36,28 +36,47 @@ __device__ __forceinline__ float e8m0_value(uint32_t e) {
     return __uint_as_float(e == 255u ? 0x7FFFFFFFu : (e == 0u ? 0x00400000u : e << 23));
 }
 
-// Eight elements as fp32, and the largest |x| among them as fp32 bits (an integer maximum: NaN and
-// infinity bits order above every finite value).
-__device__ __forceinline__ uint32_t load8(const float* p, float (&x)[8]) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p));
-    const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-    return m;
-}
-__device__ __forceinline__ uint32_t load8(const __nv_bfloat16* p, float (&x)[8]) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-        m = max(m, max((w[i] << 16) & 0x7FFFFFFFu, w[i] & 0x7FFF0000u));
+// Eight consecutive elements as loaded, their values in fp32, and the largest |x| among them as fp32
+// bits (an integer maximum: NaN and infinity bits order above every finite value).
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* p) {
+        a = __ldg(reinterpret_cast<const float4*>(p));
+        b = __ldg(reinterpret_cast<const float4*>(p) + 1);
     }
-    return m;
+    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ uint32_t values(float (&x)[8]) const {
+        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+        return m;
+    }
+};
+template <>
+struct Raw8<__nv_bfloat16> {
+    uint4 v;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = __ldg(reinterpret_cast<const uint4*>(p)); }
+    __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ uint32_t values(float (&x)[8]) const {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+            m = max(m, max((w[i] << 16) & 0x7FFFFFFFu, w[i] & 0x7FFF0000u));
+        }
+        return m;
+    }
+};
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
+    Raw8<__nv_bfloat16> r;
+    r.load(p);
+    r.values(x);
 }
 
 // Maximum over the four lanes that share a block of 32.
@@ -81,40 +100,39 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&x)[8]) {
 }
 
 // One 128 x 128 scale tile of a matrix: 256 threads, sixteen lanes per row (8 elements each, four
-// lanes per block), 8 passes of 16 rows.  The tile's scales are gathered in shared memory
-// and written once, 512 contiguous bytes.
+// lanes per block), 8 passes of 16 rows whose loads are all issued first (4 passes at a time for
+// fp32).  The tile's scales are gathered in shared memory and written once, 512 contiguous bytes.
 template <typename T>
 __device__ __forceinline__ void mxfp4_quantize_tile(const T* __restrict__ X, int64_t rows, int64_t cols,
                                                     int64_t rt, int64_t kt, uint8_t* __restrict__ codes,
                                                     uint8_t* __restrict__ scales, uint8_t* s_sc) {
-    const int seg = threadIdx.x & 15;
+    constexpr int kBatch = sizeof(T) == 4 ? 4 : 8;
+    const int seg = threadIdx.x & 15, r0 = threadIdx.x >> 4;
     const int64_t col = kt * 128 + seg * 8;
-    float x[8][8];
-    uint32_t m[8];
+    const int64_t left = col < cols ? rows - rt * 128 : 0;       // rows of this tile that exist
+    const T* src = X + (rt * 128 + r0) * cols + col;
+    uint8_t* dst = codes + ((rt * 128 + r0) * cols + col) / 2;
 #pragma unroll
-    for (int p = 0; p < 8; ++p) {
-        const int64_t row = rt * 128 + p * 16 + (threadIdx.x >> 4);
-        m[p] = 0;
-        if (row < rows && col < cols) m[p] = load8(X + row * cols + col, x[p]);
-        else
+    for (int p0 = 0; p0 < 8; p0 += kBatch) {
+        Raw8<T> raw[kBatch];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[p][i] = 0.f;
-    }
+        for (int p = 0; p < kBatch; ++p) {
+            if ((p0 + p) * 16 + r0 < left) raw[p].load(src + (p0 + p) * 16 * cols);
+            else raw[p].zero();
+        }
 #pragma unroll
-    for (int p = 0; p < 8; ++p) {
-        const int lr = p * 16 + (threadIdx.x >> 4);
-        const int64_t row = rt * 128 + lr;
-        const uint32_t ef = quad_max(m[p]) >> 23;                // biased exponent of max|x|
-        const uint32_t e = ef == 255u ? 255u : (ef > 2u ? ef - 2u : 0u);
-        // 2^(127 - e); 0 for a NaN block, whose codes are 0
-        const float inv = __uint_as_float(e == 255u ? 0u : (254u - e) << 23);
+        for (int p = 0; p < kBatch; ++p) {
+            const int lr = (p0 + p) * 16 + r0;
+            float x[8];
+            const uint32_t ef = quad_max(raw[p].values(x)) >> 23;     // biased exponent of max|x|
+            const uint32_t e = ef == 255u ? 255u : (ef > 2u ? ef - 2u : 0u);
+            const float inv = __uint_as_float((254u - e) << 23);      // 2^(127 - e)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[p][i] = __fmul_rn(x[p][i], inv);
-        const uint32_t q = e == 255u ? 0u : e2m1x8(x[p]);
-        if (row < rows && col < cols) *reinterpret_cast<uint32_t*>(codes + (row * cols + col) / 2) = q;
-        if ((seg & 3) == 0)
-            s_sc[(lr & 31) * 16 + (lr >> 5) * 4 + (seg >> 2)] =
-                (row < rows && col < cols) ? static_cast<uint8_t>(e) : 0;
+            for (int i = 0; i < 8; ++i) x[i] = __fmul_rn(x[i], inv);
+            const uint32_t q = e == 255u ? 0u : e2m1x8(x);
+            if (lr < left) *reinterpret_cast<uint32_t*>(dst + (p0 + p) * 8 * cols) = q;
+            if ((seg & 3) == 0) s_sc[(lr & 31) * 16 + (lr >> 5) * 4 + (seg >> 2)] = lr < left ? static_cast<uint8_t>(e) : 0;
+        }
     }
     __syncthreads();
     if (threadIdx.x < kMxTileBytes / 16)
@@ -122,7 +140,6 @@ __device__ __forceinline__ void mxfp4_quantize_tile(const T* __restrict__ X, int
             reinterpret_cast<const uint4*>(s_sc)[threadIdx.x];
 }
 
-// grid: one CTA per scale tile, column tiles fastest.
 // zero[0, n_zero): ticket counters of a later kernel of the call, cleared on the way.
 template <typename T>
 __global__ void __launch_bounds__(256) k_mxfp4_quantize(const T* __restrict__ X, int64_t rows, int64_t cols,
@@ -155,38 +172,59 @@ __device__ __forceinline__ uint4 e2m1_decode8_bf16(uint32_t q) {
                       prmt(lo_b, hi_b, 0x7362));
 }
 
-// One thread per 8 elements: 4 code bytes in, 16 (bf16) or 32 (fp32) bytes out.
+// Eight packed codes times the block's scale.  The products are formed in fp32, so that the one rounding
+// to bf16 is that of the exact value.
+__device__ __forceinline__ void e2m1_scale8(uint32_t q, float s, float (&f)[8]) {
+    const uint4 v = e2m1_decode8_bf16(q);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        f[2 * k] = __fmul_rn(__uint_as_float(w[k] << 16), s);
+        f[2 * k + 1] = __fmul_rn(__uint_as_float(w[k] & 0xFFFF0000u), s);
+    }
+}
+__device__ __forceinline__ uint4 e2m1_scale8_bf16(uint32_t q, float s) {
+    float f[8];
+    e2m1_scale8(q, s, f);
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+}
+
+// Eight elements per thread and step: 4 code bytes in, 16 (bf16) or 32 (fp32) bytes out; kMxUnroll
+// steps' loads are issued together.
+constexpr int kMxUnroll = 4;
 template <typename T>
 __global__ void __launch_bounds__(256) k_mxfp4_dequant(const uint8_t* __restrict__ codes,
                                                        const uint8_t* __restrict__ scales, int64_t rows,
-                                                       int64_t cols, T* __restrict__ out, int* __restrict__ zero,
-                                                       int n_zero) {
+                                                       int64_t cols, T* __restrict__ out) {
     griddep_enter();
-    if (blockIdx.x == 0)
-        for (int i = threadIdx.x; i < n_zero; i += 256) zero[i] = 0;
-    const int64_t n8 = rows * cols / 8, per_row = cols / 8, kts = mx_col_tiles(cols);
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n8;
-         i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-        const int64_t row = i / per_row, blk = (i - row * per_row) >> 2;
-        const uint32_t e = __ldg(scales + mx_scale_offset(row, blk, kts));
-        const uint32_t q = __ldg(reinterpret_cast<const uint32_t*>(codes) + i);
-        const uint4 v = e2m1_decode8_bf16(q);
-        // in fp32, so that the one rounding to bf16 is that of the exact value
-        const float s = e8m0_value(e);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        float f[8];
+    const int64_t n8 = rows * cols / 8, kts = mx_col_tiles(cols);
+    const uint32_t per_row = static_cast<uint32_t>(cols / 8);
+    const int64_t i0 = static_cast<int64_t>(blockIdx.x) * (256 * kMxUnroll) + threadIdx.x;
+    uint32_t q[kMxUnroll], e[kMxUnroll];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            f[2 * k] = __fmul_rn(__uint_as_float(w[k] << 16), s);
-            f[2 * k + 1] = __fmul_rn(__uint_as_float(w[k] & 0xFFFF0000u), s);
+    for (int u = 0; u < kMxUnroll; ++u) {
+        const int64_t i = i0 + u * 256;
+        q[u] = e[u] = 0;
+        if (i < n8) {
+            // (a row index by 32-bit division where the matrix has fewer than 2^35 elements)
+            const int64_t row = n8 >> 32 ? i / per_row : static_cast<uint32_t>(i) / per_row;
+            q[u] = __ldg(reinterpret_cast<const uint32_t*>(codes) + i);
+            e[u] = __ldg(scales + mx_scale_offset(row, (i - row * per_row) >> 2, kts));
         }
+    }
+#pragma unroll
+    for (int u = 0; u < kMxUnroll; ++u) {
+        const int64_t i = i0 + u * 256;
+        if (i >= n8) break;
+        const float s = e8m0_value(e[u]);
         if constexpr (sizeof(T) == 4) {
+            float f[8];
+            e2m1_scale8(q[u], s, f);
             float4* o = reinterpret_cast<float4*>(out) + 2 * i;
             o[0] = make_float4(f[0], f[1], f[2], f[3]);
             o[1] = make_float4(f[4], f[5], f[6], f[7]);
         } else {
-            reinterpret_cast<uint4*>(out)[i] = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
-                                                          pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+            reinterpret_cast<uint4*>(out)[i] = e2m1_scale8_bf16(q[u], s);
         }
     }
 }

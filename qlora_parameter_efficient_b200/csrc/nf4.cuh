@@ -181,25 +181,33 @@ __global__ void __launch_bounds__(256) k_nf4_quantize(const TW* __restrict__ W, 
 
 // ------------------------------------------------------------------ decode (stand-alone)
 
-// bf16 output: one thread per 64-block through the same byte-permute decoder as the GEMMs.
+// bf16 output through the same byte-permute decoder as the GEMMs: eight weights per thread and step
+// (4 code bytes in, 16 bytes out, consecutive threads consecutive), kNf4Unroll steps' loads issued
+// together.  11008 x 4096: 42 us with one thread per 64-block, whose stores are 128 bytes apart.
+constexpr int kNf4Unroll = 4;
 __global__ void __launch_bounds__(256) k_nf4_dequant_bf16(const uint8_t* __restrict__ codes,
                                                           const uint8_t* __restrict__ absmax_q,
                                                           const float* __restrict__ c2,
                                                           int64_t nblocks,
                                                           __nv_bfloat16* __restrict__ out) {
-    const int64_t blk = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-    if (blk >= nblocks) return;
-    const float s = nf4_block_scale(absmax_q[blk], c2[blk / kGroup]);
-    const Nf4Planes p = nf4_make_planes(s);
-    const uint4* src = reinterpret_cast<const uint4*>(codes + blk * (kBlock / 2));
-    uint4* dst = reinterpret_cast<uint4*>(out + blk * kBlock);
+    const int64_t n8 = nblocks * (kBlock / 8);
+    const int64_t i0 = static_cast<int64_t>(blockIdx.x) * (256 * kNf4Unroll) + threadIdx.x;
+    uint32_t q[kNf4Unroll], q8[kNf4Unroll];
+    float c[kNf4Unroll];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const uint4 q = src[h];
-        dst[4 * h + 0] = nf4_decode8(q.x, p);
-        dst[4 * h + 1] = nf4_decode8(q.y, p);
-        dst[4 * h + 2] = nf4_decode8(q.z, p);
-        dst[4 * h + 3] = nf4_decode8(q.w, p);
+    for (int u = 0; u < kNf4Unroll; ++u) {
+        const int64_t i = i0 + u * 256;
+        if (i < n8) {
+            q[u] = __ldg(reinterpret_cast<const uint32_t*>(codes) + i);
+            q8[u] = __ldg(absmax_q + (i >> 3));
+            c[u] = __ldg(c2 + (i >> 3) / kGroup);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < kNf4Unroll; ++u) {
+        const int64_t i = i0 + u * 256;
+        if (i < n8)
+            reinterpret_cast<uint4*>(out)[i] = nf4_decode8(q[u], nf4_make_planes(nf4_block_scale(q8[u], c[u])));
     }
 }
 

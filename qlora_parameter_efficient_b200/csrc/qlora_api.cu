@@ -1069,7 +1069,7 @@ qlora_status nf4_dequantize(const qlora_nf4* w, void* W_out, qlora_dtype out_dty
     if (w->d_out < 1 || w->d_in < 64 || w->d_in % 64) return QLORA_ERR_UNSUPPORTED;
     const int64_t nblocks = w->d_out * w->d_in / 64;
     if (out_dtype == QLORA_BF16) {
-        k_nf4_dequant_bf16<<<static_cast<unsigned>(cdiv(nblocks, 256)), 256, 0, stream>>>(
+        k_nf4_dequant_bf16<<<static_cast<unsigned>(cdiv(nblocks * 8, 256 * kNf4Unroll)), 256, 0, stream>>>(
             w->codes, w->absmax_q, w->c2, nblocks, static_cast<__nv_bfloat16*>(W_out));
         QL_LAUNCH_CHECK();
         return QLORA_OK;
