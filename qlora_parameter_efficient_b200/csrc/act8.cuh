@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(320, 1)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_free + L::kAcc);
     volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = warp_index(), lane = threadIdx.x & 31;
     const int C = args.ranks;
     const int rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int tile = blockIdx.x / C;
@@ -282,78 +282,84 @@ __global__ void __launch_bounds__(320, 1)
     for (int j = 0; j < kHalf; ++j) acc[j] = 0.f;
 
     if (warp == 0) {
-        if (lane == 0) {
-            int issued = 0;
-            for (int it = 0, s = 0, ph = 0; it < n_iters; ++it) {
-                if (!mbar_wait(&empty[s], ph ^ 1, abort, args.wait_ns)) {
-                    fail();
-                    break;
-                }
-                const int kx = (k_begin + it) * 64;
-                mbar_arrive_expect_tx(&full[s], (int8 ? L::kRaw : L::kA) + b_bytes);
-                uint8_t* a = int8 ? sR + s * L::kRaw : sA + s * L::kA;
+        int issued = 0;
+        const uint32_t bytes = (int8 ? L::kRaw : L::kA) + b_bytes;
+        for (int it = 0, s = 0, ph = 0; it < n_iters; ++it) {
+            if (!mbar_wait_uniform(&empty[s], ph ^ 1, abort, args.wait_ns)) {
+                fail();
+                break;
+            }
+            const int kx = (k_begin + it) * 64;
+            uint8_t* a = int8 ? sR + s * L::kRaw : sA + s * L::kA;
+            uint8_t* dst = sB + s * b_bytes;
+            if (elect_one()) {
+                mbar_arrive_expect_tx(&full[s], bytes);
                 if (amn) {
                     tma_load_2d(a, tmA, &full[s], m0, kx);
                     if (!int8) tma_load_2d(a + 8192, tmA, &full[s], m0 + 64, kx);
                 } else {
                     tma_load_2d(a, tmA, &full[s], kx, m0);
                 }
-                uint8_t* dst = sB + s * b_bytes;
                 if (bmn) {
                     for (int c = 0; c < chunks; ++c) tma_load_2d(dst + c * L::kChunk, tmB, &full[s], c * 64, kx);
                 } else {
                     tma_load_2d(dst, tmB, &full[s], kx, 0);
                 }
-                issued = it + 1;
-                if (++s == S) s = 0, ph ^= 1;
             }
-            if (*abort)
-                for (int it = max(0, issued - S); it < issued; ++it)
-                    mbar_wait(&full[it % S], (it / S) & 1, nullptr, args.wait_ns);
+            __syncwarp();
+            issued = it + 1;
+            if (++s == S) s = 0, ph ^= 1;
         }
+        if (*abort)
+            for (int it = max(0, issued - S); it < issued; ++it)
+                mbar_wait(&full[it % S], (it / S) & 1, nullptr, args.wait_ns);
     } else if (warp == 1) {
-        if (lane == 0) {
-            const uint32_t idesc = make_idesc_bf16(128, n_mma, amn, bmn);
-            const uint32_t a_step = amn ? 2048 : 32, a_lbo = amn ? 8192 : 16;
-            const uint32_t b_step = bmn ? 2048 : 32, b_lbo = bmn ? 8192 : 16;
-            int seg = 0, in_seg = 0;
-            for (int it = 0, s = 0, ph = 0; it < n_iters; ++it) {
-                bool ok = true;
-                if (in_seg == 0 && seg >= NA)
-                    ok = mbar_wait(&acc_free[seg % NA], ((seg / NA) & 1) ^ 1, abort, args.wait_ns);
-                if (ok) ok = mbar_wait(&full[s], ph, abort, args.wait_ns);
-                if (ok && int8) ok = mbar_wait(&decoded[s], ph, abort, args.wait_ns);
-                if (!ok) {
-                    fail();
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t d = tmem + static_cast<uint32_t>((seg % NA) * acc_cols);
-                const uint32_t a = smem_u32(sA + s * L::kA);
+        const uint32_t idesc = make_idesc_bf16(128, n_mma, amn, bmn);
+        const uint32_t a_step = amn ? 2048 : 32, b_step = bmn ? 2048 : 32;
+        const uint64_t a_desc = make_sw128_desc(smem_u32(sA), amn ? 8192 : 16, 1024);
+        const uint64_t b_desc = make_sw128_desc(smem_u32(sB), bmn ? 8192 : 16, 1024);
+        int in_seg = 0, acc_i = 0, acc_ph = 1;      // accumulator tile of the segment, phase of its release
+        for (int it = 0, s = 0, ph = 0; it < n_iters; ++it) {
+            bool ok = true;
+            if (in_seg == 0) ok = mbar_wait_uniform(&acc_free[acc_i], acc_ph, abort, args.wait_ns);
+            if (ok) ok = mbar_wait_uniform(int8 ? &decoded[s] : &full[s], ph, abort, args.wait_ns);
+            if (ok && int8) ok = mbar_wait_uniform(&full[s], ph, abort, args.wait_ns);
+            if (!ok) {
+                fail();
+                break;
+            }
+            tc_fence_after();
+            const uint32_t d = tmem + static_cast<uint32_t>(acc_i * acc_cols);
+            // (descriptors hold addresses in 16-byte units; shared memory ends below their field's 256 KB)
+            const uint64_t ad = a_desc + static_cast<uint32_t>(s * (L::kA >> 4));
+            const uint64_t bd = b_desc + static_cast<uint32_t>(s * (b_bytes >> 4));
+            const bool last = in_seg + 1 == seg_len || it == n_iters - 1;
+            if (elect_one()) {
                 for (int b = 0; b < groups; ++b) {
-                    const uint32_t bb = smem_u32(sB + s * b_bytes + b * 2 * L::kChunk);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        umma_bf16_ss(d, make_sw128_desc(a + k * a_step, a_lbo, 1024),
-                                     make_sw128_desc(bb + k * b_step, b_lbo, 1024), idesc,
+                        umma_bf16_ss(d, ad + ((k * a_step) >> 4), bd + ((b * 2 * L::kChunk + k * b_step) >> 4), idesc,
                                      (in_seg > 0 || b > 0 || k > 0) ? 1u : 0u);
                 }
                 umma_commit(&empty[s]);
-                if (++in_seg == seg_len || it == n_iters - 1) {
-                    umma_commit(&accf[seg % NA]);
-                    in_seg = 0;
-                    ++seg;
-                }
-                if (++s == S) s = 0, ph ^= 1;
+                if (last) umma_commit(&accf[acc_i]);
             }
+            __syncwarp();
+            ++in_seg;
+            if (last) {
+                in_seg = 0;
+                if (++acc_i == NA) acc_i = 0, acc_ph ^= 1;
+            }
+            if (++s == S) s = 0, ph ^= 1;
         }
     } else {
         bool ok = true;
-        auto drain = [&](int seg) {
-            ok = mbar_wait_warp(&accf[seg % NA], (seg / NA) & 1, abort, args.wait_ns);
+        int acc_i = 0, acc_ph = 0;
+        auto drain = [&]() {
+            ok = mbar_wait_warp(&accf[acc_i], acc_ph, abort, args.wait_ns);
             if (!ok) return;
             tc_fence_after();
-            const uint32_t t = tmem + (static_cast<uint32_t>(q * 32) << 16) + (seg % NA) * acc_cols + half * kHalf;
+            const uint32_t t = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc_i * acc_cols + half * kHalf;
 #pragma unroll
             for (int c = 0; c < kHalf; c += 32)
                 if (half * kHalf + c < job.N) {
@@ -368,7 +374,8 @@ __global__ void __launch_bounds__(320, 1)
                 }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&acc_free[seg % NA]);
+            if (lane == 0) mbar_arrive(&acc_free[acc_i]);
+            if (++acc_i == NA) acc_i = 0, acc_ph ^= 1;
         };
         if (int8) {
             const int td = threadIdx.x - 64;                      // 0..255: the int8 block of this thread
@@ -412,11 +419,11 @@ __global__ void __launch_bounds__(320, 1)
                 }
                 // one or two segments behind the decode, so that a drain does not wait for MMAs in flight
                 // and the segments of the next round find their accumulator tiles free
-                for (const int end = (it0 + 4) / seg_len - NA / 2; ok && drained < end && drained < n_seg;) drain(drained++);
+                for (const int end = (it0 + 4) / seg_len - NA / 2; ok && drained < end && drained < n_seg; ++drained) drain();
             }
-            while (ok && drained < n_seg) drain(drained++);
+            for (; ok && drained < n_seg; ++drained) drain();
         } else {
-            for (int g = 0; ok && g < n_seg; ++g) drain(g);
+            for (int g = 0; ok && g < n_seg; ++g) drain();
         }
         if (!ok) fail();
     }

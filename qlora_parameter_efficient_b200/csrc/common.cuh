@@ -111,6 +111,33 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity,
     return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 
+// Wait of a whole warp with a result the compiler knows to be uniform (a vote), for warps that issue
+// TMA copies or MMAs: their operands live in uniform registers, and under divergent control flow
+// (one lane in an `if`) every issue first moves them there, which measured about 90 cycles per MMA,
+// scale copy or bulk copy.  With the whole warp in the loop and elect_one() around the issue alone
+// the operands are computed in uniform registers.
+__device__ __forceinline__ bool mbar_wait_uniform(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                                  uint64_t limit_ns) {
+    const uint32_t addr = smem_u32(bar);
+    if (__all_sync(0xffffffffu, mbar_try_wait(addr, parity))) return true;
+    const uint64_t t0 = globaltimer_ns();
+    while (true) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(addr, parity))) return true;
+        const bool stop = (abort != nullptr && *abort) || globaltimer_ns() - t0 > limit_ns;
+        if (__any_sync(0xffffffffu, stop)) return false;
+    }
+}
+
+// True in one lane of a converged warp, always the same one.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(ok));
+    return ok != 0;
+}
+
+// The warp's index in its block, as a uniform value.
+__device__ __forceinline__ int warp_index() { return __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0); }
+
 // ------------------------------------------------------------------ clusters
 
 __device__ __forceinline__ uint32_t cluster_ctarank() {

@@ -60,10 +60,12 @@ __device__ __forceinline__ void umma_mxf4_ss(uint32_t d_tmem, uint64_t adesc, ui
 
 // Copy one 512-byte scale tile (32 lines of 16 bytes) to four tensor-memory columns, repeated for
 // the four lane quarters.
+// Its shared-memory descriptor: no swizzle, 8-line groups of 128 bytes, 128 bytes apart.
+__device__ __forceinline__ uint64_t make_scale_desc(uint32_t saddr) {
+    return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (1ull << 16) | (8ull << 32) | (1ull << 46);
+}
 template <int CG>
-__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint32_t saddr) {
-    // no swizzle: 8-line groups of 128 bytes, 128 bytes apart
-    const uint64_t desc = static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (1ull << 16) | (8ull << 32) | (1ull << 46);
+__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t desc) {
     if constexpr (CG == 1)
         asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
     else
@@ -219,7 +221,7 @@ __global__ void __launch_bounds__(MxStreamCfg<NT>::kThreads)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(accf + 1);
     volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = warp_index(), lane = threadIdx.x & 31;
     const int C = args.ranks;
     const int rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int tile = blockIdx.x / C;
@@ -259,92 +261,108 @@ __global__ void __launch_bounds__(MxStreamCfg<NT>::kThreads)
     auto mmas_of = [&](int it) { return min(4, args.k64 - (c_begin + it) * 4); };
 
     if (warp == 0) {
-        if (lane == 0) {
-            auto load_w = [&](int it) {
-                const int s = it % S;
-                const int c = c_begin + it;
-                const uint32_t sf = static_cast<uint32_t>((mmas_of(it) + 1) / 2) * kMxTileBytes;
-                mbar_arrive_expect_tx(&full[s], L::kA + L::kB + 2 * sf);
-                tma_load_2d(sA + s * L::kA, &tmW, &full[s], c * 128, n0);
-                bulk_load(sSa + s * L::kSf,
-                          args.w_scales + (static_cast<int64_t>(tile) * args.col_tiles + 2 * c) * kMxTileBytes, sf,
-                          &full[s]);
-            };
-            auto load_x = [&](int it) {
-                const int s = it % S;
-                const int c = c_begin + it;
-                const uint32_t sf = static_cast<uint32_t>((mmas_of(it) + 1) / 2) * kMxTileBytes;
-                tma_load_2d(sB + s * L::kB, &tmX, &full[s], c * 128, t0);
-                bulk_load(sSb + s * L::kSf,
-                          args.x_scales + (static_cast<int64_t>(t0 >> 7) * args.col_tiles + 2 * c) * kMxTileBytes, sf,
-                          &full[s]);
-            };
-            const int ahead = min(S, n_main);
-            for (int it = 0; it < ahead; ++it) load_w(it);
-            griddep_wait();
-            for (int it = 0; it < ahead; ++it) load_x(it);
-            int issued = ahead;
-            for (int it = ahead; it < n_iters; ++it) {
-                const int s = it % S;
-                if (!mbar_wait(&empty[s], ((it / S) & 1) ^ 1, abort, args.wait_ns)) {
-                    set_error(args.err, kErrTimeout);
-                    *abort = 1;
-                    break;
-                }
+        auto load_w = [&](int it, int s) {
+            const int c = c_begin + it;
+            const uint32_t sf = static_cast<uint32_t>((mmas_of(it) + 1) / 2) * kMxTileBytes;
+            mbar_arrive_expect_tx(&full[s], L::kA + L::kB + 2 * sf);
+            tma_load_2d(sA + s * L::kA, &tmW, &full[s], c * 128, n0);
+            bulk_load(sSa + s * L::kSf,
+                      args.w_scales + (static_cast<int64_t>(tile) * args.col_tiles + 2 * c) * kMxTileBytes, sf, &full[s]);
+        };
+        auto load_x = [&](int it, int s) {
+            const int c = c_begin + it;
+            const uint32_t sf = static_cast<uint32_t>((mmas_of(it) + 1) / 2) * kMxTileBytes;
+            tma_load_2d(sB + s * L::kB, &tmX, &full[s], c * 128, t0);
+            bulk_load(sSb + s * L::kSf,
+                      args.x_scales + (static_cast<int64_t>(t0 >> 7) * args.col_tiles + 2 * c) * kMxTileBytes, sf,
+                      &full[s]);
+        };
+        const int ahead = min(S, n_main);
+        if (elect_one())
+            for (int it = 0; it < ahead; ++it) load_w(it, it);
+        __syncwarp();
+        griddep_wait();
+        if (elect_one())
+            for (int it = 0; it < ahead; ++it) load_x(it, it);
+        __syncwarp();
+        int issued = ahead;
+        for (int it = ahead, s = ahead % S, ph = ahead / S; it < n_iters; ++it) {
+            if (!mbar_wait_uniform(&empty[s], ph ^ 1, abort, args.wait_ns)) {
+                set_error(args.err, kErrTimeout);
+                *abort = 1;
+                break;
+            }
+            if (elect_one()) {
                 if (it < n_main) {
-                    load_w(it);
-                    load_x(it);
+                    load_w(it, s);
+                    load_x(it, s);
                 } else {
                     const int kx = (it - n_main) * 64;
                     mbar_arrive_expect_tx(&full[s], L::kA + L::kB);
                     tma_load_2d(sA + s * L::kA, &tmBx, &full[s], kx, n0);
                     tma_load_2d(sB + s * L::kB, &tmUx, &full[s], kx, t0);
                 }
-                issued = it + 1;
             }
-            if (*abort)
-                for (int it = max(0, issued - S); it < issued; ++it)
-                    mbar_wait(&full[it % S], (it / S) & 1, nullptr, args.wait_ns);
+            __syncwarp();
+            issued = it + 1;
+            if (++s == S) s = 0, ph ^= 1;
         }
+        if (*abort)
+            for (int it = max(0, issued - S); it < issued; ++it)
+                mbar_wait(&full[it % S], (it / S) & 1, nullptr, args.wait_ns);
     } else if (warp == 1) {
-        if (lane == 0) {
-            const uint32_t idesc_x = make_idesc_bf16(128, NT, false, false);
-            bool ok = true;
-            for (int it = 0; it < n_iters; ++it) {
-                const int s = it % S;
-                ok = mbar_wait(&full[s], (it / S) & 1, abort, args.wait_ns);
-                // scale columns are used in turn: those of step it - 2 are free once its MMAs are done
-                if (ok && it >= 2) ok = mbar_wait(&empty[(it - 2) % S], ((it - 2) / S) & 1, abort, args.wait_ns);
-                if (!ok) {
-                    set_error(args.err, kErrTimeout);
-                    *abort = 1;
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t a = smem_u32(sA + s * L::kA), b = smem_u32(sB + s * L::kB);
-                if (it < n_main) {
-                    const uint32_t sfa = tmem + L::kAcc + (it & 1) * 16, sfb = sfa + 8;
-                    const int nk = mmas_of(it);
-                    for (int h = 0; h < (nk + 1) / 2; ++h) {
-                        tmem_cp_scales<1>(sfa + 4 * h, smem_u32(sSa + s * L::kSf + h * kMxTileBytes));
-                        tmem_cp_scales<1>(sfb + 4 * h, smem_u32(sSb + s * L::kSf + h * kMxTileBytes));
-                    }
-                    for (int k = 0; k < nk; ++k) {
-                        const uint32_t id = (k & 1) * 2;
-                        umma_mxf4_ss<1>(tmem, make_sw128_desc(a + k * 32, 16, 1024),
-                                        make_sw128_desc(b + k * 32, 16, 1024), make_idesc_mxf4(128, NT, id, id),
-                                        sfa + 4 * (k >> 1), sfb + 4 * (k >> 1), (it > 0 || k > 0) ? 1u : 0u);
-                    }
-                } else {
-                    const int nk = it == n_iters - 1 ? args.ext_k16_last : 4;
-                    for (int k = 0; k < nk; ++k)
-                        umma_bf16_ss(tmem, make_sw128_desc(a + k * 32, 16, 1024), make_sw128_desc(b + k * 32, 16, 1024),
-                                     idesc_x, (it > 0 || k > 0) ? 1u : 0u);
-                }
-                umma_commit(&empty[s]);
+        const uint32_t idesc_x = make_idesc_bf16(128, NT, false, false);
+        const uint32_t idesc0 = make_idesc_mxf4(128, NT, 0, 0), idesc2 = make_idesc_mxf4(128, NT, 2, 2);
+        const uint64_t a_desc = make_sw128_desc(smem_u32(sA), 16, 1024), b_desc = make_sw128_desc(smem_u32(sB), 16, 1024);
+        const uint64_t sa_desc = make_scale_desc(smem_u32(sSa)), sb_desc = make_scale_desc(smem_u32(sSb));
+        // scale columns are used in turn: those of step it - 2 are free once its MMAs are done
+        int s2 = 0, ph2 = 0;
+        for (int it = 0, s = 0, ph = 0; it < n_iters; ++it) {
+            bool ok = mbar_wait_uniform(&full[s], ph, abort, args.wait_ns);
+            if (ok && it >= 2) {
+                ok = mbar_wait_uniform(&empty[s2], ph2, abort, args.wait_ns);
+                if (++s2 == S) s2 = 0, ph2 ^= 1;
             }
-            umma_commit(accf);
+            if (!ok) {
+                set_error(args.err, kErrTimeout);
+                *abort = 1;
+                break;
+            }
+            tc_fence_after();
+            const uint64_t ad = a_desc + static_cast<uint32_t>(s * (L::kA >> 4));
+            const uint64_t bd = b_desc + static_cast<uint32_t>(s * (L::kB >> 4));
+            if (it < n_main) {
+                const uint32_t sfa = tmem + L::kAcc + (it & 1) * 16, sfb = sfa + 8;
+                const uint64_t sad = sa_desc + static_cast<uint32_t>(s * (L::kSf >> 4));
+                const uint64_t sbd = sb_desc + static_cast<uint32_t>(s * (L::kSf >> 4));
+                const int nk = mmas_of(it);
+                if (elect_one()) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        if (2 * h < nk) {
+                            tmem_cp_scales<1>(sfa + 4 * h, sad + h * (kMxTileBytes >> 4));
+                            tmem_cp_scales<1>(sfb + 4 * h, sbd + h * (kMxTileBytes >> 4));
+                        }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (k < nk)
+                            umma_mxf4_ss<1>(tmem, ad + 2 * k, bd + 2 * k, (k & 1) ? idesc2 : idesc0, sfa + 4 * (k >> 1),
+                                            sfb + 4 * (k >> 1), (it > 0 || k > 0) ? 1u : 0u);
+                    umma_commit(&empty[s]);
+                }
+            } else {
+                const int nk = it == n_iters - 1 ? args.ext_k16_last : 4;
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (k < nk) umma_bf16_ss(tmem, ad + 2 * k, bd + 2 * k, idesc_x, (it > 0 || k > 0) ? 1u : 0u);
+                    umma_commit(&empty[s]);
+                }
+            }
+            __syncwarp();
+            if (++s == S) s = 0, ph ^= 1;
         }
+        if (elect_one()) umma_commit(accf);
     }
     __syncwarp();
 
@@ -498,7 +516,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGemmSmem<MX>::kT
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_free + 2);
     volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = warp_index(), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
     const int n_tiles_total = args.m_tiles * args.n_tiles;
@@ -560,28 +578,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGemmSmem<MX>::kT
     };
 
     if (warp == 0) {
-        if (lane == 0) {
-            const uint32_t full_leader = mapa_shared(smem_u32(&full[0]), 0);
-            int git = 0;
-            for (int u = 0; u < n_units && !*abort; ++u) {
-                int tile, k0, k1;
-                unit(u, tile, k0, k1);
-                const int m0 = (tile % args.m_tiles) * 256 + static_cast<int>(rank) * 128;
-                const int nt = tile / args.m_tiles;
-                const int n0 = nt * 256 + static_cast<int>(rank) * 128;
-                for (int it = k0; it < k1; ++it, ++git) {
-                    const int s = git % S;
-                    if (!mbar_wait(&empty[s], ((git / S) & 1) ^ 1, abort, args.wait_ns)) {
-                        fail();
-                        break;
-                    }
-                    const uint32_t bar = full_leader + static_cast<uint32_t>(s * 8);
-                    uint8_t* a = sA + s * L::kA;
-                    uint8_t* b = sB + s * L::kB;
-                    const bool main_step = it < args.k_steps;
-                    if (rank == 0)
-                        mbar_arrive_expect_tx(&full[s], 2 * (main_step ? L::kStage : L::kA + L::kB));
-                    if (main_step) {
+        const uint32_t full_leader = mapa_shared(smem_u32(&full[0]), 0);
+        int s = 0, ph = 0;
+        bool ok = true;
+        for (int u = 0; ok && u < n_units; ++u) {
+            int tile, k0, k1;
+            unit(u, tile, k0, k1);
+            const int m0 = (tile % args.m_tiles) * 256 + static_cast<int>(rank) * 128;
+            const int nt = tile / args.m_tiles;
+            const int n0 = nt * 256 + static_cast<int>(rank) * 128;
+            for (int it = k0; it < k1; ++it) {
+                ok = mbar_wait_uniform(&empty[s], ph ^ 1, abort, args.wait_ns);
+                if (!ok) break;
+                const uint32_t bar = full_leader + static_cast<uint32_t>(s * 8);
+                uint8_t* a = sA + s * L::kA;
+                uint8_t* b = sB + s * L::kB;
+                if (elect_one()) {
+                    if (it < args.k_steps) {
+                        if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * L::kStage);
                         if (MX) {
                             tma_load_2d_pair(a, &tmA, bar, it * 128, m0);
                             tma_load_2d_pair(b, &tmB, bar, it * 128, n0);
@@ -597,6 +611,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGemmSmem<MX>::kT
                         }
                     } else {
                         const int kx = (it - args.k_steps) * 64;
+                        if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * (L::kA + L::kB));
                         tma_load_2d_pair(a, &tmAx, bar, kx, m0);
                         if (MX) {
                             tma_load_2d_pair(b, &tmBx, bar, kx, n0);
@@ -606,70 +621,81 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGemmSmem<MX>::kT
                         }
                     }
                 }
+                __syncwarp();
+                if (++s == S) s = 0, ph ^= 1;
             }
         }
+        if (!ok) fail();
     } else if (warp == 1) {
-        if (rank == 0 && lane == 0) {
+        if (rank == 0) {
             const uint32_t idesc = make_idesc_bf16(256, 256, false, !MX);
-            int git = 0;
+            const uint32_t idesc0 = make_idesc_mxf4(256, 256, 0, 0), idesc2 = make_idesc_mxf4(256, 256, 2, 2);
+            const uint64_t a_desc = make_sw128_desc(smem_u32(sA), 16, 1024);
+            const uint64_t b_desc = make_sw128_desc(smem_u32(sB), MX ? 16 : 8192, 1024);
+            const uint64_t sa_desc = make_scale_desc(smem_u32(sSa)), sb_desc = make_scale_desc(smem_u32(sSb));
+            constexpr uint32_t kBStep = MX ? 2 : 2048 >> 4;
+            int git = 0, s = 0, ph = 0, s2 = 0, ph2 = 0;
             bool ok = true;
             for (int u = 0; ok && u < n_units; ++u) {
                 int tile, k0, k1;
                 unit(u, tile, k0, k1);
                 // MX: the shared columns of unit u - 1 have been read; else: all of unit u - 2
                 const int prev = u - (MX ? 1 : 2);
-                if (prev >= 0 && !mbar_wait_cluster(&acc_free[prev & 1], (prev >> 1) & 1, abort, args.wait_ns)) {
-                    fail();
-                    break;
-                }
+                if (prev >= 0) ok = mbar_wait_uniform(&acc_free[prev & 1], (prev >> 1) & 1, abort, args.wait_ns);
+                if (!ok) break;
                 tc_fence_after();
                 const uint32_t d = tmem + static_cast<uint32_t>((u & 1) * L::kAcc1);
                 for (int it = k0; it < k1; ++it, ++git) {
-                    const int s = git % S;
-                    ok = mbar_wait(&full[s], (git / S) & 1, abort, args.wait_ns);
+                    ok = mbar_wait_uniform(&full[s], ph, abort, args.wait_ns);
                     // two sets of scale columns in turn: those of stage git - 2 are free once its MMAs are done
-                    if (MX && ok && git >= 2)
-                        ok = mbar_wait(&empty[(git - 2) % S], ((git - 2) / S) & 1, abort, args.wait_ns);
-                    if (!ok) {
-                        fail();
-                        break;
+                    if (MX && ok && git >= 2) {
+                        ok = mbar_wait_uniform(&empty[s2], ph2, abort, args.wait_ns);
+                        if (++s2 == S) s2 = 0, ph2 ^= 1;
                     }
+                    if (!ok) break;
                     tc_fence_after();
-                    const uint32_t a = smem_u32(sA + s * L::kA), b = smem_u32(sB + s * L::kB);
-                    if (it < args.k_steps) {
+                    const uint64_t ad = a_desc + static_cast<uint32_t>(s * (L::kA >> 4));
+                    const uint64_t bd = b_desc + static_cast<uint32_t>(s * (L::kB >> 4));
+                    const bool first = it == k0;
+                    if (MX && it < args.k_steps) {
+                        const uint32_t sfa = tmem + L::kSfCol + (git & 1) * 24, sfb = sfa + 8;
+                        const uint64_t sad = sa_desc + static_cast<uint32_t>(s * (L::kSfA >> 4));
+                        const uint64_t sbd = sb_desc + static_cast<uint32_t>(s * (L::kSfB >> 4));
                         const int nk = it == args.k_steps - 1 ? args.k_mma_last : 4;
-                        if constexpr (MX) {
-                            const uint32_t sfa = tmem + L::kSfCol + (git & 1) * 24, sfb = sfa + 8;
-                            for (int h = 0; h < (nk + 1) / 2; ++h) {
-                                tmem_cp_scales<2>(sfa + 4 * h, smem_u32(sSa + s * L::kSfA + h * 512));
-                                tmem_cp_scales<2>(sfb + 8 * h, smem_u32(sSb + s * L::kSfB + h * 512));
-                                tmem_cp_scales<2>(sfb + 8 * h + 4, smem_u32(sSb + s * L::kSfB + 1024 + h * 512));
-                            }
-                            for (int k = 0; k < nk; ++k) {
-                                const uint32_t id = (k & 1) * 2;
-                                umma_mxf4_ss<2>(d, make_sw128_desc(a + k * 32, 16, 1024),
-                                                make_sw128_desc(b + k * 32, 16, 1024),
-                                                make_idesc_mxf4(256, 256, id, id), sfa + 4 * (k >> 1),
-                                                sfb + 8 * (k >> 1), (it > k0 || k > 0) ? 1u : 0u);
-                            }
-                        } else {
-                            for (int k = 0; k < nk; ++k)
-                                umma_bf16_ss_2sm(d, make_sw128_desc(a + k * 32, 16, 1024),
-                                                 make_sw128_desc(b + k * 2048, 8192, 1024), idesc,
-                                                 (it > k0 || k > 0) ? 1u : 0u);
+                        if (elect_one()) {
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+                                if (2 * h < nk) {
+                                    tmem_cp_scales<2>(sfa + 4 * h, sad + h * 32);
+                                    tmem_cp_scales<2>(sfb + 8 * h, sbd + h * 32);
+                                    tmem_cp_scales<2>(sfb + 8 * h + 4, sbd + 64 + h * 32);
+                                }
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                if (k < nk)
+                                    umma_mxf4_ss<2>(d, ad + 2 * k, bd + 2 * k, (k & 1) ? idesc2 : idesc0,
+                                                    sfa + 4 * (k >> 1), sfb + 8 * (k >> 1), (!first || k > 0) ? 1u : 0u);
+                            umma_commit_2sm_both(&empty[s]);
                         }
                     } else {
-                        const int nk = it == iters_per_tile - 1 ? args.ext_k16_last : 4;
-                        for (int k = 0; k < nk; ++k)
-                            umma_bf16_ss_2sm(d, make_sw128_desc(a + k * 32, 16, 1024),
-                                             MX ? make_sw128_desc(b + k * 32, 16, 1024)
-                                                : make_sw128_desc(b + k * 2048, 8192, 1024),
-                                             idesc, (it > k0 || k > 0) ? 1u : 0u);
+                        const int nk = it == iters_per_tile - 1 && it >= args.k_steps ? args.ext_k16_last
+                                       : it == args.k_steps - 1                       ? args.k_mma_last
+                                                                                      : 4;
+                        if (elect_one()) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                if (k < nk)
+                                    umma_bf16_ss_2sm(d, ad + 2 * k, bd + kBStep * k, idesc, (!first || k > 0) ? 1u : 0u);
+                            umma_commit_2sm_both(&empty[s]);
+                        }
                     }
-                    umma_commit_2sm_both(&empty[s]);
+                    __syncwarp();
+                    if (++s == S) s = 0, ph ^= 1;
                 }
-                umma_commit_2sm_both(&accf[u & 1]);
+                if (ok && elect_one()) umma_commit_2sm_both(&accf[u & 1]);
+                __syncwarp();
             }
+            if (!ok) fail();
         }
     } else {
         // ---------------------------------------------------------------- epilogue
