@@ -141,7 +141,8 @@ __host__ __device__ __forceinline__ ActTriple act_triple(int r) {
 enum : int {
     kActTriple = 0,   // scale D as three bf16 terms (ActTriple layout)
     kActCols = 1,     // fp32 out[j, m] = scale D[m, j]  (dA)
-    kActRows = 2      // fp32 out[m, j] = scale D[m, j]  (dB)
+    kActRows = 2,     // fp32 out[m, j] = scale D[m, j]  (dB)
+    kActU = 3         // bf16 out[m, j] = scale D[m, j] (row stride ld) and out2[m, j] = D[m, j] (nullable)
 };
 
 // One product of a launch: D[M, N] = sum over K of A[M, K] B[N, K], B bf16 or a bf16 triple.
@@ -159,11 +160,40 @@ struct ActJob {
     float scale;
     int accumulate;          // kActCols, kActRows: add to out
     void* out;
+    int ld;
+    __nv_bfloat16* out2;
+    // Forward: A (bf16 [M, K]) is also quantized to MXFP4 on its way through shared memory (null: not)
+    uint8_t *mx_codes, *mx_scales;
+};
+// Copy of a matrix whose rows are no whole 16-byte units to zero-padded rows.
+struct PadCopy {
+    const __nv_bfloat16* src;
+    __nv_bfloat16* dst;
+    int64_t rows;
+    int cols, ld, ctas;
+    __device__ __forceinline__ void run(int cta) const {
+        const int64_t n = rows * ld;
+        for (int64_t i = static_cast<int64_t>(cta) * blockDim.x + threadIdx.x; i < n;
+             i += static_cast<int64_t>(ctas) * blockDim.x) {
+            const int64_t row = i / ld;
+            const int col = static_cast<int>(i - row * ld);
+            dst[i] = col < cols ? src[row * cols + col] : __float2bfloat16_rn(0.f);
+        }
+    }
 };
 struct ActGemmArgs {
     ActJob job[2];
-    int tiles0;              // M tiles of job 0; tiles above belong to job 1
+    int tiles0, tiles;       // M tiles of job 0, of both
     int ranks;               // CTAs per cluster, K split over them
+    // Done by the CTAs past the tiles (each range a multiple of ranks): a padded copy, and the MXFP4 of X
+    // [qx_rows, qx_cols], one scale tile per CTA, where the products' own CTAs are too few for it
+    PadCopy pad;
+    int qx_ctas, qx_tiles;
+    const __nv_bfloat16* qx;
+    int64_t qx_rows, qx_cols;
+    uint8_t *qx_codes, *qx_scales;
+    int* zero;               // ticket counters of a later kernel of the call, cleared by CTA 0
+    int n_zero;
     int* err;
     uint64_t wait_ns;
 };
@@ -218,14 +248,29 @@ __global__ void __launch_bounds__(320, 1)
     const int C = args.ranks;
     const int rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int tile = blockIdx.x / C;
+    if (tile >= args.tiles) {
+        griddep_enter();
+        const int b = static_cast<int>(blockIdx.x) - args.tiles * C;
+        if (b >= args.qx_ctas) {
+            args.pad.run(b - args.qx_ctas);
+        } else if (b < args.qx_tiles) {
+            const int64_t kts = mx_col_tiles(args.qx_cols);
+            mxfp4_quantize_tile(args.qx, args.qx_rows, args.qx_cols, b / kts, b % kts, args.qx_codes, args.qx_scales,
+                                smem_raw);
+        }
+        return;
+    }
     const int ji = tile >= args.tiles0 ? 1 : 0;
     const ActJob& job = args.job[ji];
     const CUtensorMap* tmA = ji ? &tmA1 : &tmA0;
     const CUtensorMap* tmB = ji ? &tmB1 : &tmB0;
     const int m0 = (tile - (ji ? args.tiles0 : 0)) * 128;
     const bool int8 = job.int8, amn = job.amn, bmn = job.bmn;
-    const int k_begin = static_cast<int>(static_cast<int64_t>(job.k_steps) * rank / C);
-    const int n_iters = static_cast<int>(static_cast<int64_t>(job.k_steps) * (rank + 1) / C) - k_begin;
+    // (K ranges begin at whole scale tiles of 128 columns)
+    const int64_t k_pairs = (job.k_steps + 1) / 2;
+    const int k_begin = static_cast<int>(k_pairs * rank / C) * 2;
+    const int n_iters = min(job.k_steps, static_cast<int>(k_pairs * (rank + 1) / C) * 2) - k_begin;
+    const bool quant = job.mx_codes != nullptr;
     const ActTriple tr = act_triple(job.N);
     const int terms = RPT == 64 && job.triple ? 3 : 1;         // column groups of an accumulator tile
     const int groups = RPT == 128 && job.triple ? 3 : 1;       // MMAs per 16 of K
@@ -246,7 +291,7 @@ __global__ void __launch_bounds__(320, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < L::kMaxStages; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
+            mbar_init(&empty[s], quant ? 9 : 1);     // the MMAs, and the warps that quantize
             mbar_init(&decoded[s], 8);
         }
         for (int b = 0; b < L::kAcc; ++b) {
@@ -269,6 +314,8 @@ __global__ void __launch_bounds__(320, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     griddep_enter();
+    if (blockIdx.x == 0)
+        for (int i = threadIdx.x; i < args.n_zero; i += 320) args.zero[i] = 0;
 
     auto fail = [&]() {
         set_error(args.err, kErrTimeout);
@@ -422,6 +469,43 @@ __global__ void __launch_bounds__(320, 1)
                 for (const int end = (it0 + 4) / seg_len - NA / 2; ok && drained < end && drained < n_seg; ++drained) drain();
             }
             for (; ok && drained < n_seg; ++drained) drain();
+        } else if (quant) {
+            // one block of 32 per thread and stage, from the swizzled operand tile
+            const int td = threadIdx.x - 64, row = td >> 1, b = td & 1, sw = row & 7;
+            const int64_t grow = static_cast<int64_t>(m0) + row;
+            const bool in = grow < job.M;
+            uint8_t* codes = job.mx_codes + grow * (job.K / 2) + b * 16;
+            // the scale word of (row, two stages): its tile advances by 512 bytes every other stage
+            uint8_t* word = job.mx_scales + mx_scale_offset(grow, k_begin * 2, mx_col_tiles(job.K));
+            uint32_t e_word = 0;
+            int drained = 0;
+            for (int it = 0, s = 0, ph = 0; ok && it < n_iters; ++it) {
+                ok = mbar_wait_warp(&full[s], ph, abort, args.wait_ns);
+                if (!ok) break;
+                const uint8_t* src = sA + s * L::kA + row * 128;
+                Raw8<__nv_bfloat16> raw[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    raw[c].v = *reinterpret_cast<const uint4*>(src + (((4 * b + c) ^ sw) << 4));
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&empty[s]);       // the tile has been read
+                uint32_t e, q[4];
+                mxfp4_block32(raw, e, q);
+                if (in) *reinterpret_cast<uint4*>(codes + static_cast<int64_t>(k_begin + it) * 32) = make_uint4(q[0], q[1], q[2], q[3]);
+                e |= __shfl_xor_sync(0xffffffffu, e, 1) << 8;        // (of the even lane: both blocks' bytes)
+                e_word |= e << (16 * (it & 1));
+                if ((it & 1) || it == n_iters - 1) {
+                    if (in && b == 0) *reinterpret_cast<uint32_t*>(word + (it >> 1) * kMxTileBytes) = e_word;
+                    e_word = 0;
+                }
+                if (++s == S) s = 0, ph ^= 1;
+                // two segments behind, so that no drain waits for MMAs in flight
+                if ((it + 1) % seg_len == 0 && (it + 1) / seg_len - 2 > drained) {
+                    drain();
+                    ++drained;
+                }
+            }
+            for (; ok && drained < n_seg; ++drained) drain();
         } else {
             for (int g = 0; ok && g < n_seg; ++g) drain();
         }
@@ -457,7 +541,7 @@ __global__ void __launch_bounds__(320, 1)
         auto total = [&](int rl, int j) {
             float v = 0.f;
             for (int c = 0; c < C; ++c) v += red[(c * R + rl) * L::kLdRed + j];
-            return job.scale * v;
+            return job.mode == kActU ? v : job.scale * v;
         };
         const int td = threadIdx.x - 64;
         if (job.mode == kActTriple) {
@@ -473,6 +557,15 @@ __global__ void __launch_bounds__(320, 1)
                     const float rest = v - __bfloat162float(h);
                     v = fabsf(rest) < __int_as_float(0x7F800000) ? rest : 0.f;
                 }
+            }
+        } else if (job.mode == kActU) {
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(job.out);
+            for (int i = td; i < rows * N; i += 256) {
+                const int rl = i / N, j = i % N;
+                const int64_t row = row0 + rl;
+                const float v = total(rl, j);
+                out[row * job.ld + j] = __float2bfloat16_rn(job.scale * v);
+                if (job.out2) job.out2[row * N + j] = __float2bfloat16_rn(v);
             }
         } else if (job.mode == kActCols) {
             float* out = static_cast<float*>(job.out);
@@ -509,12 +602,7 @@ struct BwdPrepArgs {
     uint32_t per_row;             // d_in / 8
     __nv_bfloat16* w;
     int ctas_w;
-    struct Pad {
-        const __nv_bfloat16* src;
-        __nv_bfloat16* dst;
-        int64_t rows;
-        int cols, ld, ctas;
-    } pad[3];
+    PadCopy pad[3];
     int* zero;
     int n_zero;
 };
@@ -553,15 +641,7 @@ __global__ void __launch_bounds__(256) k_bwd_prepare(const __grid_constant__ Bwd
     b -= a.ctas_w;
 #pragma unroll
     for (int p = 0; p < 3; ++p) {
-        if (b >= 0 && b < a.pad[p].ctas) {
-            const int64_t n = a.pad[p].rows * a.pad[p].ld;
-            for (int64_t i = static_cast<int64_t>(b) * 256 + threadIdx.x; i < n;
-                 i += static_cast<int64_t>(a.pad[p].ctas) * 256) {
-                const int64_t row = i / a.pad[p].ld;
-                const int col = static_cast<int>(i - row * a.pad[p].ld);
-                a.pad[p].dst[i] = col < a.pad[p].cols ? a.pad[p].src[row * a.pad[p].cols + col] : __float2bfloat16_rn(0.f);
-            }
-        }
+        if (b >= 0 && b < a.pad[p].ctas) a.pad[p].run(b);
         b -= a.pad[p].ctas;
     }
     if (b == 0)

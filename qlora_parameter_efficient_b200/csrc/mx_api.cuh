@@ -7,6 +7,7 @@ namespace {
 
 // ======================================================================= planning
 
+constexpr int pad8(int64_t n) { return static_cast<int>((n + 7) / 8 * 8); }   // whole 16-byte units of bf16
 constexpr int64_t kMaxDim = 1LL << 30;
 constexpr int64_t kMxStreamMaxT = 512;
 
@@ -59,17 +60,17 @@ PairSched pair_schedule(int64_t M, int64_t N, int64_t k_steps, int64_t min_steps
     return g;
 }
 
-// Ranks of a weight-stream cluster: as many of 8, 4, 2, 1 as K has stages for and the resident CTAs
-// (slots) can take at once.
-int mx_ranks(int64_t tiles, int64_t chunks, int64_t slots) {
-    for (int c = 8; c > 1; c >>= 1)
-        if (chunks >= c && tiles * c <= slots) return c;
+// Ranks of a weight-stream cluster: as many of 4, 2, 1 as K has stages for and two CTAs per SM can take
+// at once (8 ranks of half the length measured 8.0 against 7.0 us at one token of a 4096 x 4096 layer).
+int mx_ranks(int64_t tiles, int64_t chunks) {
+    for (int c = 4; c > 1; c >>= 1)
+        if (chunks >= c && tiles * c <= 2 * kSmsForSplit) return c;
     return 1;
 }
 
 struct MxFwdPlan {
-    int RP = 0, split_u = 1;
-    size_t codes = 0, scales = 0, us = 0, b_pad = 0, part = 0, pair = 0, total = 0;
+    int RP = 0;
+    size_t codes = 0, scales = 0, us = 0, b_pad = 0, pair = 0, total = 0;
     PairSched sched;
 };
 MxFwdPlan mx_fwd_plan(int64_t T, int64_t d_out, int64_t d_in, int r) {
@@ -81,14 +82,12 @@ MxFwdPlan mx_fwd_plan(int64_t T, int64_t d_out, int64_t d_in, int r) {
         return o;
     };
     p.RP = pad_rank(r);
-    p.codes = take(static_cast<size_t>(T) * d_in / 2);
-    p.scales = take(mx_scale_bytes(T, d_in));
-    p.us = take(static_cast<size_t>(T) * p.RP * 2);
-    if (r % 8) p.b_pad = take(static_cast<size_t>(d_out) * p.RP * 2);
     if (mx_route(T) != kMxDecode) {
-        p.split_u = choose_split(cdiv(T, kBM), cdiv(d_in, kBK));
-        p.part = take(static_cast<size_t>(p.split_u) * T * p.RP * 4);
+        p.codes = take(static_cast<size_t>(T) * d_in / 2);
+        p.scales = take(mx_scale_bytes(T, d_in));
     }
+    p.us = take(static_cast<size_t>(T) * p.RP * 2);
+    if (r % 8) p.b_pad = take(static_cast<size_t>(d_out) * pad8(r) * 2);
     if (mx_route(T) == kMxPair) {
         p.sched = pair_schedule(T, d_out, cdiv(d_in, 256), 2);
         p.pair = take(p.sched.bytes());
@@ -112,11 +111,10 @@ MxBwdPlan mx_bwd_plan(int64_t T, int64_t d_out, int64_t d_in, int r) {
         return o;
     };
     p.RP = pad_rank(r);
-    const size_t rp = static_cast<size_t>(p.RP), row = static_cast<size_t>(T) * rp;
-    if (r % 8) p.b_pad = take(static_cast<size_t>(d_out) * rp * 2);
+    if (r % 8) p.b_pad = take(static_cast<size_t>(d_out) * pad8(r) * 2);
     if (d_out % 8) p.dh_pad = take(static_cast<size_t>(T) * ((d_out + 7) / 8 * 8) * 2);
     const size_t triple = static_cast<size_t>(T) * act_triple(r).ld * 2;
-    p.u3 = take(std::max(triple, row * 2));   // U and s G, three bf16 terms each
+    p.u3 = take(triple);           // U and s G, three bf16 terms each (or a given U in padded rows)
     p.g3 = take(triple);
     p.w = take(static_cast<size_t>(d_out) * d_in * 2);      // the decoded weight
     p.sched = pair_schedule(T, d_in, cdiv(d_out, 64), 8);
@@ -155,8 +153,7 @@ qlora_status launch_mx_stream(const CUtensorMap& tw, const CUtensorMap& tx, cons
     static std::atomic<uint64_t> configured{0};
     QL_TRY(allow_smem(k_mx_stream<NT>, L::kTotal, configured));
     const int64_t tiles = cdiv(g.d_out, 128), tok = cdiv(g.T, NT);
-    // one CTA per SM above 64 tokens, two below
-    g.ranks = mx_ranks(tiles * tok, cdiv(g.k64, 4), NT <= 64 ? 2 * kSmsForSplit : kSmsForSplit);
+    g.ranks = L::kQuant ? mx_ranks(tiles, cdiv(g.k64, 4)) : 1;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -177,12 +174,13 @@ qlora_status launch_mx_stream(const CUtensorMap& tw, const CUtensorMap& tx, cons
 }
 
 // One launch of one or two adapter products.  The cluster size (K ranks) is the one with the shortest
-// schedule on 148 SMs, one CTA each: waves x (K steps of a rank + what a CTA costs besides, about
-// six K steps).
+// schedule on 148 SMs, one CTA each, by the measured costs: a K step of a bf16 product 1 (0.33 us), of a
+// triple 1.3, of one whose operand is decoded or quantized on the way 1.8, a CTA besides 8.
 struct ActLaunch {
     ActGemmArgs g{};
     CUtensorMap a[2], b[2];
     int n = 0;
+    bool pdl = true;         // launched with programmatic dependent launch
     ActJob& add(int64_t M, int N, int64_t K) {
         ActJob& j = g.job[n++];
         j.M = static_cast<int>(M);
@@ -204,37 +202,47 @@ qlora_status launch_act_gemm(ActLaunch& l, int* err, cudaStream_t st) {
         l.b[1] = l.b[0];
     }
     int64_t tiles = 0;
-    int steps = 1 << 30, most = 0;
+    int steps = 1 << 30;
     for (int i = 0; i < l.n; ++i) {
         tiles += cdiv(l.g.job[i].M, 128);
         steps = std::min(steps, l.g.job[i].k_steps);
-        most = std::max(most, l.g.job[i].k_steps);
     }
-    int64_t best = 0;
-    for (int c = 1; c <= 8 && c <= steps; c *= 2) {
-        const int64_t cost = cdiv(tiles * c, kSmsForSplit) * (cdiv(most, c) + 6);
+    double best = 0;
+    for (int c = 1; c <= 8 && 2 * c <= steps + 1; c *= 2) {
+        // one wave ends with its longest CTA; several end, on average, half a CTA after an even share
+        double total = 0, longest = 0;
+        for (int i = 0; i < l.n; ++i) {
+            const ActJob& j = l.g.job[i];
+            const double one = cdiv(j.k_steps, c) * ((j.int8 || j.mx_codes) ? 1.8 : j.triple ? 1.3 : 1.0) + 8;
+            total += one * cdiv(j.M, 128) * c;
+            longest = std::max(longest, one);
+        }
+        const double cost = tiles * c <= kSmsForSplit ? longest : total / kSmsForSplit + longest / 2;
         if (c == 1 || cost < best) {
             best = cost;
             l.g.ranks = c;
         }
     }
     l.g.tiles0 = static_cast<int>(cdiv(l.g.job[0].M, 128));
+    l.g.tiles = static_cast<int>(tiles);
+    l.g.pad.ctas = static_cast<int>(cdiv(l.g.pad.ctas, l.g.ranks)) * l.g.ranks;
+    l.g.qx_ctas = static_cast<int>(cdiv(l.g.qx_tiles, l.g.ranks)) * l.g.ranks;
     l.g.err = err;
     l.g.wait_ns = kWaitNs;
     cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = static_cast<unsigned>(l.g.ranks);
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(l.g.ranks);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(tiles * l.g.ranks));
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles * l.g.ranks + l.g.qx_ctas + l.g.pad.ctas));
     cfg.blockDim = dim3(320);
     cfg.dynamicSmemBytes = L::kTotal;
     cfg.stream = st;
     cfg.attrs = attr;
-    cfg.numAttrs = l.g.ranks > 1 ? 2 : 1;
+    cfg.numAttrs = l.pdl ? 2 : 1;
     if (cudaLaunchKernelEx(&cfg, kern, l.a[0], l.b[0], l.a[1], l.b[1], l.g) != cudaSuccess) return QLORA_ERR_CUDA;
     QL_LAUNCH_CHECK();
     return QLORA_OK;
@@ -299,6 +307,17 @@ qlora_status dx_gemm(const void* W, const void* dH, int64_t dh_ld, int64_t T, in
     return launch_pair_gemm<false>(t, g, sch, pair_ws, err, st);
 }
 
+PadCopy pad_copy(const void* src, void* dst, int64_t rows, int64_t cols, int64_t ld, int most_ctas) {
+    PadCopy p{};
+    p.src = static_cast<const __nv_bfloat16*>(src);
+    p.dst = static_cast<__nv_bfloat16*>(dst);
+    p.rows = rows;
+    p.cols = static_cast<int>(cols);
+    p.ld = static_cast<int>(ld);
+    p.ctas = static_cast<int>(std::min<int64_t>(cdiv(rows * ld, 1024), most_ctas));
+    return p;
+}
+
 // ======================================================================= sequences
 
 qlora_status mx_fwd(const qlora_mxfp4* w, const void* X, int64_t T, const void* A, const void* B, int r, float s,
@@ -315,38 +334,52 @@ qlora_status mx_fwd(const qlora_mxfp4* w, const void* X, int64_t T, const void* 
     // map fills the rank padding with 0), else a padded copy
     const bool direct = r % 8 == 0;
     const void* b_src = direct ? B : at<void>(ws, p.b_pad);
-    const int b_ld = direct ? r : RP;
+    const int b_ld = pad8(r);
     // The first kernel is launched without programmatic dependent launch: whatever wrote the weight
     // and whatever used this workspace has finished before it starts.
     if (route == kMxDecode) {
         MxPrepArgs a{};
         a.X = static_cast<const bf*>(X);
         a.A = static_cast<const bf*>(A);
-        a.B = static_cast<const bf*>(B);
         a.T = static_cast<int>(T);
         a.r = r;
-        a.col_tiles = static_cast<int>(mx_col_tiles(d_in));
         a.ld_us = RP;
-        a.ld_b = RP;
         a.d_in = d_in;
-        a.d_out = d_out;
         a.s = s;
-        a.codes = codes;
-        a.scales = scales;
         a.u_save = static_cast<bf*>(U_save);
         a.us = us;
-        a.b_pad = direct ? nullptr : at<bf>(ws, p.b_pad);
-        const int pad_ctas = direct ? 0 : static_cast<int>(std::min<int64_t>(cdiv(d_out * RP, 256), kSmsForSplit));
-        k_mx_prepare<<<static_cast<unsigned>(a.col_tiles + r + pad_ctas), 256, 0, st>>>(a);
+        if (!direct) a.pad = pad_copy(B, at<void>(ws, p.b_pad), d_out, r, b_ld, kSmsForSplit);
+        k_mx_prepare<<<static_cast<unsigned>(r + a.pad.ctas), 256, 0, st>>>(a);
         QL_LAUNCH_CHECK();
     } else {
-        k_mxfp4_quantize<bf><<<static_cast<unsigned>(cdiv(T, 128) * mx_col_tiles(d_in)), 256, 0, st>>>(
-            static_cast<const bf*>(X), T, d_in, codes, scales, at<int>(ws, p.pair + p.sched.part_bytes), p.sched.n_cnt);
-        QL_LAUNCH_CHECK();
-        if (!direct)
-            QL_TRY(pad_bf16(static_cast<const bf*>(B), d_out, r, r, at<bf>(ws, p.b_pad), d_out, RP, 0, RP, st));
-        QL_TRY(compute_u_bf16(X, T, d_in, A, r, RP, r, s, p.split_u, at<float>(ws, p.part), static_cast<bf*>(U_save),
-                              nullptr, us, err, st));
+        // U = X A^T and the MXFP4 of X, in one pass over X
+        ActLaunch l;
+        l.pdl = false;
+        ActJob& ju = l.add(T, r, d_in);
+        ju.mode = kActU;
+        ju.scale = s;
+        ju.out = us;
+        ju.ld = RP;
+        ju.out2 = static_cast<bf*>(U_save);
+        const int64_t qx_tiles = cdiv(T, 128) * mx_col_tiles(d_in);
+        if (cdiv(T, 128) * 8 > kSmsForSplit / 2) {
+            ju.mx_codes = codes;
+            ju.mx_scales = scales;
+        } else {
+            // few token tiles: their CTAs (8 at most for each) would be slow at it, the other SMs are free
+            l.g.qx = static_cast<const bf*>(X);
+            l.g.qx_rows = T;
+            l.g.qx_cols = d_in;
+            l.g.qx_codes = codes;
+            l.g.qx_scales = scales;
+            l.g.qx_tiles = static_cast<int>(qx_tiles);
+        }
+        if (!direct) l.g.pad = pad_copy(B, at<void>(ws, p.b_pad), d_out, r, b_ld, kSmsForSplit / 2);
+        l.g.zero = at<int>(ws, p.pair + p.sched.part_bytes);
+        l.g.n_zero = p.sched.n_cnt;
+        QL_TRY(tmap_bf16(&l.a[0], X, T, d_in, d_in, 128));
+        QL_TRY(tmap_bf16(&l.b[0], A, r, d_in, d_in, static_cast<uint32_t>(RP)));
+        QL_TRY(act_gemm(RP, l, err, st));
     }
     if (route == kMxPair) {
         CUtensorMap t[6];
@@ -373,7 +406,8 @@ qlora_status mx_fwd(const qlora_mxfp4* w, const void* X, int64_t T, const void* 
     CUtensorMap tw, tx, tb, tu;
     const uint32_t nt = route == kMxDecode ? 16 : (route == kMxStream64 ? 64 : 128);
     QL_TRY(tmap_u8_sw128(&tw, w->codes, d_out, d_in / 2, d_in / 2, 128));
-    QL_TRY(tmap_u8_sw128(&tx, codes, T, d_in / 2, d_in / 2, nt));
+    if (route == kMxDecode) tx = tw;       // (X is quantized in the kernel)
+    else QL_TRY(tmap_u8_sw128(&tx, codes, T, d_in / 2, d_in / 2, nt));
     QL_TRY(tmap_bf16(&tb, b_src, d_out, r, b_ld, 128));
     QL_TRY(tmap_bf16(&tu, us, T, r, RP, nt));
     MxStreamArgs g{};
@@ -385,6 +419,8 @@ qlora_status mx_fwd(const qlora_mxfp4* w, const void* X, int64_t T, const void* 
     g.ext_k16_last = static_cast<int>(cdiv(r - 64 * (g.ext_steps - 1), 16));
     g.w_scales = w->scales;
     g.x_scales = scales;
+    g.X = static_cast<const bf*>(X);
+    g.d_in = d_in;
     g.out = static_cast<bf*>(H);
     g.err = err;
     g.wait_ns = kWaitNs;
@@ -437,27 +473,19 @@ qlora_status mx_bwd(MxBase base, const void* X, const qlora_act8* X8, const void
             a.zero = at<int>(ws, p.pair + p.sched.part_bytes);
             a.n_zero = p.sched.n_cnt;
         }
-        auto pad = [&](int i, const void* src, void* dst, int64_t rows, int64_t cols, int64_t ld) {
-            a.pad[i].src = static_cast<const bf*>(src);
-            a.pad[i].dst = static_cast<bf*>(dst);
-            a.pad[i].rows = rows;
-            a.pad[i].cols = static_cast<int>(cols);
-            a.pad[i].ld = static_cast<int>(ld);
-            a.pad[i].ctas = static_cast<int>(std::min<int64_t>(cdiv(rows * ld, 1024), 4 * kSmsForSplit));
-        };
         // rows that are no whole 16-byte units cannot be read by a tensor map
         if (d_out % 8) {
-            pad(0, dH, at<void>(ws, p.dh_pad), T, d_out, dh_ld);
+            a.pad[0] = pad_copy(dH, at<void>(ws, p.dh_pad), T, d_out, dh_ld, 4 * kSmsForSplit);
             dH = at<void>(ws, p.dh_pad);
         }
         if (r % 8 && grads) {
-            pad(1, B, at<void>(ws, p.b_pad), d_out, r, RP);
+            a.pad[1] = pad_copy(B, at<void>(ws, p.b_pad), d_out, r, pad8(r), kSmsForSplit);
             b_src = at<void>(ws, p.b_pad);
-            b_ld = RP;
+            b_ld = pad8(r);
             if (U_saved) {
-                pad(2, U_saved, u3, T, r, RP);
+                a.pad[2] = pad_copy(U_saved, u3, T, r, pad8(r), kSmsForSplit);
                 u_src = u3;
-                u_ld = RP;
+                u_ld = pad8(r);
             }
         }
         const int ctas = a.ctas_w + a.pad[0].ctas + a.pad[1].ctas + a.pad[2].ctas + (a.n_zero ? 1 : 0);
@@ -571,11 +599,10 @@ qlora_status mxfp4_quantize(const void* W, qlora_dtype w_dtype, int64_t rows, in
     QL_TRY(mx_check_dims(rows, cols));
     const unsigned tiles = static_cast<unsigned>(cdiv(rows, 128) * mx_col_tiles(cols));
     if (w_dtype == QLORA_F32)
-        k_mxfp4_quantize<float><<<tiles, 256, 0, stream>>>(static_cast<const float*>(W), rows, cols, codes, scales,
-                                                         nullptr, 0);
+        k_mxfp4_quantize<float><<<tiles, 256, 0, stream>>>(static_cast<const float*>(W), rows, cols, codes, scales);
     else
         k_mxfp4_quantize<__nv_bfloat16><<<tiles, 256, 0, stream>>>(static_cast<const __nv_bfloat16*>(W), rows, cols,
-                                                                   codes, scales, nullptr, 0);
+                                                                   codes, scales);
     QL_LAUNCH_CHECK();
     return QLORA_OK;
 }

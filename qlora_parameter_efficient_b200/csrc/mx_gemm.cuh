@@ -17,6 +17,7 @@
 //   operands also the backward's dX over a decoded weight.
 #pragma once
 
+#include "act8.cuh"
 #include "common.cuh"
 #include "mxfp4.cuh"
 #include "nf4_gemm2.cuh"
@@ -80,68 +81,58 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)
         : "r"(taddr));
 }
 
-// Prepare a decode-size call (T <= 16) in one launch.  CTAs [0, col_tiles): MXFP4 of X, one scale
-// tile each; [col_tiles, col_tiles + r): one adapter row j each, U[:, j] = X A[j]^T in fp32, written
-// unscaled to u_save (nullable, [T, r]) and as bf16(s U) to us [T, ld_us]; the rest: B copied to rows
-// of ld_b (only where r is not a multiple of 8 and B's rows are no whole 16-byte units).
-// s U in bf16 costs 2^-9 of the adapter term, as the rounding of H costs 2^-9 of H.
+// The adapter side of a decode-size call (T <= 16), beside which the weight stream already runs.  CTAs
+// [0, r): one adapter row j each, U[:, j] = X A[j]^T in fp32, written unscaled to u_save (nullable,
+// [T, r]) and as bf16(s U) to us [T, ld_us]; the rest: B copied to padded rows (only where r is not a
+// multiple of 8).  s U in bf16 costs 2^-8 of the adapter term, as the rounding of H costs 2^-8 of H.
 constexpr int kMxDecodeT = 16;
 struct MxPrepArgs {
-    const __nv_bfloat16 *X, *A, *B;
-    int T, r, col_tiles, ld_us, ld_b;
-    int64_t d_in, d_out;
+    const __nv_bfloat16 *X, *A;
+    int T, r, ld_us;
+    int64_t d_in;
     float s;
-    uint8_t *codes, *scales;
-    __nv_bfloat16 *u_save, *us, *b_pad;
+    __nv_bfloat16 *u_save, *us;
+    PadCopy pad;
 };
 __global__ void __launch_bounds__(256) k_mx_prepare(const MxPrepArgs a) {
-    __shared__ __align__(16) uint8_t s_sc[kMxTileBytes];
     __shared__ float s_red[8][kMxDecodeT];
     griddep_launch_dependents();
-    const int b = blockIdx.x;
-    if (b < a.col_tiles) {
-        mxfp4_quantize_tile(a.X, a.T, a.d_in, 0, b, a.codes, a.scales, s_sc);
-    } else if (b < a.col_tiles + a.r) {
-        const int j = b - a.col_tiles;
-        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-        float acc[kMxDecodeT];
+    const int j = blockIdx.x;
+    if (j >= a.r) {
+        a.pad.run(j - a.r);
+        return;
+    }
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float acc[kMxDecodeT];
 #pragma unroll
-        for (int t = 0; t < kMxDecodeT; ++t) acc[t] = 0.f;
-        for (int64_t c = threadIdx.x * 8; c < a.d_in; c += 256 * 8) {
-            float w[8], x[8];
-            load8(a.A + j * a.d_in + c, w);
-#pragma unroll
-            for (int t = 0; t < kMxDecodeT; ++t)
-                if (t < a.T) {
-                    load8(a.X + t * a.d_in + c, x);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) acc[t] = fmaf(w[i], x[i], acc[t]);
-                }
-        }
+    for (int t = 0; t < kMxDecodeT; ++t) acc[t] = 0.f;
+    for (int64_t c = threadIdx.x * 8; c < a.d_in; c += 256 * 8) {
+        float w[8];
+        load8(a.A + j * a.d_in + c, w);
 #pragma unroll
         for (int t = 0; t < kMxDecodeT; ++t)
             if (t < a.T) {
+                float x[8];
+                load8(a.X + t * a.d_in + c, x);
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], o);
-                if (lane == 0) s_red[warp][t] = acc[t];
+                for (int i = 0; i < 8; ++i) acc[t] = fmaf(w[i], x[i], acc[t]);
             }
-        __syncthreads();
-        if (threadIdx.x < a.T) {
-            const int t = threadIdx.x;
-            float u = 0.f;
+    }
 #pragma unroll
-            for (int w = 0; w < 8; ++w) u += s_red[w][t];
-            if (a.u_save) a.u_save[t * a.r + j] = __float2bfloat16_rn(u);
-            a.us[t * a.ld_us + j] = __float2bfloat16_rn(a.s * u);
+    for (int t = 0; t < kMxDecodeT; ++t)
+        if (t < a.T) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], o);
+            if (lane == 0) s_red[warp][t] = acc[t];
         }
-    } else {
-        const int64_t n = a.d_out * a.ld_b;
-        for (int64_t i = static_cast<int64_t>(b - a.col_tiles - a.r) * 256 + threadIdx.x; i < n;
-             i += static_cast<int64_t>(gridDim.x - a.col_tiles - a.r) * 256) {
-            const int64_t row = i / a.ld_b;
-            const int c = static_cast<int>(i - row * a.ld_b);
-            a.b_pad[i] = c < a.r ? a.B[row * a.r + c] : __float2bfloat16_rn(0.f);
-        }
+    __syncthreads();
+    if (threadIdx.x < a.T) {
+        const int t = threadIdx.x;
+        float u = 0.f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) u += s_red[w][t];
+        if (a.u_save) a.u_save[t * a.r + j] = __float2bfloat16_rn(u);
+        a.us[t * a.ld_us + j] = __float2bfloat16_rn(a.s * u);
     }
 }
 
@@ -153,13 +144,6 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                  : "memory");
 }
 
-__device__ __forceinline__ void st_cluster_f32(uint32_t cluster_addr, float v) {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
-}
-
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
-
 // ------------------------------------------------------------------ weight-streaming kernel
 
 struct MxStreamArgs {
@@ -170,7 +154,9 @@ struct MxStreamArgs {
     int ext_steps;            // adapter K steps of 64, taken by the last rank
     int ext_k16_last;
     const uint8_t* w_scales;
-    const uint8_t* x_scales;
+    const uint8_t* x_scales;  // MXFP4 X (NT > 16), or
+    const __nv_bfloat16* X;   // X itself (NT = 16), quantized by the CTAs that use it
+    int64_t d_in;
     __nv_bfloat16* out;       // [T, d_out]
     int* err;
     uint64_t wait_ns;
@@ -185,21 +171,27 @@ struct MxStreamCfg {
     static constexpr int kB = NT * 128;             // codes of the tokens
     static constexpr int kSf = 1024;                // two scale tiles (each operand)
     static constexpr int kStage = kA + kB + 2 * kSf;
-    // two CTAs per SM up to 64 tokens, and one above
-    static constexpr int kStages = NT <= 16 ? 5 : (NT <= 64 ? 3 : 4);
-    static constexpr int kRed = NT * 128 * 4;       // partials of this rank's share of the tokens
-    static constexpr int kTotal = 1024 + kStages * kStage + kRed + 256;
+    // two CTAs per SM
+    static constexpr int kStages = NT <= 16 ? 5 : (NT <= 64 ? 4 : 3);
+    static constexpr int kRing = kStages * kStage;
+    static constexpr int kRed = (NT + 4) * 128 * 4; // partials of this rank's share of the rows (over the ring)
+    static constexpr int kTotal = 1024 + kRing + 256;
+    static constexpr bool kQuant = NT == 16;
     static constexpr int kThreads = 192;
     static constexpr int kAcc = NT < 32 ? 32 : NT;  // accumulator columns
     static constexpr uint32_t kTmem = NT <= 32 ? 64 : (NT <= 64 ? 128 : 256);   // + 2 x 16 scale columns
     static_assert(kAcc + 32 <= static_cast<int>(kTmem), "tensor memory");
-    static_assert(kTotal * (NT <= 64 ? 2 : 1) <= 232448, "shared memory budget");
+    static_assert((kTotal + 1024) * 2 <= 233472 && kRed <= kRing, "shared memory budget");
 };
 
-// grid: x = weight tile * ranks + rank, y = token tile; clusters of `ranks` along x.
-// Launched with programmatic dependent launch: the weight's tiles are read before the kernel
-// that quantizes X has finished (that kernel is launched without it, so whatever wrote
-// the weight is done), everything else after.
+// grid: x = weight tile * ranks + rank, y = token tile; clusters of `ranks` along x (NT = 16 only: joining
+// the partials of more tokens through the cluster's shared memory costs more than the shorter K saves,
+// 44 against 20 us at 200 tokens of an 8192 x 8192 layer).
+// Launched with programmatic dependent launch: the weight's tiles are read before the kernel in front
+// (which forms U and, for NT > 16, quantizes X) has finished; that kernel is launched without it, so
+// whatever wrote the weight and X is done.  What it writes is read, and H written, after it has ended.
+// NT = 16: warps 2..5 quantize this rank's part of X into the ring themselves, one block of 32 per
+// thread and stage, so that the stream does not wait for another kernel before its last step.
 template <int NT>
 __global__ void __launch_bounds__(MxStreamCfg<NT>::kThreads)
     k_mx_stream(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
@@ -214,15 +206,15 @@ __global__ void __launch_bounds__(MxStreamCfg<NT>::kThreads)
     uint8_t* sB = sA + S * L::kA;
     uint8_t* sSa = sB + S * L::kB;
     uint8_t* sSb = sSa + S * L::kSf;
-    float* red = reinterpret_cast<float*>(sSb + S * L::kSf);
-    uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(red) + L::kRed);
+    float* red = reinterpret_cast<float*>(smem);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kRing);
     uint64_t* empty = full + S;
     uint64_t* accf = empty + S;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(accf + 1);
     volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = warp_index(), lane = threadIdx.x & 31;
-    const int C = args.ranks;
+    const int C = L::kQuant ? args.ranks : 1;
     const int rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int tile = blockIdx.x / C;
     const int n0 = tile * 128;
@@ -235,7 +227,7 @@ __global__ void __launch_bounds__(MxStreamCfg<NT>::kThreads)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
-            mbar_init(&full[s], 1);
+            mbar_init(&full[s], L::kQuant ? 5 : 1);      // the copies, and the four quantizing warps
             mbar_init(&empty[s], 1);
         }
         mbar_init(accf, 1);
@@ -254,7 +246,6 @@ __global__ void __launch_bounds__(MxStreamCfg<NT>::kThreads)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    if (C > 1) cluster_arrive();
     griddep_launch_dependents();
 
     // MMAs (K = 64) and scale tiles of main stage `it`
@@ -264,12 +255,13 @@ __global__ void __launch_bounds__(MxStreamCfg<NT>::kThreads)
         auto load_w = [&](int it, int s) {
             const int c = c_begin + it;
             const uint32_t sf = static_cast<uint32_t>((mmas_of(it) + 1) / 2) * kMxTileBytes;
-            mbar_arrive_expect_tx(&full[s], L::kA + L::kB + 2 * sf);
+            mbar_arrive_expect_tx(&full[s], L::kQuant ? L::kA + sf : L::kA + L::kB + 2 * sf);
             tma_load_2d(sA + s * L::kA, &tmW, &full[s], c * 128, n0);
             bulk_load(sSa + s * L::kSf,
                       args.w_scales + (static_cast<int64_t>(tile) * args.col_tiles + 2 * c) * kMxTileBytes, sf, &full[s]);
         };
         auto load_x = [&](int it, int s) {
+            if (L::kQuant) return;
             const int c = c_begin + it;
             const uint32_t sf = static_cast<uint32_t>((mmas_of(it) + 1) / 2) * kMxTileBytes;
             tma_load_2d(sB + s * L::kB, &tmX, &full[s], c * 128, t0);
@@ -281,10 +273,12 @@ __global__ void __launch_bounds__(MxStreamCfg<NT>::kThreads)
         if (elect_one())
             for (int it = 0; it < ahead; ++it) load_w(it, it);
         __syncwarp();
-        griddep_wait();
-        if (elect_one())
-            for (int it = 0; it < ahead; ++it) load_x(it, it);
-        __syncwarp();
+        if (!L::kQuant) {
+            griddep_wait();
+            if (elect_one())
+                for (int it = 0; it < ahead; ++it) load_x(it, it);
+            __syncwarp();
+        }
         int issued = ahead;
         for (int it = ahead, s = ahead % S, ph = ahead / S; it < n_iters; ++it) {
             if (!mbar_wait_uniform(&empty[s], ph ^ 1, abort, args.wait_ns)) {
@@ -292,6 +286,7 @@ __global__ void __launch_bounds__(MxStreamCfg<NT>::kThreads)
                 *abort = 1;
                 break;
             }
+            if (L::kQuant && it == n_main) griddep_wait();
             if (elect_one()) {
                 if (it < n_main) {
                     load_w(it, s);
@@ -363,6 +358,41 @@ __global__ void __launch_bounds__(MxStreamCfg<NT>::kThreads)
             if (++s == S) s = 0, ph ^= 1;
         }
         if (elect_one()) umma_commit(accf);
+    } else if constexpr (L::kQuant) {
+        // token `row`, block `blk` of each stage's 256 columns
+        const int td = threadIdx.x - 64, row = td >> 3, blk = td & 7;
+        const bool in = row < args.T;
+        const __nv_bfloat16* src = args.X + row * args.d_in + static_cast<int64_t>(c_begin) * 256 + blk * 32;
+        auto fetch = [&](int it, Raw8<__nv_bfloat16> (&raw)[4]) {
+            const bool there = in && it < n_main && static_cast<int64_t>(c_begin + it) * 256 + blk * 32 < args.d_in;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                if (there) raw[c].load(src + static_cast<int64_t>(it) * 256 + c * 8);
+                else raw[c].zero();
+            }
+        };
+        Raw8<__nv_bfloat16> nxt[4];
+        fetch(0, nxt);
+        for (int it = 0, s = 0, ph = 0; it < n_iters; ++it) {
+            Raw8<__nv_bfloat16> cur[4] = {nxt[0], nxt[1], nxt[2], nxt[3]};
+            fetch(it + 1, nxt);
+            if (!mbar_wait_warp(&empty[s], ph ^ 1, abort, args.wait_ns)) {
+                set_error(args.err, kErrTimeout);
+                *abort = 1;
+                break;
+            }
+            if (it < n_main) {
+                uint32_t e, q[4];
+                mxfp4_block32(cur, e, q);
+                *reinterpret_cast<uint4*>(sB + s * L::kB + row * 128 + ((blk ^ (row & 7)) << 4)) =
+                    make_uint4(q[0], q[1], q[2], q[3]);
+                sSb[s * L::kSf + (blk >> 2) * kMxTileBytes + row * 16 + (blk & 3)] = static_cast<uint8_t>(e);
+                fence_proxy_async_smem();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[s]);
+            if (++s == S) s = 0, ph ^= 1;
+        }
     }
     __syncwarp();
 
@@ -378,7 +408,7 @@ __global__ void __launch_bounds__(MxStreamCfg<NT>::kThreads)
         }
         tc_fence_after();
     }
-    if (C == 1) {
+    if (!L::kQuant || C == 1) {
         griddep_wait();          // earlier kernels of the stream may still read or write H
         if (warp >= 2 && !*abort) {
 #pragma unroll 1
@@ -393,35 +423,38 @@ __global__ void __launch_bounds__(MxStreamCfg<NT>::kThreads)
                             __float2bfloat16_rn(__uint_as_float(r[j]));
             }
         }
-    } else {
-        // rank o sums the tokens o, o + C, ... of the tile; every rank sends it its partials:
-        // red[source rank][token / C][128 rows]
-        cluster_wait();          // every rank has started (its shared memory may be written)
-        const int per = NT / C;
+    } else if constexpr (L::kQuant) {
+        // rank o sums the weight rows [o R, (o + 1) R): every rank sends it its partials of them,
+        // red[source rank][row][tokens], once every rank's MMAs are done with the ring underneath
+        constexpr int kLd = NT + 4;
+        const int R = 128 / C;
+        cluster_barrier();
         if (warp >= 2 && !*abort) {
+            const int lr = q * 32 + lane;
+            const uint32_t dst = mapa_shared(smem_u32(red + (rank * R + lr % R) * kLd), static_cast<uint32_t>(lr / R));
 #pragma unroll 1
             for (int c0 = 0; c0 < t_end; c0 += 16) {
                 uint32_t r[16];
                 tmem_ld_32x32b_x16(tbase + c0, r);
                 tmem_ld_wait();
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const int t = c0 + j;
-                    if (t < t_end)
-                        st_cluster_f32(mapa_shared(smem_u32(red + (rank * per + t / C) * 128 + q * 32 + lane),
-                                                   static_cast<uint32_t>(t % C)),
-                                       __uint_as_float(r[j]));
-                }
+                for (int g = 0; g < 4; ++g)
+                    if (c0 + 4 * g < t_end)
+                        asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + (c0 + 4 * g) * 4),
+                                     "r"(r[4 * g]), "r"(r[4 * g + 1]), "r"(r[4 * g + 2]), "r"(r[4 * g + 3])
+                                     : "memory");
             }
         }
-        cluster_arrive();
-        cluster_wait();
+        cluster_barrier();
         griddep_wait();
-        if (warp >= 2 && !*abort && row < args.d_out) {
-            for (int t = rank; t < t_end; t += C) {
+        if (warp >= 2 && !*abort) {
+            const int col0 = n0 + rank * R;
+            for (int i = threadIdx.x - 64; i < R * t_end; i += 128) {
+                const int rl = i % R, t = i / R;
                 float acc = 0.f;
-                for (int c = 0; c < C; ++c) acc += red[(c * per + t / C) * 128 + q * 32 + lane];
-                args.out[static_cast<int64_t>(t0 + t) * args.d_out + row] = __float2bfloat16_rn(acc);
+                for (int c = 0; c < C; ++c) acc += red[(c * R + rl) * kLd + t];
+                if (col0 + rl < args.d_out)
+                    args.out[static_cast<int64_t>(t0 + t) * args.d_out + col0 + rl] = __float2bfloat16_rn(acc);
             }
         }
     }

@@ -99,7 +99,24 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&x)[8]) {
     return q;
 }
 
-// One 128 x 128 scale tile of a matrix: 256 threads, sixteen lanes per row (8 elements each, four
+// MXFP4 of one whole block of 32 in one thread.
+__device__ __forceinline__ void mxfp4_block32(const Raw8<__nv_bfloat16> (&raw)[4], uint32_t& e, uint32_t (&q)[4]) {
+    float x[4][8];
+    uint32_t m = 0;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) m = max(m, raw[c].values(x[c]));
+    const uint32_t ef = m >> 23;
+    e = ef == 255u ? 255u : (ef > 2u ? ef - 2u : 0u);
+    const float inv = __uint_as_float((254u - e) << 23);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[c][i] = __fmul_rn(x[c][i], inv);
+        q[c] = e == 255u ? 0u : e2m1x8(x[c]);
+    }
+}
+
+// One 128 x 128 scale tile of a matrix: 256 threads (any more of the block stand by), sixteen lanes per row (8 elements each, four
 // lanes per block), 8 passes of 16 rows whose loads are all issued first (4 passes at a time for
 // fp32).  The tile's scales are gathered in shared memory and written once, 512 contiguous bytes.
 template <typename T>
@@ -110,6 +127,7 @@ __device__ __forceinline__ void mxfp4_quantize_tile(const T* __restrict__ X, int
     const int seg = threadIdx.x & 15, r0 = threadIdx.x >> 4;
     const int64_t col = kt * 128 + seg * 8;
     const int64_t left = col < cols ? rows - rt * 128 : 0;       // rows of this tile that exist
+    const bool mine = threadIdx.x < 256;
     const T* src = X + (rt * 128 + r0) * cols + col;
     uint8_t* dst = codes + ((rt * 128 + r0) * cols + col) / 2;
 #pragma unroll
@@ -117,7 +135,7 @@ __device__ __forceinline__ void mxfp4_quantize_tile(const T* __restrict__ X, int
         Raw8<T> raw[kBatch];
 #pragma unroll
         for (int p = 0; p < kBatch; ++p) {
-            if ((p0 + p) * 16 + r0 < left) raw[p].load(src + (p0 + p) * 16 * cols);
+            if (mine && (p0 + p) * 16 + r0 < left) raw[p].load(src + (p0 + p) * 16 * cols);
             else raw[p].zero();
         }
 #pragma unroll
@@ -130,8 +148,8 @@ __device__ __forceinline__ void mxfp4_quantize_tile(const T* __restrict__ X, int
 #pragma unroll
             for (int i = 0; i < 8; ++i) x[i] = __fmul_rn(x[i], inv);
             const uint32_t q = e == 255u ? 0u : e2m1x8(x);
-            if (lr < left) *reinterpret_cast<uint32_t*>(dst + (p0 + p) * 8 * cols) = q;
-            if ((seg & 3) == 0) s_sc[(lr & 31) * 16 + (lr >> 5) * 4 + (seg >> 2)] = lr < left ? static_cast<uint8_t>(e) : 0;
+            if (mine && lr < left) *reinterpret_cast<uint32_t*>(dst + (p0 + p) * 8 * cols) = q;
+            if (mine && (seg & 3) == 0) s_sc[(lr & 31) * 16 + (lr >> 5) * 4 + (seg >> 2)] = lr < left ? static_cast<uint8_t>(e) : 0;
         }
     }
     __syncthreads();
@@ -140,16 +158,12 @@ __device__ __forceinline__ void mxfp4_quantize_tile(const T* __restrict__ X, int
             reinterpret_cast<const uint4*>(s_sc)[threadIdx.x];
 }
 
-// zero[0, n_zero): ticket counters of a later kernel of the call, cleared on the way.
+// grid: one CTA per scale tile, column tiles fastest.
 template <typename T>
 __global__ void __launch_bounds__(256) k_mxfp4_quantize(const T* __restrict__ X, int64_t rows, int64_t cols,
-                                                        uint8_t* __restrict__ codes,
-                                                        uint8_t* __restrict__ scales, int* __restrict__ zero,
-                                                        int n_zero) {
+                                                        uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
     __shared__ __align__(16) uint8_t s_sc[kMxTileBytes];
     griddep_enter();
-    if (blockIdx.x == 0)
-        for (int i = threadIdx.x; i < n_zero; i += 256) zero[i] = 0;
     const int64_t kts = mx_col_tiles(cols);
     mxfp4_quantize_tile(X, rows, cols, blockIdx.x / kts, blockIdx.x % kts, codes, scales, s_sc);
 }
