@@ -208,13 +208,17 @@ struct ActGemmSmem {
     static constexpr int kMaxStages = 6;
     static constexpr int kAcc = 4;                              // accumulator tiles, at most
     static constexpr int kTotal = 1024 + kRing + 512;
+    // groups of eight decoding warps (one at rank > 64, whose drains need the registers)
+    static constexpr int kGroups = RPT == 64 ? 2 : 1;
+    static constexpr int kThreads = 32 * (2 + 8 * kGroups);
     static constexpr int kLdRed = RPT + 4;                      // floats per row of the joining buffer
     static_assert(kTotal <= 232448 && 128 * kLdRed * 4 <= kRing, "shared memory budget");
     static_assert(3 * (kA + kRaw + 3 * RPT / 64 * kChunk) <= kRing, "three stages at least");
 };
 
-// Warp 0: TMA; warp 1: MMA; warps 2..9: int8 decode (one 32-element block per thread and stage) and
-// accumulator drains.  A cluster's ranks split K; their sums meet in shared memory, each rank adding and
+// Warp 0: TMA; warp 1: MMA; warps 2..9 and, up to rank 64, 10..17: int8 decode or MXFP4 quantization, one
+// 32-element block per thread and stage, the groups taking pairs of stages in turn (one group alone is
+// bound by the latency of its own chain, 1100 cycles a stage); warps 2..9 also drain the accumulators.  A cluster's ranks split K; their sums meet in shared memory, each rank adding and
 // writing 128 / ranks rows in rank order, so no partial goes through memory.  Up to two products share
 // a launch (U and G; dA and dB).
 //
@@ -228,7 +232,7 @@ struct ActGemmSmem {
 // L2.  An MMA of M = 128 takes about 75 cycles however small N is (it reads its A tile), hence one of
 // N = 3 stride for a triple and not three.
 template <int RPT>
-__global__ void __launch_bounds__(320, 1)
+__global__ void __launch_bounds__(ActGemmSmem<RPT>::kThreads, 1)
     k_act_gemm(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmB0,
                const __grid_constant__ CUtensorMap tmA1, const __grid_constant__ CUtensorMap tmB1,
                const __grid_constant__ ActGemmArgs args) {
@@ -266,11 +270,11 @@ __global__ void __launch_bounds__(320, 1)
     const CUtensorMap* tmB = ji ? &tmB1 : &tmB0;
     const int m0 = (tile - (ji ? args.tiles0 : 0)) * 128;
     const bool int8 = job.int8, amn = job.amn, bmn = job.bmn;
-    // (K ranges begin at whole scale tiles of 128 columns)
-    const int64_t k_pairs = (job.k_steps + 1) / 2;
-    const int k_begin = static_cast<int>(k_pairs * rank / C) * 2;
-    const int n_iters = min(job.k_steps, static_cast<int>(k_pairs * (rank + 1) / C) * 2) - k_begin;
     const bool quant = job.mx_codes != nullptr;
+    const int unit = quant ? 2 : 1;             // K steps a range is made of (quantizing: whole scale tiles)
+    const int64_t units = (job.k_steps + unit - 1) / unit;
+    const int k_begin = static_cast<int>(units * rank / C) * unit;
+    const int n_iters = min(job.k_steps, static_cast<int>(units * (rank + 1) / C) * unit) - k_begin;
     const ActTriple tr = act_triple(job.N);
     const int terms = RPT == 64 && job.triple ? 3 : 1;         // column groups of an accumulator tile
     const int groups = RPT == 128 && job.triple ? 3 : 1;       // MMAs per 16 of K
@@ -315,14 +319,16 @@ __global__ void __launch_bounds__(320, 1)
     const uint32_t tmem = *tmem_slot;
     griddep_enter();
     if (blockIdx.x == 0)
-        for (int i = threadIdx.x; i < args.n_zero; i += 320) args.zero[i] = 0;
+        for (int i = threadIdx.x; i < args.n_zero; i += L::kThreads) args.zero[i] = 0;
 
     auto fail = [&]() {
         set_error(args.err, kErrTimeout);
         *abort = 1;
     };
     // warps 2..9: this thread's row and half of the columns
-    const int q = warp & 3, half = (warp - 2) >> 2;
+    const bool drains = warp >= 2 && warp < 10;
+    const int group = (warp - 2) >> 3;                      // of the decoding warps
+    const int q = warp & 3, half = ((warp - 2) >> 2) & 1;
     constexpr int kHalf = RPT / 2;
     float acc[kHalf];
 #pragma unroll
@@ -424,8 +430,21 @@ __global__ void __launch_bounds__(320, 1)
             if (lane == 0) mbar_arrive(&acc_free[acc_i]);
             if (++acc_i == NA) acc_i = 0, acc_ph ^= 1;
         };
+        // pairs of stages in turn
+        int s = 2 * group, ph = 0;
+        if (s >= S) s -= S, ph ^= 1;
+        auto skip = [&](int n) {
+            s += n;
+            if (s >= S) s -= S, ph ^= 1;
+        };
+        int drained = 0;
+        // after the pair at it0: the segments whose MMAs are behind it (those of the next rounds then find
+        // their accumulator tiles free)
+        auto drain_behind = [&](int it0) {
+            for (const int end = (it0 + 4) / seg_len - NA / 2; ok && drained < end && drained < n_seg; ++drained) drain();
+        };
         if (int8) {
-            const int td = threadIdx.x - 64;                      // 0..255: the int8 block of this thread
+            const int td = (threadIdx.x - 64) & 255;              // the int8 block of this thread
             const int row = amn ? td >> 2 : td >> 1;              // row of the int8 tile
             const int blk_in = amn ? td & 3 : td & 1;             // block within the row
             auto scale_at = [&](int it) -> uint32_t {
@@ -438,17 +457,17 @@ __global__ void __launch_bounds__(320, 1)
             };
             const int dst_off = amn ? (blk_in >> 1) * 8192 + row * 128 : row * 128;
             const int c0 = amn ? (blk_in & 1) * 4 : blk_in * 4, sw = row & 7;
-            // four steps' scales are in flight (a load takes longer than a step)
-            uint32_t e[4];
+            // the scales of this group's next pair are in flight while it decodes (a load takes longer than
+            // a step)
+            uint32_t e[2];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) e[u] = scale_at(u);
-            int drained = 0;
-            for (int it0 = 0, s = 0, ph = 0; ok && it0 < n_iters; it0 += 4) {
+            for (int u = 0; u < 2; ++u) e[u] = scale_at(2 * group + u);
+            for (int it0 = 2 * group; ok && it0 < n_iters; it0 += 2 * L::kGroups) {
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
+                for (int u = 0; u < 2; ++u) {
                     if (!ok || it0 + u >= n_iters) break;
                     const float st = act8_step(e[u]);
-                    e[u] = scale_at(it0 + u + 4);
+                    e[u] = scale_at(it0 + u + 2 * L::kGroups);
                     ok = mbar_wait_warp(&full[s], ph, abort, args.wait_ns);
                     if (!ok) break;
                     // (elements outside the matrix were filled with 0 by the copy)
@@ -462,53 +481,49 @@ __global__ void __launch_bounds__(320, 1)
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&decoded[s]);
-                    if (++s == S) s = 0, ph ^= 1;
+                    skip(1);
                 }
-                // one or two segments behind the decode, so that a drain does not wait for MMAs in flight
-                // and the segments of the next round find their accumulator tiles free
-                for (const int end = (it0 + 4) / seg_len - NA / 2; ok && drained < end && drained < n_seg; ++drained) drain();
+                if (L::kGroups > 1) skip(2);
+                if (drains) drain_behind(it0);
             }
-            for (; ok && drained < n_seg; ++drained) drain();
         } else if (quant) {
             // one block of 32 per thread and stage, from the swizzled operand tile
-            const int td = threadIdx.x - 64, row = td >> 1, b = td & 1, sw = row & 7;
+            const int td = (threadIdx.x - 64) & 255, row = td >> 1, b = td & 1, sw = row & 7;
             const int64_t grow = static_cast<int64_t>(m0) + row;
             const bool in = grow < job.M;
             uint8_t* codes = job.mx_codes + grow * (job.K / 2) + b * 16;
-            // the scale word of (row, two stages): its tile advances by 512 bytes every other stage
+            // a pair of stages fills one scale word of the row; its tile advances by 512 bytes with the pair
             uint8_t* word = job.mx_scales + mx_scale_offset(grow, k_begin * 2, mx_col_tiles(job.K));
-            uint32_t e_word = 0;
-            int drained = 0;
-            for (int it = 0, s = 0, ph = 0; ok && it < n_iters; ++it) {
-                ok = mbar_wait_warp(&full[s], ph, abort, args.wait_ns);
-                if (!ok) break;
-                const uint8_t* src = sA + s * L::kA + row * 128;
-                Raw8<__nv_bfloat16> raw[4];
+            for (int it0 = 2 * group; ok && it0 < n_iters; it0 += 2 * L::kGroups) {
+                uint32_t e_word = 0;
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    raw[c].v = *reinterpret_cast<const uint4*>(src + (((4 * b + c) ^ sw) << 4));
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&empty[s]);       // the tile has been read
-                uint32_t e, q[4];
-                mxfp4_block32(raw, e, q);
-                if (in) *reinterpret_cast<uint4*>(codes + static_cast<int64_t>(k_begin + it) * 32) = make_uint4(q[0], q[1], q[2], q[3]);
-                e |= __shfl_xor_sync(0xffffffffu, e, 1) << 8;        // (of the even lane: both blocks' bytes)
-                e_word |= e << (16 * (it & 1));
-                if ((it & 1) || it == n_iters - 1) {
-                    if (in && b == 0) *reinterpret_cast<uint32_t*>(word + (it >> 1) * kMxTileBytes) = e_word;
-                    e_word = 0;
+                for (int u = 0; u < 2; ++u) {
+                    if (!ok || it0 + u >= n_iters) break;
+                    ok = mbar_wait_warp(&full[s], ph, abort, args.wait_ns);
+                    if (!ok) break;
+                    const uint8_t* src = sA + s * L::kA + row * 128;
+                    Raw8<__nv_bfloat16> raw[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        raw[c].v = *reinterpret_cast<const uint4*>(src + (((4 * b + c) ^ sw) << 4));
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&empty[s]);       // the tile has been read
+                    uint32_t e, v[4];
+                    mxfp4_block32(raw, e, v);
+                    if (in)
+                        *reinterpret_cast<uint4*>(codes + static_cast<int64_t>(k_begin + it0 + u) * 32) =
+                            make_uint4(v[0], v[1], v[2], v[3]);
+                    e |= __shfl_xor_sync(0xffffffffu, e, 1) << 8;        // (of the even lane: both blocks' bytes)
+                    e_word |= e << (16 * u);
+                    skip(1);
                 }
-                if (++s == S) s = 0, ph ^= 1;
-                // two segments behind, so that no drain waits for MMAs in flight
-                if ((it + 1) % seg_len == 0 && (it + 1) / seg_len - 2 > drained) {
-                    drain();
-                    ++drained;
-                }
+                if (ok && in && b == 0) *reinterpret_cast<uint32_t*>(word + (it0 >> 1) * kMxTileBytes) = e_word;
+                if (L::kGroups > 1) skip(2);
+                if (drains) drain_behind(it0);
             }
-            for (; ok && drained < n_seg; ++drained) drain();
-        } else {
-            for (int g = 0; ok && g < n_seg; ++g) drain();
         }
+        if (drains)
+            for (; ok && drained < n_seg; ++drained) drain();
         if (!ok) fail();
     }
     __syncwarp();
@@ -520,7 +535,7 @@ __global__ void __launch_bounds__(320, 1)
     if (C > 1) cluster_barrier();
     else __syncthreads();
     const bool dead = *abort != 0;
-    if (warp >= 2 && !dead) {
+    if (drains && !dead) {
         const int row = q * 32 + lane;
         const uint32_t dst = mapa_shared(smem_u32(smem), static_cast<uint32_t>(C > 1 ? row / R : 0)) +
                              static_cast<uint32_t>(((rank * R + row % R) * L::kLdRed + half * kHalf) * 4);
@@ -533,7 +548,7 @@ __global__ void __launch_bounds__(320, 1)
     }
     if (C > 1) cluster_barrier();
     else __syncthreads();
-    if (warp >= 2 && !dead) {
+    if (drains && !dead) {
         const float* red = reinterpret_cast<const float*>(smem);
         const int row0 = m0 + rank * R;
         const int rows = min(R, job.M - row0);

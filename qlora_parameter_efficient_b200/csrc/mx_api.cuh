@@ -205,10 +205,10 @@ qlora_status launch_act_gemm(ActLaunch& l, int* err, cudaStream_t st) {
     int steps = 1 << 30;
     for (int i = 0; i < l.n; ++i) {
         tiles += cdiv(l.g.job[i].M, 128);
-        steps = std::min(steps, l.g.job[i].k_steps);
+        steps = std::min(steps, l.g.job[i].mx_codes ? (l.g.job[i].k_steps + 1) / 2 : l.g.job[i].k_steps);
     }
     double best = 0;
-    for (int c = 1; c <= 8 && 2 * c <= steps + 1; c *= 2) {
+    for (int c = 1; c <= 8 && c <= steps; c *= 2) {
         // one wave ends with its longest CTA; several end, on average, half a CTA after an even share
         double total = 0, longest = 0;
         for (int i = 0; i < l.n; ++i) {
@@ -238,7 +238,7 @@ qlora_status launch_act_gemm(ActLaunch& l, int* err, cudaStream_t st) {
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(tiles * l.g.ranks + l.g.qx_ctas + l.g.pad.ctas));
-    cfg.blockDim = dim3(320);
+    cfg.blockDim = dim3(L::kThreads);
     cfg.dynamicSmemBytes = L::kTotal;
     cfg.stream = st;
     cfg.attrs = attr;
