@@ -142,7 +142,16 @@ enum : int {
     kActTriple = 0,   // scale D as three bf16 terms (ActTriple layout)
     kActCols = 1,     // fp32 out[j, m] = scale D[m, j]  (dA)
     kActRows = 2,     // fp32 out[m, j] = scale D[m, j]  (dB)
-    kActU = 3         // bf16 out[m, j] = scale D[m, j] (row stride ld) and out2[m, j] = D[m, j] (nullable)
+    kActU = 3,        // bf16 out[m, j] = scale D[m, j] (row stride ld) and out2[m, j] = D[m, j] (nullable)
+    kActDx = 4        // bf16 out[j, m] = D[m, j]  (dX of few tokens)
+};
+
+// How the A operand is stored; all but bf16 are decoded to it in shared memory.
+enum : int {
+    kOpBf16 = 0,
+    kOpInt8 = 1,      // 8-bit checkpoint
+    kOpMxfp4 = 2,     // the weight of a backward for few tokens, [K, M] (its rows are K)
+    kOpNf4 = 3
 };
 
 // One product of a launch: D[M, N] = sum over K of A[M, K] B[N, K], B bf16 or a bf16 triple.
@@ -150,12 +159,15 @@ struct ActJob {
     int M, N;                // output rows (channels or tokens) and columns (the rank)
     int64_t K;               // contraction length
     int k_steps;             // ceil(K / 64)
-    int int8;                // A is int8 with E8M0 scales, decoded to bf16 in shared memory (else bf16)
+    int op;                  // how A is stored
     int amn;                 // A is stored [K, M] (tokens are K) and consumed MN-major, else [M, K]
     int bmn;                 // B is stored [K, N], else [N, K]
     int triple;              // B is an ActTriple (bmn only)
-    const uint8_t* scales;   // E8M0 bytes of the int8 operand, row-major
-    int64_t ld_scales;       // blocks per stored row
+    const uint8_t* scales;   // E8M0 bytes (int8: row-major, MXFP4: tiled) or NF4's uint8 constants
+    const float* c2;         // NF4's group constants
+    int64_t ld_scales;       // scales per stored row (MXFP4: scale tiles)
+    int n_tiles;             // tiles of RPT columns of D
+    int ext_steps;           // kActDx: the adapter's K steps of 64, taken by the last rank
     int mode;
     float scale;
     int accumulate;          // kActCols, kActRows: add to out
@@ -192,8 +204,6 @@ struct ActGemmArgs {
     const __nv_bfloat16* qx;
     int64_t qx_rows, qx_cols;
     uint8_t *qx_codes, *qx_scales;
-    int* zero;               // ticket counters of a later kernel of the call, cleared by CTA 0
-    int n_zero;
     int* err;
     uint64_t wait_ns;
 };
@@ -229,13 +239,14 @@ struct ActGemmSmem {
 // 16 or 24 MMAs, whose sums warps 2..9 add up in registers, rounding to nearest, from two to four
 // accumulator tiles in turn.
 // Bound by memory: a K step of 64 reads 8 KB of int8 (or 16 KB of bf16) from HBM and the B tiles from
-// L2.  An MMA of M = 128 takes about 75 cycles however small N is (it reads its A tile), hence one of
+// L2.  With few tokens dX^T = W^T dH^T is such a product too (kActDx): M = d_in, N = tokens, the weight
+// decoded once per CTA and split along d_out over the SMs.  An MMA of M = 128 takes about 75 cycles however small N is (it reads its A tile), hence one of
 // N = 3 stride for a triple and not three.
 template <int RPT>
 __global__ void __launch_bounds__(ActGemmSmem<RPT>::kThreads, 1)
     k_act_gemm(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmB0,
                const __grid_constant__ CUtensorMap tmA1, const __grid_constant__ CUtensorMap tmB1,
-               const __grid_constant__ ActGemmArgs args) {
+               const __grid_constant__ ActGemmArgs args) {      // (kActDx: tmA1, tmB1 are the adapter's)
     using L = ActGemmSmem<RPT>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -268,25 +279,30 @@ __global__ void __launch_bounds__(ActGemmSmem<RPT>::kThreads, 1)
     const ActJob& job = args.job[ji];
     const CUtensorMap* tmA = ji ? &tmA1 : &tmA0;
     const CUtensorMap* tmB = ji ? &tmB1 : &tmB0;
-    const int m0 = (tile - (ji ? args.tiles0 : 0)) * 128;
-    const bool int8 = job.int8, amn = job.amn, bmn = job.bmn;
+    const int tj = tile - (ji ? args.tiles0 : 0);
+    const int m0 = tj / job.n_tiles * 128, n0 = tj % job.n_tiles * RPT;
+    const int N = min(RPT, job.N - n0);         // columns of this tile
+    const int op = job.op;
+    const bool dec = op != kOpBf16, amn = job.amn, bmn = job.bmn;
     const bool quant = job.mx_codes != nullptr;
     const int unit = quant ? 2 : 1;             // K steps a range is made of (quantizing: whole scale tiles)
     const int64_t units = (job.k_steps + unit - 1) / unit;
     const int k_begin = static_cast<int>(units * rank / C) * unit;
-    const int n_iters = min(job.k_steps, static_cast<int>(units * (rank + 1) / C) * unit) - k_begin;
+    const int n_main = min(job.k_steps, static_cast<int>(units * (rank + 1) / C) * unit) - k_begin;
+    const int n_iters = n_main + (rank == C - 1 ? job.ext_steps : 0);
     const ActTriple tr = act_triple(job.N);
     const int terms = RPT == 64 && job.triple ? 3 : 1;         // column groups of an accumulator tile
     const int groups = RPT == 128 && job.triple ? 3 : 1;       // MMAs per 16 of K
-    const int n_mma = terms == 3 ? 3 * tr.stride : (job.N + 15) & ~15;
+    const int n_mma = terms == 3 ? 3 * tr.stride : (N + 15) & ~15;
     const int chunks = job.triple ? tr.ld / 64 : RPT / 64;     // of the B tile
     const int acc_cols = terms == 3 ? tr.ld : RPT;
     const int NA = min(L::kAcc, 512 / acc_cols);               // accumulator tiles
     const int seg_len = groups == 3 ? 2 : 4;                   // K steps of 64 per accumulator segment
     const int n_seg = (n_iters + seg_len - 1) / seg_len;
-    // ring: A tiles, B tiles, int8 tiles
+    // ring: A tiles, B tiles, tiles as stored
     const int b_bytes = chunks * L::kChunk;
-    const int stage = L::kA + b_bytes + (int8 ? L::kRaw : 0);
+    const int raw_bytes = op == kOpInt8 ? L::kRaw : dec ? L::kRaw / 2 : 0;
+    const int stage = L::kA + b_bytes + raw_bytes;
     const int S = min(L::kMaxStages, L::kRing / stage);
     uint8_t* sA = smem;
     uint8_t* sB = sA + S * L::kA;
@@ -318,8 +334,6 @@ __global__ void __launch_bounds__(ActGemmSmem<RPT>::kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     griddep_enter();
-    if (blockIdx.x == 0)
-        for (int i = threadIdx.x; i < args.n_zero; i += L::kThreads) args.zero[i] = 0;
 
     auto fail = [&]() {
         set_error(args.err, kErrTimeout);
@@ -336,27 +350,38 @@ __global__ void __launch_bounds__(ActGemmSmem<RPT>::kThreads, 1)
 
     if (warp == 0) {
         int issued = 0;
-        const uint32_t bytes = (int8 ? L::kRaw : L::kA) + b_bytes;
         for (int it = 0, s = 0, ph = 0; it < n_iters; ++it) {
             if (!mbar_wait_uniform(&empty[s], ph ^ 1, abort, args.wait_ns)) {
                 fail();
                 break;
             }
-            const int kx = (k_begin + it) * 64;
-            uint8_t* a = int8 ? sR + s * L::kRaw : sA + s * L::kA;
+            uint8_t* a = sA + s * L::kA;
             uint8_t* dst = sB + s * b_bytes;
             if (elect_one()) {
-                mbar_arrive_expect_tx(&full[s], bytes);
-                if (amn) {
-                    tma_load_2d(a, tmA, &full[s], m0, kx);
-                    if (!int8) tma_load_2d(a + 8192, tmA, &full[s], m0 + 64, kx);
+                if (it < n_main) {
+                    const int kx = (k_begin + it) * 64;
+                    mbar_arrive_expect_tx(&full[s], (dec ? raw_bytes : L::kA) + b_bytes);
+                    if (op == kOpInt8) {
+                        tma_load_2d(sR + s * raw_bytes, tmA, &full[s], amn ? m0 : kx, amn ? kx : m0);
+                    } else if (dec) {
+                        tma_load_2d(sR + s * raw_bytes, tmA, &full[s], m0 / 2, kx);
+                    } else if (amn) {
+                        tma_load_2d(a, tmA, &full[s], m0, kx);
+                        tma_load_2d(a + 8192, tmA, &full[s], m0 + 64, kx);
+                    } else {
+                        tma_load_2d(a, tmA, &full[s], kx, m0);
+                    }
+                    if (bmn) {
+                        for (int c = 0; c < chunks; ++c) tma_load_2d(dst + c * L::kChunk, tmB, &full[s], c * 64, kx);
+                    } else {
+                        tma_load_2d(dst, tmB, &full[s], kx, n0);
+                    }
                 } else {
-                    tma_load_2d(a, tmA, &full[s], kx, m0);
-                }
-                if (bmn) {
-                    for (int c = 0; c < chunks; ++c) tma_load_2d(dst + c * L::kChunk, tmB, &full[s], c * 64, kx);
-                } else {
-                    tma_load_2d(dst, tmB, &full[s], kx, 0);
+                    const int kx = (it - n_main) * 64;
+                    mbar_arrive_expect_tx(&full[s], L::kA + b_bytes);
+                    tma_load_2d(a, &tmA1, &full[s], m0, kx);
+                    tma_load_2d(a + 8192, &tmA1, &full[s], m0 + 64, kx);
+                    tma_load_2d(dst, &tmB1, &full[s], kx, n0);
                 }
             }
             __syncwarp();
@@ -375,8 +400,8 @@ __global__ void __launch_bounds__(ActGemmSmem<RPT>::kThreads, 1)
         for (int it = 0, s = 0, ph = 0; it < n_iters; ++it) {
             bool ok = true;
             if (in_seg == 0) ok = mbar_wait_uniform(&acc_free[acc_i], acc_ph, abort, args.wait_ns);
-            if (ok) ok = mbar_wait_uniform(int8 ? &decoded[s] : &full[s], ph, abort, args.wait_ns);
-            if (ok && int8) ok = mbar_wait_uniform(&full[s], ph, abort, args.wait_ns);
+            if (ok && dec) ok = mbar_wait_uniform(&decoded[s], ph, abort, args.wait_ns);
+            if (ok) ok = mbar_wait_uniform(&full[s], ph, abort, args.wait_ns);
             if (!ok) {
                 fail();
                 break;
@@ -415,7 +440,7 @@ __global__ void __launch_bounds__(ActGemmSmem<RPT>::kThreads, 1)
             const uint32_t t = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc_i * acc_cols + half * kHalf;
 #pragma unroll
             for (int c = 0; c < kHalf; c += 32)
-                if (half * kHalf + c < job.N) {
+                if (half * kHalf + c < N) {
                     // the smallest terms first (columns past a group are the next one's: never used)
                     for (int k = terms - 1; k >= 0; --k) {
                         uint32_t r[32];
@@ -443,7 +468,62 @@ __global__ void __launch_bounds__(ActGemmSmem<RPT>::kThreads, 1)
         auto drain_behind = [&](int it0) {
             for (const int end = (it0 + 4) / seg_len - NA / 2; ok && drained < end && drained < n_seg; ++drained) drain();
         };
-        if (int8) {
+        if (op >= kOpMxfp4) {
+            // 32 columns of one weight row per thread and stage (the adapter's steps need no decode)
+            const int td = (threadIdx.x - 64) & 255, row = td >> 2, blk_in = td & 3, sw = row & 7;
+            const int64_t mblk = m0 / 32 + blk_in;
+            uint32_t e[2] = {0, 0};
+            float c2[2] = {0.f, 0.f};
+            auto fetch = [&](int it, uint32_t& ev, float& cv) {
+                const int64_t wrow = static_cast<int64_t>(k_begin + it) * 64 + row;
+                if (it >= n_main || wrow >= job.K || mblk * 32 >= job.M) return;
+                if (op == kOpMxfp4) {
+                    ev = __ldg(job.scales + mx_scale_offset(wrow, mblk, job.ld_scales));
+                } else {
+                    const int64_t blk = wrow * job.ld_scales + mblk / 2;
+                    ev = __ldg(job.scales + blk);
+                    cv = __ldg(job.c2 + blk / kGroup);
+                }
+            };
+            const int dst_off = (blk_in >> 1) * 8192 + row * 128, c0 = (blk_in & 1) * 4;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) fetch(2 * group + u, e[u], c2[u]);
+            for (int it0 = 2 * group; ok && it0 < n_iters; it0 += 2 * L::kGroups) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    if (!ok || it0 + u >= n_iters) break;
+                    const uint32_t ev = e[u];
+                    const float cv = c2[u];
+                    fetch(it0 + u + 2 * L::kGroups, e[u], c2[u]);
+                    ok = mbar_wait_warp(&full[s], ph, abort, args.wait_ns);
+                    if (!ok) break;
+                    if (it0 + u < n_main) {
+                        // (codes outside the weight are 0: the value 0 in MXFP4; NF4's is not, but meets only
+                        // rows of dH that are 0 or columns past d_in)
+                        const uint4 q = *reinterpret_cast<const uint4*>(sR + s * raw_bytes + row * 64 + blk_in * 16);
+                        const uint32_t qs[4] = {q.x, q.y, q.z, q.w};
+                        uint8_t* dst = sA + s * L::kA + dst_off;
+                        if (op == kOpMxfp4) {
+                            const float sc = e8m0_value(ev);
+#pragma unroll
+                            for (int c = 0; c < 4; ++c)
+                                *reinterpret_cast<uint4*>(dst + (((c0 + c) ^ sw) << 4)) = e2m1_scale8_bf16(qs[c], sc);
+                        } else {
+                            const Nf4Planes pl = nf4_make_planes(nf4_block_scale(ev, cv));
+#pragma unroll
+                            for (int c = 0; c < 4; ++c)
+                                *reinterpret_cast<uint4*>(dst + (((c0 + c) ^ sw) << 4)) = nf4_decode8(qs[c], pl);
+                        }
+                        fence_proxy_async_smem();
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&decoded[s]);
+                    skip(1);
+                }
+                if (L::kGroups > 1) skip(2);
+                if (drains) drain_behind(it0);
+            }
+        } else if (op == kOpInt8) {
             const int td = (threadIdx.x - 64) & 255;              // the int8 block of this thread
             const int row = amn ? td >> 2 : td >> 1;              // row of the int8 tile
             const int blk_in = amn ? td & 3 : td & 1;             // block within the row
@@ -541,7 +621,7 @@ __global__ void __launch_bounds__(ActGemmSmem<RPT>::kThreads, 1)
                              static_cast<uint32_t>(((rank * R + row % R) * L::kLdRed + half * kHalf) * 4);
 #pragma unroll
         for (int j = 0; j < kHalf; j += 4)
-            if (half * kHalf + j < job.N)
+            if (half * kHalf + j < N)
                 asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(dst + j * 4), "f"(acc[j]),
                              "f"(acc[j + 1]), "f"(acc[j + 2]), "f"(acc[j + 3])
                              : "memory");
@@ -552,14 +632,19 @@ __global__ void __launch_bounds__(ActGemmSmem<RPT>::kThreads, 1)
         const float* red = reinterpret_cast<const float*>(smem);
         const int row0 = m0 + rank * R;
         const int rows = min(R, job.M - row0);
-        const int N = job.N;
         auto total = [&](int rl, int j) {
             float v = 0.f;
             for (int c = 0; c < C; ++c) v += red[(c * R + rl) * L::kLdRed + j];
-            return job.mode == kActU ? v : job.scale * v;
+            return job.mode == kActU || job.mode == kActDx ? v : job.scale * v;
         };
         const int td = threadIdx.x - 64;
-        if (job.mode == kActTriple) {
+        if (job.mode == kActDx) {
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(job.out);
+            for (int i = td; i < R * N; i += 256) {
+                const int j = i / R, rl = i % R;
+                if (rl < rows) out[static_cast<int64_t>(n0 + j) * job.M + row0 + rl] = __float2bfloat16_rn(total(rl, j));
+            }
+        } else if (job.mode == kActTriple) {
             __nv_bfloat16* out = static_cast<__nv_bfloat16*>(job.out) + static_cast<int64_t>(row0) * tr.ld;
             for (int i = td; i < rows * tr.stride; i += 256) {
                 const int rl = i / tr.stride, j = i % tr.stride;
@@ -604,10 +689,11 @@ __global__ void __launch_bounds__(ActGemmSmem<RPT>::kThreads, 1)
     }
 }
 
-// Everything a backward has to lay out before its products, in one launch: the weight decoded to bf16
-// (MXFP4 or NF4, eight elements per thread), and copies of matrices whose rows are no whole 16-byte
-// units to zero-padded rows (dH, B, a given U); the last CTA clears the ticket counters.  Each part
-// has its own range of CTAs.
+// What a backward has to lay out before its products: the weight decoded to bf16 (MXFP4 or NF4, eight
+// elements per thread), copies of matrices whose rows are no whole 16-byte units to zero-padded rows (dH, B,
+// a given U), and cleared ticket counters.  Each part has its own range of CTAs.  It reads nothing that the
+// kernel in front writes and writes nothing that it reads, so it runs beside it and waits for it last: a
+// kernel behind then still finds both finished.
 struct BwdPrepArgs {
     const uint8_t* codes;
     const uint8_t* mx_scales;     // MXFP4 weight, or
@@ -651,6 +737,7 @@ __global__ void __launch_bounds__(256) k_bwd_prepare(const __grid_constant__ Bwd
                                                        ? e2m1_scale8_bf16(q[u], e8m0_value(e[u]))
                                                        : nf4_decode8(q[u], nf4_make_planes(nf4_block_scale(e[u], c[u])));
         }
+        griddep_wait();
         return;
     }
     b -= a.ctas_w;
@@ -661,6 +748,7 @@ __global__ void __launch_bounds__(256) k_bwd_prepare(const __grid_constant__ Bwd
     }
     if (b == 0)
         for (int i = threadIdx.x; i < a.n_zero; i += 256) a.zero[i] = 0;
+    griddep_wait();
 }
 
 }  // namespace qlora

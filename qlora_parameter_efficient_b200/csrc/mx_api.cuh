@@ -10,6 +10,7 @@ namespace {
 constexpr int pad8(int64_t n) { return static_cast<int>((n + 7) / 8 * 8); }   // whole 16-byte units of bf16
 constexpr int64_t kMaxDim = 1LL << 30;
 constexpr int64_t kMxStreamMaxT = 512;
+constexpr int64_t kDxFewT = 128;
 
 qlora_status mx_check_dims(int64_t rows, int64_t cols) {
     if (rows < 1 || rows > kMaxDim || cols < 64 || cols % 64 || cols > kMaxDim) return QLORA_ERR_UNSUPPORTED;
@@ -36,26 +37,38 @@ MxRoute mx_route(int64_t T) {
     return T <= kMxStreamMaxT ? kMxStream128 : kMxPair;
 }
 
-// Schedule of k_pair_gemm: pairs of SMs; the tiles of an incomplete last wave are split along K over
-// as many pairs as the wave has for each, up to 8 and with at least min_steps stages a part.
+// Schedule of k_pair_gemm: pairs of SMs, tiles of 256 x 256 or (bf16) 256 x 128, and how many ways the tiles
+// of an incomplete last wave are split along K: the shortest by the measured costs in microseconds.  A bf16
+// stage takes 0.27 on a 256-wide tile and 0.2 on a 128-wide one, joining two parts 7 (4) and each further
+// part 1.  An MXFP4 tile is done in 5 to 20 us and is never split (4096^3: 49.9 us whole, 56.5 us with
+// its last wave split in two).
 struct PairSched {
-    int pairs = 1, tail = 0, split = 1;
+    int bn = 256, pairs = 1, tail = 0, split = 1;
     size_t part_bytes = 0;
     int n_cnt = 0;
     size_t bytes() const { return part_bytes + align256(static_cast<size_t>(n_cnt) * sizeof(int)); }
 };
-PairSched pair_schedule(int64_t M, int64_t N, int64_t k_steps, int64_t min_steps) {
+PairSched pair_schedule(int64_t M, int64_t N, int64_t k_steps, bool mx) {
     PairSched g;
-    const int64_t tiles = cdiv(M, 256) * cdiv(N, 256), slots = kSmsForSplit / 2;
-    const int64_t rem = tiles % slots;
-    int64_t split = rem ? std::min<int64_t>(8, std::min(slots / rem, k_steps / min_steps)) : 1;
-    if (split < 1) split = 1;
-    g.split = static_cast<int>(split);
-    g.tail = split > 1 ? static_cast<int>(rem) : 0;
-    g.pairs = static_cast<int>(tiles >= slots ? slots : rem * split);
-    if (split > 1) {
-        g.part_bytes = static_cast<size_t>(rem) * 8 * split * 2048 * 16;
-        g.n_cnt = static_cast<int>(rem) * 8;
+    const int64_t slots = kSmsForSplit / 2;
+    double best = 0;
+    for (int bn = 256; bn >= (mx ? 256 : 128); bn -= 128) {
+        const int64_t tiles = cdiv(M, 256) * cdiv(N, bn), whole = tiles / slots, rem = tiles % slots;
+        const double step = bn == 256 ? 0.27 : 0.2, join = bn == 256 ? 5 : 2;
+        for (int c = 1; c <= (rem && !mx ? kPairMaxSplit : 1); ++c) {
+            if (c > 1 && (c * rem > slots || c > k_steps)) break;
+            const double t = step * static_cast<double>(k_steps * whole + (rem ? cdiv(k_steps, c) : 0)) + (c > 1 ? join + c : 0);
+            if (best > 0 && t >= best) continue;
+            best = t;
+            g.bn = bn;
+            g.split = c;
+            g.tail = c > 1 ? static_cast<int>(rem) : 0;
+            g.pairs = static_cast<int>(whole ? slots : rem * c);
+        }
+    }
+    if (g.split > 1) {
+        g.part_bytes = static_cast<size_t>(g.tail) * 8 * g.split * (g.bn * 8) * 16;
+        g.n_cnt = g.tail * 8;
     }
     return g;
 }
@@ -70,7 +83,7 @@ int mx_ranks(int64_t tiles, int64_t chunks) {
 
 struct MxFwdPlan {
     int RP = 0;
-    size_t codes = 0, scales = 0, us = 0, b_pad = 0, pair = 0, total = 0;
+    size_t codes = 0, scales = 0, us = 0, b_pad = 0, total = 0;
     PairSched sched;
 };
 MxFwdPlan mx_fwd_plan(int64_t T, int64_t d_out, int64_t d_in, int r) {
@@ -89,8 +102,7 @@ MxFwdPlan mx_fwd_plan(int64_t T, int64_t d_out, int64_t d_in, int r) {
     p.us = take(static_cast<size_t>(T) * p.RP * 2);
     if (r % 8) p.b_pad = take(static_cast<size_t>(d_out) * pad8(r) * 2);
     if (mx_route(T) == kMxPair) {
-        p.sched = pair_schedule(T, d_out, cdiv(d_in, 256), 2);
-        p.pair = take(p.sched.bytes());
+        p.sched = pair_schedule(T, d_out, cdiv(d_in, 256), true);
     }
     p.total = off;
     return p;
@@ -116,9 +128,11 @@ MxBwdPlan mx_bwd_plan(int64_t T, int64_t d_out, int64_t d_in, int r) {
     const size_t triple = static_cast<size_t>(T) * act_triple(r).ld * 2;
     p.u3 = take(triple);           // U and s G, three bf16 terms each (or a given U in padded rows)
     p.g3 = take(triple);
-    p.w = take(static_cast<size_t>(d_out) * d_in * 2);      // the decoded weight
-    p.sched = pair_schedule(T, d_in, cdiv(d_out, 64), 8);
-    p.pair = take(p.sched.bytes());
+    if (T > kDxFewT) {
+        p.w = take(static_cast<size_t>(d_out) * d_in * 2);  // the decoded weight
+        p.sched = pair_schedule(T, d_in, cdiv(d_out, 64), false);
+        p.pair = take(p.sched.bytes());
+    }
     p.total = off;
     return p;
 }
@@ -187,6 +201,7 @@ struct ActLaunch {
         j.N = N;
         j.K = K;
         j.k_steps = static_cast<int>(cdiv(K, 64));
+        j.n_tiles = 1;
         j.scale = 1.f;
         return j;
     }
@@ -197,14 +212,14 @@ qlora_status launch_act_gemm(ActLaunch& l, int* err, cudaStream_t st) {
     auto kern = k_act_gemm<RPT>;
     static std::atomic<uint64_t> configured{0};
     QL_TRY(allow_smem(kern, L::kTotal, configured));
-    if (l.n == 1) {
+    if (l.n == 1 && !l.g.job[0].ext_steps) {
         l.a[1] = l.a[0];
         l.b[1] = l.b[0];
     }
     int64_t tiles = 0;
     int steps = 1 << 30;
     for (int i = 0; i < l.n; ++i) {
-        tiles += cdiv(l.g.job[i].M, 128);
+        tiles += cdiv(l.g.job[i].M, 128) * l.g.job[i].n_tiles;
         steps = std::min(steps, l.g.job[i].mx_codes ? (l.g.job[i].k_steps + 1) / 2 : l.g.job[i].k_steps);
     }
     double best = 0;
@@ -213,8 +228,8 @@ qlora_status launch_act_gemm(ActLaunch& l, int* err, cudaStream_t st) {
         double total = 0, longest = 0;
         for (int i = 0; i < l.n; ++i) {
             const ActJob& j = l.g.job[i];
-            const double one = cdiv(j.k_steps, c) * ((j.int8 || j.mx_codes) ? 1.8 : j.triple ? 1.3 : 1.0) + 8;
-            total += one * cdiv(j.M, 128) * c;
+            const double one = cdiv(j.k_steps, c) * ((j.op != kOpBf16 || j.mx_codes) ? 1.8 : j.triple ? 1.3 : 1.0) + 8;
+            total += one * cdiv(j.M, 128) * j.n_tiles * c;
             longest = std::max(longest, one);
         }
         const double cost = tiles * c <= kSmsForSplit ? longest : total / kSmsForSplit + longest / 2;
@@ -223,7 +238,7 @@ qlora_status launch_act_gemm(ActLaunch& l, int* err, cudaStream_t st) {
             l.g.ranks = c;
         }
     }
-    l.g.tiles0 = static_cast<int>(cdiv(l.g.job[0].M, 128));
+    l.g.tiles0 = static_cast<int>(cdiv(l.g.job[0].M, 128) * l.g.job[0].n_tiles);
     l.g.tiles = static_cast<int>(tiles);
     l.g.pad.ctas = static_cast<int>(cdiv(l.g.pad.ctas, l.g.ranks)) * l.g.ranks;
     l.g.qx_ctas = static_cast<int>(cdiv(l.g.qx_tiles, l.g.ranks)) * l.g.ranks;
@@ -247,23 +262,26 @@ qlora_status launch_act_gemm(ActLaunch& l, int* err, cudaStream_t st) {
     QL_LAUNCH_CHECK();
     return QLORA_OK;
 }
-qlora_status act_gemm(int RP, ActLaunch& l, int* err, cudaStream_t st) {
-    return RP == 64 ? launch_act_gemm<64>(l, err, st) : launch_act_gemm<128>(l, err, st);
+qlora_status act_gemm(int rpt, ActLaunch& l, int* err, cudaStream_t st) {
+    return rpt == 64 ? launch_act_gemm<64>(l, err, st) : launch_act_gemm<128>(l, err, st);
 }
 
-template <bool MX>
+template <bool MX, int BN>
 qlora_status launch_pair_gemm(const CUtensorMap (&t)[6], PairGemmArgs g, const PairSched& sch, void* ws, int* err,
                               cudaStream_t st) {
-    using L = PairGemmSmem<MX>;
+    using L = PairGemmSmem<MX, BN>;
+    auto kern = k_pair_gemm<MX, BN>;
     g.split = sch.split;
     g.tail_tiles = sch.tail;
-    g.part = static_cast<float*>(ws);
-    g.cnt = reinterpret_cast<int*>(static_cast<uint8_t*>(ws) + sch.part_bytes);
+    if (sch.split > 1) {
+        g.part = static_cast<float*>(ws);
+        g.cnt = reinterpret_cast<int*>(static_cast<uint8_t*>(ws) + sch.part_bytes);
+    }
     g.err = err;
     g.wait_ns = kWaitNs;
     static std::atomic<uint64_t> configured{0};
-    QL_TRY(allow_smem(k_pair_gemm<MX>, L::kTotal, configured));
-    if (launch_pdl(k_pair_gemm<MX>, dim3(2 * sch.pairs), dim3(L::kThreads), L::kTotal, st, t[0], t[1], t[2], t[3], t[4],
+    QL_TRY(allow_smem(kern, L::kTotal, configured));
+    if (launch_pdl(kern, dim3(2 * sch.pairs), dim3(L::kThreads), L::kTotal, st, t[0], t[1], t[2], t[3], t[4],
                    t[5], g) != cudaSuccess)
         return QLORA_ERR_CUDA;
     QL_LAUNCH_CHECK();
@@ -301,10 +319,11 @@ qlora_status dx_gemm(const void* W, const void* dH, int64_t dh_ld, int64_t T, in
     g.ext_steps = RP / 64;
     g.ext_k16_last = static_cast<int>(cdiv(r - 64 * (g.ext_steps - 1), 16));
     g.m_tiles = static_cast<int>(cdiv(T, 256));
-    g.n_tiles = static_cast<int>(cdiv(d_in, 256));
+    g.n_tiles = static_cast<int>(cdiv(d_in, sch.bn));
     g.out = static_cast<__nv_bfloat16*>(dX);
     g.ld_out = d_in;
-    return launch_pair_gemm<false>(t, g, sch, pair_ws, err, st);
+    return sch.bn == 256 ? launch_pair_gemm<false, 256>(t, g, sch, pair_ws, err, st)
+                         : launch_pair_gemm<false, 128>(t, g, sch, pair_ws, err, st);
 }
 
 PadCopy pad_copy(const void* src, void* dst, int64_t rows, int64_t cols, int64_t ld, int most_ctas) {
@@ -375,8 +394,6 @@ qlora_status mx_fwd(const qlora_mxfp4* w, const void* X, int64_t T, const void* 
             l.g.qx_tiles = static_cast<int>(qx_tiles);
         }
         if (!direct) l.g.pad = pad_copy(B, at<void>(ws, p.b_pad), d_out, r, b_ld, kSmsForSplit / 2);
-        l.g.zero = at<int>(ws, p.pair + p.sched.part_bytes);
-        l.g.n_zero = p.sched.n_cnt;
         QL_TRY(tmap_bf16(&l.a[0], X, T, d_in, d_in, 128));
         QL_TRY(tmap_bf16(&l.b[0], A, r, d_in, d_in, static_cast<uint32_t>(RP)));
         QL_TRY(act_gemm(RP, l, err, st));
@@ -401,7 +418,7 @@ qlora_status mx_fwd(const qlora_mxfp4* w, const void* X, int64_t T, const void* 
         g.a_sf_tiles = g.b_sf_tiles = static_cast<int>(mx_col_tiles(d_in));
         g.out = static_cast<bf*>(H);
         g.ld_out = d_out;
-        return launch_pair_gemm<true>(t, g, p.sched, at<void>(ws, p.pair), err, st);
+        return launch_pair_gemm<true, 256>(t, g, p.sched, nullptr, err, st);
     }
     CUtensorMap tw, tx, tb, tu;
     const uint32_t nt = route == kMxDecode ? 16 : (route == kMxStream64 ? 64 : 128);
@@ -453,27 +470,22 @@ qlora_status mx_bwd(MxBase base, const void* X, const qlora_act8* X8, const void
     const void* u_src = U_saved ? U_saved : u3;
     const ActTriple tr = act_triple(r);
     int b_ld = r, u_ld = U_saved ? r : tr.ld;
-    // The first kernel is launched without programmatic dependent launch, so that whatever used the
-    // workspace before has ended.
+    // The call's first kernel is launched without programmatic dependent launch, so that whatever used
+    // the workspace before has ended; the others start their prologue, or all of it where they depend on
+    // nothing of this call, beside the one in front.
+    bool first = true;
+    auto prepare = [&](BwdPrepArgs& a) -> qlora_status {
+        const int ctas = a.ctas_w + a.pad[0].ctas + a.pad[1].ctas + a.pad[2].ctas + (a.n_zero ? 1 : 0);
+        if (!ctas) return QLORA_OK;
+        if (first) k_bwd_prepare<<<ctas, 256, 0, st>>>(a);
+        else if (launch_pdl(k_bwd_prepare, dim3(ctas), dim3(256), 0, st, a) != cudaSuccess) return QLORA_ERR_CUDA;
+        QL_LAUNCH_CHECK();
+        first = false;
+        return QLORA_OK;
+    };
     {
-        BwdPrepArgs a{};
-        if (want_dx) {
-            a.codes = base.mx ? base.mx->codes : base.nf4->codes;
-            if (base.mx) {
-                a.mx_scales = base.mx->scales;
-            } else {
-                a.absmax_q = base.nf4->absmax_q;
-                a.c2 = base.nf4->c2;
-            }
-            a.n8 = d_out * d_in / 8;
-            a.col_tiles = mx_col_tiles(d_in);
-            a.per_row = static_cast<uint32_t>(d_in / 8);
-            a.w = W;
-            a.ctas_w = static_cast<int>(cdiv(a.n8, 256 * kPrepUnroll));
-            a.zero = at<int>(ws, p.pair + p.sched.part_bytes);
-            a.n_zero = p.sched.n_cnt;
-        }
         // rows that are no whole 16-byte units cannot be read by a tensor map
+        BwdPrepArgs a{};
         if (d_out % 8) {
             a.pad[0] = pad_copy(dH, at<void>(ws, p.dh_pad), T, d_out, dh_ld, 4 * kSmsForSplit);
             dH = at<void>(ws, p.dh_pad);
@@ -488,11 +500,7 @@ qlora_status mx_bwd(MxBase base, const void* X, const qlora_act8* X8, const void
                 u_ld = pad8(r);
             }
         }
-        const int ctas = a.ctas_w + a.pad[0].ctas + a.pad[1].ctas + a.pad[2].ctas + (a.n_zero ? 1 : 0);
-        if (ctas) {
-            k_bwd_prepare<<<ctas, 256, 0, st>>>(a);
-            QL_LAUNCH_CHECK();
-        }
+        QL_TRY(prepare(a));
     }
     if (grads) {
         // s G = s dH B, and U = X~ A^T unless the forward kept it
@@ -509,7 +517,7 @@ qlora_status mx_bwd(MxBase base, const void* X, const qlora_act8* X8, const void
             ju.mode = kActTriple;
             ju.out = u3;
             if (X8) {
-                ju.int8 = 1;
+                ju.op = kOpInt8;
                 ju.scales = X8->scales;
                 ju.ld_scales = d_in / 32;
                 QL_TRY(tmap_u8(&l.a[1], X8->q, T, d_in, d_in, 64, 128));
@@ -518,10 +526,55 @@ qlora_status mx_bwd(MxBase base, const void* X, const qlora_act8* X8, const void
             }
             QL_TRY(tmap_bf16(&l.b[1], A, r, d_in, d_in, static_cast<uint32_t>(RP)));
         }
+        l.pdl = !first;
+        first = false;
         QL_TRY(act_gemm(RP, l, err, st));
     }
+    if (want_dx && T > kDxFewT) {
+        BwdPrepArgs a{};
+        a.codes = base.mx ? base.mx->codes : base.nf4->codes;
+        if (base.mx) {
+            a.mx_scales = base.mx->scales;
+        } else {
+            a.absmax_q = base.nf4->absmax_q;
+            a.c2 = base.nf4->c2;
+        }
+        a.n8 = d_out * d_in / 8;
+        a.col_tiles = mx_col_tiles(d_in);
+        a.per_row = static_cast<uint32_t>(d_in / 8);
+        a.w = W;
+        a.ctas_w = static_cast<int>(cdiv(a.n8, 256 * kPrepUnroll));
+        a.zero = at<int>(ws, p.pair + p.sched.part_bytes);
+        a.n_zero = p.sched.n_cnt;
+        QL_TRY(prepare(a));
+    }
     // dX = dH W + (sG) A; the adapter term's s G is rounded to bf16 (2^-8 of that term, as dX itself is)
-    if (want_dx) QL_TRY(dx_gemm(W, dH, dh_ld, T, d_out, d_in, g3, A, RP, r, dX, p.sched, at<void>(ws, p.pair), err, st));
+    if (want_dx && T <= kDxFewT) {
+        ActLaunch l;
+        ActJob& j = l.add(d_in, static_cast<int>(T), d_out);
+        const int rpt = T <= 64 ? 64 : 128;
+        j.amn = 1;
+        j.n_tiles = static_cast<int>(cdiv(T, rpt));
+        j.ext_steps = RP / 64;
+        j.mode = kActDx;
+        j.out = dX;
+        if (base.mx) {
+            j.op = kOpMxfp4;
+            j.scales = base.mx->scales;
+            j.ld_scales = mx_col_tiles(d_in);
+        } else {
+            j.op = kOpNf4;
+            j.scales = base.nf4->absmax_q;
+            j.c2 = base.nf4->c2;
+            j.ld_scales = d_in / 64;
+        }
+        QL_TRY(tmap_u8(&l.a[0], base.mx ? base.mx->codes : base.nf4->codes, d_out, d_in / 2, d_in / 2, 64, 64));
+        QL_TRY(tmap_bf16(&l.b[0], dH, T, d_out, dh_ld, static_cast<uint32_t>(rpt)));
+        QL_TRY(tmap_bf16(&l.a[1], A, r, d_in, d_in, 64));
+        QL_TRY(tmap_bf16(&l.b[1], g3, T, r, tr.ld, static_cast<uint32_t>(rpt)));
+        l.pdl = !first;
+        QL_TRY(act_gemm(rpt, l, err, st));
+    } else if (want_dx) QL_TRY(dx_gemm(W, dH, dh_ld, T, d_out, d_in, g3, A, RP, r, dX, p.sched, at<void>(ws, p.pair), err, st));
     if (grads) {
         // dA^T[d_in, r] = X~^T (s G) and dB[d_out, r] = s dH^T U
         ActLaunch l;
@@ -532,7 +585,7 @@ qlora_status mx_bwd(MxBase base, const void* X, const qlora_act8* X8, const void
         ja.accumulate = acc;
         ja.out = dA;
         if (X8) {
-            ja.int8 = 1;
+            ja.op = kOpInt8;
             ja.scales = X8->scales;
             ja.ld_scales = d_in / 32;
             QL_TRY(tmap_u8(&l.a[0], X8->q, T, d_in, d_in, 128, 64));

@@ -485,11 +485,11 @@ struct PairGemmArgs {
     int k_mma_last;           // MMAs of the last main stage (1..4)
     int ext_steps;            // adapter K stages of 64
     int ext_k16_last;
-    int m_tiles, n_tiles;     // 256 x 256 tiles
+    int m_tiles, n_tiles;     // 256 x BN tiles
     int a_sf_tiles, b_sf_tiles;   // MXFP4: scale tiles per row of tiles (both operands share d_in)
     int split;                // ways the tail tiles are split along K (1: not)
     int tail_tiles;           // trailing tiles that are split
-    float* part;              // [tail_tiles][2 ranks][4 warps][split][2048 float4] fp32 partials
+    float* part;              // [tail_tiles][2 ranks][4 warps][split][BN * 8 float4] fp32 partials
     int* cnt;                 // [tail_tiles][2 ranks][4 warps] tickets, zero at launch
     __nv_bfloat16* out;
     int64_t ld_out;
@@ -497,19 +497,21 @@ struct PairGemmArgs {
     uint64_t wait_ns;
 };
 
-template <bool MX>
+// BN: columns of a tile, 256, or for bf16 also 128.
+constexpr int kPairMaxSplit = 4;
+template <bool MX, int BN>
 struct PairGemmSmem {
     static constexpr int kA = 128 * 128;               // this CTA's A half: 128 rows of 128 bytes
-    static constexpr int kB = 128 * 128;               // its B half
+    static constexpr int kB = BN / 2 * 128;            // its B half
     static constexpr int kSfA = MX ? 1024 : 0;         // scales of its 128 A rows
     static constexpr int kSfB = MX ? 2048 : 0;         // scales of all 256 B rows
     static constexpr int kStage = kA + kB + kSfA + kSfB;
-    static constexpr int kStages = MX ? 6 : 7;
+    static constexpr int kStages = MX ? 6 : BN == 256 ? 7 : 9;
     static constexpr int kTotal = 1024 + kStages * kStage + 512;
     static constexpr int kThreads = 192;
     // Accumulator columns of the second buffer.  MXFP4 keeps the scales in columns 448..511, so its
     // two accumulators share 64 columns, which the epilogue reads first.
-    static constexpr int kAcc1 = MX ? 192 : 256;
+    static constexpr int kAcc1 = MX ? 192 : BN;
     static constexpr int kSfCol = 448;
     static_assert(kTotal <= 232448, "shared memory budget");
 };
@@ -521,20 +523,21 @@ struct PairGemmSmem {
 // each CTA loads half of both operands (and, for MXFP4, the scales of its own A rows and of all B
 // rows).  Both CTAs' copies complete on the leader's full[s], so one wait covers the pair; a stage
 // is released to both by the MMAs' commit.  Persistent: pair p takes tiles p, p + pairs, ...; the tiles
-// of an incomplete last wave (all of them when there are fewer tiles than pairs) are split along K
-// over `split` pairs each.  Every epilogue warp of a split tile writes its fp32 partial and takes a
+// of an incomplete last wave (all of them when there are fewer tiles than pairs) may be split along K
+// over `split` pairs each (bf16 only: an MXFP4 tile is over before a join would be).  Every epilogue warp of a split tile writes its fp32 partial and takes a
 // ticket; the last adds all partials in K order, so the result does not depend on which is last,
 // and no CTA waits for another.
 // Bound (256 x 256 x 256 MXFP4 or x 64 bf16 per 512 tensor cycles): 32 to 35 KB per SM and stage
 // out of L2.
-template <bool MX>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGemmSmem<MX>::kThreads, 1)
+template <bool MX, int BN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGemmSmem<MX, BN>::kThreads, 1)
     k_pair_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                 const __grid_constant__ CUtensorMap tmSa, const __grid_constant__ CUtensorMap tmSb,
                 const __grid_constant__ CUtensorMap tmAx, const __grid_constant__ CUtensorMap tmBx,
                 const PairGemmArgs args) {
-    using L = PairGemmSmem<MX>;
+    using L = PairGemmSmem<MX, BN>;
     constexpr int S = L::kStages;
+    static_assert(!MX || BN == 256, "MXFP4 tiles are 256 wide");
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
@@ -619,7 +622,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGemmSmem<MX>::kT
             unit(u, tile, k0, k1);
             const int m0 = (tile % args.m_tiles) * 256 + static_cast<int>(rank) * 128;
             const int nt = tile / args.m_tiles;
-            const int n0 = nt * 256 + static_cast<int>(rank) * 128;
+            const int n0 = nt * BN + static_cast<int>(rank) * (BN / 2);
             for (int it = k0; it < k1; ++it) {
                 ok = mbar_wait_uniform(&empty[s], ph ^ 1, abort, args.wait_ns);
                 if (!ok) break;
@@ -640,7 +643,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGemmSmem<MX>::kT
                         } else {
                             tma_load_2d_pair(a, &tmA, bar, it * 64, m0);
                             tma_load_2d_pair(b, &tmB, bar, n0, it * 64);
-                            tma_load_2d_pair(b + 8192, &tmB, bar, n0 + 64, it * 64);
+                            if (BN == 256) tma_load_2d_pair(b + 8192, &tmB, bar, n0 + 64, it * 64);
                         }
                     } else {
                         const int kx = (it - args.k_steps) * 64;
@@ -650,7 +653,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGemmSmem<MX>::kT
                             tma_load_2d_pair(b, &tmBx, bar, kx, n0);
                         } else {
                             tma_load_2d_pair(b, &tmBx, bar, n0, kx);
-                            tma_load_2d_pair(b + 8192, &tmBx, bar, n0 + 64, kx);
+                            if (BN == 256) tma_load_2d_pair(b + 8192, &tmBx, bar, n0 + 64, kx);
                         }
                     }
                 }
@@ -661,7 +664,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGemmSmem<MX>::kT
         if (!ok) fail();
     } else if (warp == 1) {
         if (rank == 0) {
-            const uint32_t idesc = make_idesc_bf16(256, 256, false, !MX);
+            const uint32_t idesc = make_idesc_bf16(256, BN, false, !MX);
             const uint32_t idesc0 = make_idesc_mxf4(256, 256, 0, 0), idesc2 = make_idesc_mxf4(256, 256, 2, 2);
             const uint64_t a_desc = make_sw128_desc(smem_u32(sA), 16, 1024);
             const uint64_t b_desc = make_sw128_desc(smem_u32(sB), MX ? 16 : 8192, 1024);
@@ -745,57 +748,65 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGemmSmem<MX>::kT
             }
             tc_fence_after();
             const int64_t grow = static_cast<int64_t>(tile % args.m_tiles) * 256 + rank * 128 + q * 32 + lane;
-            const int gc0 = (tile / args.m_tiles) * 256;
+            const int gc0 = (tile / args.m_tiles) * BN;
             const uint32_t tbase = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * L::kAcc1;
-            const bool split = u >= n_full && args.split > 1;
+            const bool split = !MX && u >= n_full && args.split > 1;
             bool last = true;
             const float4* parts = nullptr;
             if (split) {
                 const int64_t slot = (static_cast<int64_t>(part_tile) * 2 + rank) * 4 + q;
-                float4* mine = reinterpret_cast<float4*>(args.part) + ((slot * args.split + part) << 11);
+                parts = reinterpret_cast<const float4*>(args.part) + slot * args.split * (BN * 8);
+                float4* mine = const_cast<float4*>(parts) + part * (BN * 8);
 #pragma unroll 1
-                for (int c = 0; c < 8; ++c) {
+                for (int c = 0; c < BN / 32; ++c) {
                     uint32_t r[32];
                     tmem_ld_32x32b_x32(tbase + c * 32, r);
                     tmem_ld_wait();
+                    if (grow < args.M) {
 #pragma unroll
-                    for (int g = 0; g < 8; ++g)
-                        mine[g2_part_idx(c, g, lane)] =
-                            make_float4(__uint_as_float(r[4 * g]), __uint_as_float(r[4 * g + 1]),
-                                        __uint_as_float(r[4 * g + 2]), __uint_as_float(r[4 * g + 3]));
+                        for (int g = 0; g < 8; ++g)
+                            mine[g2_part_idx(c, g, lane)] =
+                                make_float4(__uint_as_float(r[4 * g]), __uint_as_float(r[4 * g + 1]),
+                                            __uint_as_float(r[4 * g + 2]), __uint_as_float(r[4 * g + 3]));
+                    }
                 }
                 __threadfence();
                 __syncwarp();
                 int ticket = 0;
                 if (lane == 0) ticket = atomicAdd(args.cnt + slot, 1);
                 last = __shfl_sync(0xffffffffu, ticket, 0) == args.split - 1;
-                if (last) {
-                    __threadfence();
-                    parts = reinterpret_cast<const float4*>(args.part) + ((slot * args.split) << 11);
-                }
+                if (last) __threadfence();
             }
             // MX: the columns that the other accumulator shares come first (the last 64 of
             // buffer 0, the first 64 of buffer 1)
             const int rot = (MX && buf == 0) ? 6 : 0;
 #pragma unroll 1
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < BN / 32; ++i) {
                 const int c = (i + rot) & 7;
                 uint32_t r[32];
                 if (last) {
-                    if (parts) {
+                    if (split) {
+                        // all other parts' values of the chunk in flight at once, added in K order whichever
+                        // part is last
+                        float4 o[kPairMaxSplit][8];
+#pragma unroll
+                        for (int p = 0; p < kPairMaxSplit; ++p)
+                            if (p < args.split && p != part && grow < args.M)
+#pragma unroll
+                                for (int g = 0; g < 8; ++g) o[p][g] = __ldcg(parts + p * (BN * 8) + g2_part_idx(c, g, lane));
+                        tmem_ld_32x32b_x32(tbase + c * 32, r);
+                        tmem_ld_wait();
                         float4 v[8];
 #pragma unroll
-                        for (int g = 0; g < 8; ++g) v[g] = __ldcg(parts + g2_part_idx(c, g, lane));
-                        for (int p = 1; p < args.split; ++p) {
+                        for (int p = 0; p < kPairMaxSplit; ++p)
+                            if (p < args.split)
 #pragma unroll
-                            for (int g = 0; g < 8; ++g) {
-                                const float4 o = __ldcg(parts + (static_cast<int64_t>(p) << 11) + g2_part_idx(c, g, lane));
-                                v[g].x += o.x;
-                                v[g].y += o.y;
-                                v[g].z += o.z;
-                                v[g].w += o.w;
-                            }
-                        }
+                                for (int g = 0; g < 8; ++g) {
+                                    const float4 x = p == part ? make_float4(__uint_as_float(r[4 * g]), __uint_as_float(r[4 * g + 1]),
+                                                                             __uint_as_float(r[4 * g + 2]), __uint_as_float(r[4 * g + 3]))
+                                                               : o[p][g];
+                                    v[g] = p == 0 ? x : make_float4(v[g].x + x.x, v[g].y + x.y, v[g].z + x.z, v[g].w + x.w);
+                                }
 #pragma unroll
                         for (int g = 0; g < 8; ++g) {
                             r[4 * g] = __float_as_uint(v[g].x);
@@ -827,7 +838,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGemmSmem<MX>::kT
                         }
                     }
                 }
-                if (i == (MX ? 1 : 7)) {
+                if (i == (MX ? 1 : BN / 32 - 1)) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_remote_async_payload(free_leader + static_cast<uint32_t>(buf * 8));
