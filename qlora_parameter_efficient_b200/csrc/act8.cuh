@@ -146,6 +146,15 @@ enum : int {
     kActDx = 4        // bf16 out[j, m] = D[m, j]  (dX of few tokens)
 };
 
+// The products of a launch.  One kernel for all of them would be too long for the instruction cache (and
+// measured 10 to 25% slower).
+enum : int {
+    kRoleU = 0,       // forward: U from bf16 X [T, d_in] (and the MXFP4 of X), kActU
+    kRoleUG = 1,      // backward: G from dH, U from X or its checkpoint, kActTriple
+    kRoleAB = 2,      // backward: dA from X or its checkpoint (kActCols), dB from dH (kActRows)
+    kRoleDx = 3       // backward of few tokens: dX from the weight, kActDx
+};
+
 // How the A operand is stored; all but bf16 are decoded to it in shared memory.
 enum : int {
     kOpBf16 = 0,
@@ -160,15 +169,14 @@ struct ActJob {
     int64_t K;               // contraction length
     int k_steps;             // ceil(K / 64)
     int op;                  // how A is stored
-    int amn;                 // A is stored [K, M] (tokens are K) and consumed MN-major, else [M, K]
-    int bmn;                 // B is stored [K, N], else [N, K]
-    int triple;              // B is an ActTriple (bmn only)
+    int bmn;                 // kRoleUG: B is stored [K, N], else [N, K]
+    int triple;              // B is an ActTriple (kRoleAB)
     const uint8_t* scales;   // E8M0 bytes (int8: row-major, MXFP4: tiled) or NF4's uint8 constants
     const float* c2;         // NF4's group constants
     int64_t ld_scales;       // scales per stored row (MXFP4: scale tiles)
     int n_tiles;             // tiles of RPT columns of D
     int ext_steps;           // kActDx: the adapter's K steps of 64, taken by the last rank
-    int mode;
+    int mode;                // kRoleAB: kActCols or kActRows
     float scale;
     int accumulate;          // kActCols, kActRows: add to out
     void* out;
@@ -242,7 +250,7 @@ struct ActGemmSmem {
 // L2.  With few tokens dX^T = W^T dH^T is such a product too (kActDx): M = d_in, N = tokens, the weight
 // decoded once per CTA and split along d_out over the SMs.  An MMA of M = 128 takes about 75 cycles however small N is (it reads its A tile), hence one of
 // N = 3 stride for a triple and not three.
-template <int RPT>
+template <int RPT, int ROLE>
 __global__ void __launch_bounds__(ActGemmSmem<RPT>::kThreads, 1)
     k_act_gemm(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmB0,
                const __grid_constant__ CUtensorMap tmA1, const __grid_constant__ CUtensorMap tmB1,
@@ -263,7 +271,7 @@ __global__ void __launch_bounds__(ActGemmSmem<RPT>::kThreads, 1)
     const int C = args.ranks;
     const int rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int tile = blockIdx.x / C;
-    if (tile >= args.tiles) {
+    if (ROLE == kRoleU && tile >= args.tiles) {
         griddep_enter();
         const int b = static_cast<int>(blockIdx.x) - args.tiles * C;
         if (b >= args.qx_ctas) {
@@ -275,50 +283,55 @@ __global__ void __launch_bounds__(ActGemmSmem<RPT>::kThreads, 1)
         }
         return;
     }
-    const int ji = tile >= args.tiles0 ? 1 : 0;
+    const int ji = (ROLE == kRoleUG || ROLE == kRoleAB) && tile >= args.tiles0 ? 1 : 0;
     const ActJob& job = args.job[ji];
     const CUtensorMap* tmA = ji ? &tmA1 : &tmA0;
     const CUtensorMap* tmB = ji ? &tmB1 : &tmB0;
     const int tj = tile - (ji ? args.tiles0 : 0);
-    const int m0 = tj / job.n_tiles * 128, n0 = tj % job.n_tiles * RPT;
+    const int n_tiles = ROLE == kRoleDx ? job.n_tiles : 1;
+    const int m0 = tj / n_tiles * 128, n0 = tj % n_tiles * RPT;
     const int N = min(RPT, job.N - n0);         // columns of this tile
     const int op = job.op;
-    const bool dec = op != kOpBf16, amn = job.amn, bmn = job.bmn;
-    const bool quant = job.mx_codes != nullptr;
+    const bool dec = ROLE == kRoleDx || (ROLE != kRoleU && op != kOpBf16);
+    // A is stored [K, M] (its rows are K: tokens, weight rows) and consumed MN-major, else [M, K]
+    constexpr bool amn = ROLE == kRoleAB || ROLE == kRoleDx;
+    const bool bmn = ROLE == kRoleAB || (ROLE == kRoleUG && job.bmn);
+    const bool quant = ROLE == kRoleU && job.mx_codes != nullptr;
     const int unit = quant ? 2 : 1;             // K steps a range is made of (quantizing: whole scale tiles)
     const int64_t units = (job.k_steps + unit - 1) / unit;
     const int k_begin = static_cast<int>(units * rank / C) * unit;
     const int n_main = min(job.k_steps, static_cast<int>(units * (rank + 1) / C) * unit) - k_begin;
-    const int n_iters = n_main + (rank == C - 1 ? job.ext_steps : 0);
+    const int n_iters = n_main + (ROLE == kRoleDx && rank == C - 1 ? job.ext_steps : 0);
     const ActTriple tr = act_triple(job.N);
-    const int terms = RPT == 64 && job.triple ? 3 : 1;         // column groups of an accumulator tile
-    const int groups = RPT == 128 && job.triple ? 3 : 1;       // MMAs per 16 of K
+    const bool triple = ROLE == kRoleAB && job.triple;
+    const int terms = RPT == 64 && triple ? 3 : 1;             // column groups of an accumulator tile
+    const int groups = RPT == 128 && triple ? 3 : 1;           // MMAs per 16 of K
     const int n_mma = terms == 3 ? 3 * tr.stride : (N + 15) & ~15;
-    const int chunks = job.triple ? tr.ld / 64 : RPT / 64;     // of the B tile
+    const int chunks = triple ? tr.ld / 64 : RPT / 64;         // of the B tile
     const int acc_cols = terms == 3 ? tr.ld : RPT;
     const int NA = min(L::kAcc, 512 / acc_cols);               // accumulator tiles
     const int seg_len = groups == 3 ? 2 : 4;                   // K steps of 64 per accumulator segment
     const int n_seg = (n_iters + seg_len - 1) / seg_len;
     // ring: A tiles, B tiles, tiles as stored
     const int b_bytes = chunks * L::kChunk;
-    const int raw_bytes = op == kOpInt8 ? L::kRaw : dec ? L::kRaw / 2 : 0;
+    const int raw_bytes = !dec ? 0 : ROLE == kRoleDx ? L::kRaw / 2 : L::kRaw;
     const int stage = L::kA + b_bytes + raw_bytes;
     const int S = min(L::kMaxStages, L::kRing / stage);
     uint8_t* sA = smem;
     uint8_t* sB = sA + S * L::kA;
     uint8_t* sR = sB + S * b_bytes;
 
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < L::kMaxStages; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], quant ? 9 : 1);     // the MMAs, and the warps that quantize
-            mbar_init(&decoded[s], 8);
+    if (warp == 2) {
+        if (lane < L::kMaxStages) {
+            mbar_init(&full[lane], 1);
+            mbar_init(&empty[lane], quant ? 9 : 1);     // the MMAs, and the warps that quantize
+            mbar_init(&decoded[lane], 8);
         }
-        for (int b = 0; b < L::kAcc; ++b) {
-            mbar_init(&accf[b], 1);
-            mbar_init(&acc_free[b], 8);
+        if (lane < L::kAcc) {
+            mbar_init(&accf[lane], 1);
+            mbar_init(&acc_free[lane], 8);
         }
-        *abort = 0;
+        if (lane == 0) *abort = 0;
         fence_mbar_init();
     }
     if (warp == 0 && lane == 0) {
@@ -358,13 +371,13 @@ __global__ void __launch_bounds__(ActGemmSmem<RPT>::kThreads, 1)
             uint8_t* a = sA + s * L::kA;
             uint8_t* dst = sB + s * b_bytes;
             if (elect_one()) {
-                if (it < n_main) {
+                if (ROLE != kRoleDx || it < n_main) {
                     const int kx = (k_begin + it) * 64;
                     mbar_arrive_expect_tx(&full[s], (dec ? raw_bytes : L::kA) + b_bytes);
-                    if (op == kOpInt8) {
-                        tma_load_2d(sR + s * raw_bytes, tmA, &full[s], amn ? m0 : kx, amn ? kx : m0);
-                    } else if (dec) {
+                    if (ROLE == kRoleDx) {
                         tma_load_2d(sR + s * raw_bytes, tmA, &full[s], m0 / 2, kx);
+                    } else if (dec) {
+                        tma_load_2d(sR + s * raw_bytes, tmA, &full[s], amn ? m0 : kx, amn ? kx : m0);
                     } else if (amn) {
                         tma_load_2d(a, tmA, &full[s], m0, kx);
                         tma_load_2d(a + 8192, tmA, &full[s], m0 + 64, kx);
@@ -439,15 +452,23 @@ __global__ void __launch_bounds__(ActGemmSmem<RPT>::kThreads, 1)
             tc_fence_after();
             const uint32_t t = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc_i * acc_cols + half * kHalf;
 #pragma unroll
-            for (int c = 0; c < kHalf; c += 32)
+            for (int c = 0; c < kHalf; c += 16)
                 if (half * kHalf + c < N) {
-                    // the smallest terms first (columns past a group are the next one's: never used)
-                    for (int k = terms - 1; k >= 0; --k) {
-                        uint32_t r[32];
-                        tmem_ld_32x32b_x32(t + c + k * tr.stride, r);
+                    uint32_t r0[16];
+                    tmem_ld_32x32b_x16(t + c, r0);
+                    if (RPT == 64 && terms == 3) {
+                        // the smallest terms first (columns past a group are the next one's: never used)
+                        uint32_t r1[16], r2[16];
+                        tmem_ld_32x32b_x16(t + c + tr.stride, r1);
+                        tmem_ld_32x32b_x16(t + c + 2 * tr.stride, r2);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) acc[c + j] += __uint_as_float(r[j]);
+                        for (int j = 0; j < 16; ++j)
+                            acc[c + j] += __uint_as_float(r0[j]) + (__uint_as_float(r1[j]) + __uint_as_float(r2[j]));
+                    } else {
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) acc[c + j] += __uint_as_float(r0[j]);
                     }
                 }
             tc_fence_before();
@@ -468,21 +489,25 @@ __global__ void __launch_bounds__(ActGemmSmem<RPT>::kThreads, 1)
         auto drain_behind = [&](int it0) {
             for (const int end = (it0 + 4) / seg_len - NA / 2; ok && drained < end && drained < n_seg; ++drained) drain();
         };
-        if (op >= kOpMxfp4) {
+        if constexpr (ROLE == kRoleDx) {
             // 32 columns of one weight row per thread and stage (the adapter's steps need no decode)
             const int td = (threadIdx.x - 64) & 255, row = td >> 2, blk_in = td & 3, sw = row & 7;
             const int64_t mblk = m0 / 32 + blk_in;
             uint32_t e[2] = {0, 0};
             float c2[2] = {0.f, 0.f};
+            const int64_t k0 = static_cast<int64_t>(k_begin) * 64, ld = job.ld_scales;
+            const int lim = mblk * 32 >= job.M ? 0 : min(static_cast<int64_t>(n_main), (job.K - k0 - row + 63) / 64);
+            const uint8_t* sc = job.scales;
+            const float* gc = job.c2;
             auto fetch = [&](int it, uint32_t& ev, float& cv) {
-                const int64_t wrow = static_cast<int64_t>(k_begin + it) * 64 + row;
-                if (it >= n_main || wrow >= job.K || mblk * 32 >= job.M) return;
+                if (it >= lim) return;
+                const int64_t wrow = k0 + it * 64 + row;
                 if (op == kOpMxfp4) {
-                    ev = __ldg(job.scales + mx_scale_offset(wrow, mblk, job.ld_scales));
+                    ev = __ldg(sc + mx_scale_offset(wrow, mblk, ld));
                 } else {
-                    const int64_t blk = wrow * job.ld_scales + mblk / 2;
-                    ev = __ldg(job.scales + blk);
-                    cv = __ldg(job.c2 + blk / kGroup);
+                    const int64_t blk = wrow * ld + mblk / 2;
+                    ev = __ldg(sc + blk);
+                    cv = __ldg(gc + blk / kGroup);
                 }
             };
             const int dst_off = (blk_in >> 1) * 8192 + row * 128, c0 = (blk_in & 1) * 4;
@@ -523,18 +548,17 @@ __global__ void __launch_bounds__(ActGemmSmem<RPT>::kThreads, 1)
                 if (L::kGroups > 1) skip(2);
                 if (drains) drain_behind(it0);
             }
-        } else if (op == kOpInt8) {
+        } else if ((ROLE == kRoleUG || ROLE == kRoleAB) && dec) {
             const int td = (threadIdx.x - 64) & 255;              // the int8 block of this thread
             const int row = amn ? td >> 2 : td >> 1;              // row of the int8 tile
             const int blk_in = amn ? td & 3 : td & 1;             // block within the row
-            auto scale_at = [&](int it) -> uint32_t {
-                const int64_t kx = static_cast<int64_t>(k_begin + it) * 64;
-                const int64_t srow = amn ? kx + row : m0 + row;
-                const int64_t blk = (amn ? m0 / 32 : kx / 32) + blk_in;
-                const int64_t rows = amn ? job.K : job.M;
-                if (it >= n_iters || srow >= rows || blk >= job.ld_scales) return 0u;
-                return __ldg(job.scales + srow * job.ld_scales + blk);
-            };
+            // this thread's scales: `lim` of them (0 past the matrix), `step` bytes apart
+            const int64_t ld = job.ld_scales, k0 = static_cast<int64_t>(k_begin) * 64;
+            const int64_t step = amn ? 64 * ld : 2;
+            const uint8_t* sc = job.scales + (amn ? (k0 + row) * ld + m0 / 32 : (m0 + row) * ld + k0 / 32) + blk_in;
+            const bool there = amn ? m0 / 32 + blk_in < ld : m0 + row < job.M;
+            const int lim = !there ? 0 : min(static_cast<int64_t>(n_iters), amn ? (job.K - k0 - row + 63) / 64 : n_iters);
+            auto scale_at = [&](int it) -> uint32_t { return it < lim ? __ldg(sc + it * step) : 0u; };
             const int dst_off = amn ? (blk_in >> 1) * 8192 + row * 128 : row * 128;
             const int c0 = amn ? (blk_in & 1) * 4 : blk_in * 4, sw = row & 7;
             // the scales of this group's next pair are in flight while it decodes (a load takes longer than
@@ -635,50 +659,73 @@ __global__ void __launch_bounds__(ActGemmSmem<RPT>::kThreads, 1)
         auto total = [&](int rl, int j) {
             float v = 0.f;
             for (int c = 0; c < C; ++c) v += red[(c * R + rl) * L::kLdRed + j];
-            return job.mode == kActU || job.mode == kActDx ? v : job.scale * v;
+            return v;
         };
         const int td = threadIdx.x - 64;
-        if (job.mode == kActDx) {
-            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(job.out);
+        const int mode = ROLE == kRoleU ? kActU : ROLE == kRoleUG ? kActTriple : ROLE == kRoleDx ? kActDx : job.mode;
+        const float scale = job.scale;
+        if (mode == kActDx || mode == kActCols) {
+            // column by column: consecutive threads on consecutive rows (R a power of two)
+            const int sh = 31 - __clz(R);
+            const bool add = job.accumulate != 0;
             for (int i = td; i < R * N; i += 256) {
-                const int j = i / R, rl = i % R;
-                if (rl < rows) out[static_cast<int64_t>(n0 + j) * job.M + row0 + rl] = __float2bfloat16_rn(total(rl, j));
-            }
-        } else if (job.mode == kActTriple) {
-            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(job.out) + static_cast<int64_t>(row0) * tr.ld;
-            for (int i = td; i < rows * tr.stride; i += 256) {
-                const int rl = i / tr.stride, j = i % tr.stride;
-                float v = j < N ? total(rl, j) : 0.f;
-#pragma unroll
-                for (int k = 0; k < 3; ++k) {
-                    const __nv_bfloat16 h = __float2bfloat16_rn(v);
-                    out[rl * tr.ld + k * tr.stride + j] = h;
-                    // an infinite or NaN v is carried by the first alone (inf - inf would make it NaN)
-                    const float rest = v - __bfloat162float(h);
-                    v = fabsf(rest) < __int_as_float(0x7F800000) ? rest : 0.f;
-                }
-            }
-        } else if (job.mode == kActU) {
-            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(job.out);
-            for (int i = td; i < rows * N; i += 256) {
-                const int rl = i / N, j = i % N;
-                const int64_t row = row0 + rl;
-                const float v = total(rl, j);
-                out[row * job.ld + j] = __float2bfloat16_rn(job.scale * v);
-                if (job.out2) job.out2[row * N + j] = __float2bfloat16_rn(v);
-            }
-        } else if (job.mode == kActCols) {
-            float* out = static_cast<float*>(job.out);
-            for (int i = td; i < R * N; i += 256) {
-                const int j = i / R, rl = i % R;
+                const int j = i >> sh, rl = i & (R - 1);
                 if (rl >= rows) continue;
-                float* o = out + static_cast<int64_t>(j) * job.M + row0 + rl;
-                *o = job.accumulate ? *o + total(rl, j) : total(rl, j);
+                const int64_t at = static_cast<int64_t>(n0 + j) * job.M + row0 + rl;
+                const float v = total(rl, j);
+                if (mode == kActDx) static_cast<__nv_bfloat16*>(job.out)[at] = __float2bfloat16_rn(v);
+                else static_cast<float*>(job.out)[at] = add ? static_cast<float*>(job.out)[at] + scale * v : scale * v;
             }
         } else {
-            float* out = static_cast<float*>(job.out) + static_cast<int64_t>(row0) * N;
-            for (int i = td; i < rows * N; i += 256)
-                out[i] = job.accumulate ? out[i] + total(i / N, i % N) : total(i / N, i % N);
+            // row by row, four columns per thread (the joining buffer's rows are 16-byte units)
+            const int n4 = mode == kActTriple ? tr.stride / 4 : (N + 3) / 4;
+            for (int rl = td / n4, g = td - rl * n4; rl < rows;) {
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (4 * g < N)
+                    for (int c = 0; c < C; ++c) {
+                        const float4 o = *reinterpret_cast<const float4*>(red + (c * R + rl) * L::kLdRed + 4 * g);
+                        v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+                    }
+                const int64_t row = row0 + rl;
+                const int j = 4 * g, left = N - j;           // columns of this group that exist
+                float x[4] = {v.x, left > 1 ? v.y : 0.f, left > 2 ? v.z : 0.f, left > 3 ? v.w : 0.f};
+                if (mode == kActTriple) {
+                    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(job.out) + row * tr.ld + j;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[e] *= scale;
+#pragma unroll
+                    for (int k = 0; k < 3; ++k) {
+                        uint2 w;
+                        w.x = pack_bf16x2(x[0], x[1]);
+                        w.y = pack_bf16x2(x[2], x[3]);
+                        *reinterpret_cast<uint2*>(out + k * tr.stride) = w;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            // an infinite or NaN value is carried by the first term alone (inf - inf would make
+                            // it NaN)
+                            const uint32_t h = e < 2 ? w.x : w.y;
+                            const float rest = x[e] - __uint_as_float((e & 1) ? h & 0xFFFF0000u : h << 16);
+                            x[e] = fabsf(rest) < __int_as_float(0x7F800000) ? rest : 0.f;
+                        }
+                    }
+                } else if (mode == kActU) {
+                    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(job.out) + row * job.ld + j;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (e < left) {
+                            out[e] = __float2bfloat16_rn(scale * x[e]);
+                            if (job.out2) job.out2[row * N + j + e] = __float2bfloat16_rn(x[e]);
+                        }
+                } else {
+                    float* out = static_cast<float*>(job.out) + row * N + j;
+                    const bool add = job.accumulate != 0;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (e < left) out[e] = add ? out[e] + scale * x[e] : scale * x[e];
+                }
+                // (no division in the loop: 256 threads further on)
+                for (g += 256; g >= n4; g -= n4) ++rl;
+            }
         }
     }
     tc_fence_before();

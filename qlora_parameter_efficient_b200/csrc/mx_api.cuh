@@ -206,10 +206,10 @@ struct ActLaunch {
         return j;
     }
 };
-template <int RPT>
+template <int RPT, int ROLE>
 qlora_status launch_act_gemm(ActLaunch& l, int* err, cudaStream_t st) {
     using L = ActGemmSmem<RPT>;
-    auto kern = k_act_gemm<RPT>;
+    auto kern = k_act_gemm<RPT, ROLE>;
     static std::atomic<uint64_t> configured{0};
     QL_TRY(allow_smem(kern, L::kTotal, configured));
     if (l.n == 1 && !l.g.job[0].ext_steps) {
@@ -262,8 +262,9 @@ qlora_status launch_act_gemm(ActLaunch& l, int* err, cudaStream_t st) {
     QL_LAUNCH_CHECK();
     return QLORA_OK;
 }
+template <int ROLE>
 qlora_status act_gemm(int rpt, ActLaunch& l, int* err, cudaStream_t st) {
-    return rpt == 64 ? launch_act_gemm<64>(l, err, st) : launch_act_gemm<128>(l, err, st);
+    return rpt == 64 ? launch_act_gemm<64, ROLE>(l, err, st) : launch_act_gemm<128, ROLE>(l, err, st);
 }
 
 template <bool MX, int BN>
@@ -375,7 +376,6 @@ qlora_status mx_fwd(const qlora_mxfp4* w, const void* X, int64_t T, const void* 
         ActLaunch l;
         l.pdl = false;
         ActJob& ju = l.add(T, r, d_in);
-        ju.mode = kActU;
         ju.scale = s;
         ju.out = us;
         ju.ld = RP;
@@ -396,7 +396,7 @@ qlora_status mx_fwd(const qlora_mxfp4* w, const void* X, int64_t T, const void* 
         if (!direct) l.g.pad = pad_copy(B, at<void>(ws, p.b_pad), d_out, r, b_ld, kSmsForSplit / 2);
         QL_TRY(tmap_bf16(&l.a[0], X, T, d_in, d_in, 128));
         QL_TRY(tmap_bf16(&l.b[0], A, r, d_in, d_in, static_cast<uint32_t>(RP)));
-        QL_TRY(act_gemm(RP, l, err, st));
+        QL_TRY(act_gemm<kRoleU>(RP, l, err, st));
     }
     if (route == kMxPair) {
         CUtensorMap t[6];
@@ -507,14 +507,12 @@ qlora_status mx_bwd(MxBase base, const void* X, const qlora_act8* X8, const void
         ActLaunch l;
         ActJob& jg = l.add(T, r, d_out);
         jg.bmn = 1;
-        jg.mode = kActTriple;
         jg.scale = s;
         jg.out = g3;
         QL_TRY(tmap_bf16(&l.a[0], dH, T, d_out, dh_ld, 128));
         QL_TRY(tmap_bf16(&l.b[0], b_src, d_out, r, b_ld, 64));
         if (!U_saved) {
             ActJob& ju = l.add(T, r, d_in);
-            ju.mode = kActTriple;
             ju.out = u3;
             if (X8) {
                 ju.op = kOpInt8;
@@ -528,7 +526,7 @@ qlora_status mx_bwd(MxBase base, const void* X, const qlora_act8* X8, const void
         }
         l.pdl = !first;
         first = false;
-        QL_TRY(act_gemm(RP, l, err, st));
+        QL_TRY(act_gemm<kRoleUG>(RP, l, err, st));
     }
     if (want_dx && T > kDxFewT) {
         BwdPrepArgs a{};
@@ -553,10 +551,8 @@ qlora_status mx_bwd(MxBase base, const void* X, const qlora_act8* X8, const void
         ActLaunch l;
         ActJob& j = l.add(d_in, static_cast<int>(T), d_out);
         const int rpt = T <= 64 ? 64 : 128;
-        j.amn = 1;
         j.n_tiles = static_cast<int>(cdiv(T, rpt));
         j.ext_steps = RP / 64;
-        j.mode = kActDx;
         j.out = dX;
         if (base.mx) {
             j.op = kOpMxfp4;
@@ -573,13 +569,12 @@ qlora_status mx_bwd(MxBase base, const void* X, const qlora_act8* X8, const void
         QL_TRY(tmap_bf16(&l.a[1], A, r, d_in, d_in, 64));
         QL_TRY(tmap_bf16(&l.b[1], g3, T, r, tr.ld, static_cast<uint32_t>(rpt)));
         l.pdl = !first;
-        QL_TRY(act_gemm(rpt, l, err, st));
+        QL_TRY(act_gemm<kRoleDx>(rpt, l, err, st));
     } else if (want_dx) QL_TRY(dx_gemm(W, dH, dh_ld, T, d_out, d_in, g3, A, RP, r, dX, p.sched, at<void>(ws, p.pair), err, st));
     if (grads) {
         // dA^T[d_in, r] = X~^T (s G) and dB[d_out, r] = s dH^T U
         ActLaunch l;
         ActJob& ja = l.add(d_in, r, T);
-        ja.amn = ja.bmn = 1;
         ja.triple = 1;
         ja.mode = kActCols;
         ja.accumulate = acc;
@@ -594,7 +589,6 @@ qlora_status mx_bwd(MxBase base, const void* X, const qlora_act8* X8, const void
         }
         QL_TRY(tmap_bf16(&l.b[0], g3, T, tr.ld, tr.ld, 64));
         ActJob& jb = l.add(d_out, r, T);
-        jb.amn = jb.bmn = 1;
         jb.triple = !U_saved;
         jb.mode = kActRows;
         jb.scale = s;
@@ -602,7 +596,7 @@ qlora_status mx_bwd(MxBase base, const void* X, const qlora_act8* X8, const void
         jb.out = dB;
         QL_TRY(tmap_bf16(&l.a[1], dH, T, d_out, dh_ld, 64));
         QL_TRY(tmap_bf16(&l.b[1], u_src, T, U_saved ? r : tr.ld, u_ld, 64));
-        QL_TRY(act_gemm(RP, l, err, st));
+        QL_TRY(act_gemm<kRoleAB>(RP, l, err, st));
     }
     return QLORA_OK;
 }
