@@ -743,11 +743,10 @@ __global__ void __launch_bounds__(ActGemmSmem<RPT>::kThreads, 1)
 // kernel behind then still finds both finished.
 struct BwdPrepArgs {
     const uint8_t* codes;
-    const uint8_t* mx_scales;     // MXFP4 weight, or
-    const uint8_t* absmax_q;      // NF4 weight
+    const uint8_t* mx_scales;     // MXFP4 weight (one scale tile per CTA), or
+    const uint8_t* absmax_q;      // NF4 weight (eight elements per thread and step)
     const float* c2;
-    int64_t n8, col_tiles;        // weight elements / 8
-    uint32_t per_row;             // d_in / 8
+    int64_t d_out, d_in;
     __nv_bfloat16* w;
     int ctas_w;
     PadCopy pad[3];
@@ -758,31 +757,31 @@ constexpr int kPrepUnroll = 4;
 __global__ void __launch_bounds__(256) k_bwd_prepare(const __grid_constant__ BwdPrepArgs a) {
     griddep_launch_dependents();
     int b = blockIdx.x;
+    if (b < a.ctas_w && a.mx_scales) {
+        __shared__ __align__(16) uint8_t s_sc[kMxTileBytes];
+        const int64_t kts = mx_col_tiles(a.d_in);
+        mxfp4_dequantize_tile(a.codes, a.mx_scales, a.d_out, a.d_in, b / kts, b % kts, a.w, s_sc);
+        griddep_wait();
+        return;
+    }
     if (b < a.ctas_w) {
-        const int64_t i0 = static_cast<int64_t>(b) * (256 * kPrepUnroll) + threadIdx.x;
+        const int64_t i0 = static_cast<int64_t>(b) * (256 * kPrepUnroll) + threadIdx.x, n8 = a.d_out * a.d_in / 8;
         uint32_t q[kPrepUnroll], e[kPrepUnroll];
         float c[kPrepUnroll];
 #pragma unroll
         for (int u = 0; u < kPrepUnroll; ++u) {
             const int64_t i = i0 + u * 256;
-            if (i < a.n8) {
+            if (i < n8) {
                 q[u] = __ldg(reinterpret_cast<const uint32_t*>(a.codes) + i);
-                if (a.mx_scales) {
-                    const int64_t row = a.n8 >> 32 ? i / a.per_row : static_cast<uint32_t>(i) / a.per_row;
-                    e[u] = __ldg(a.mx_scales + mx_scale_offset(row, (i - row * a.per_row) >> 2, a.col_tiles));
-                } else {
-                    e[u] = __ldg(a.absmax_q + (i >> 3));
-                    c[u] = __ldg(a.c2 + (i >> 3) / kGroup);
-                }
+                e[u] = __ldg(a.absmax_q + (i >> 3));
+                c[u] = __ldg(a.c2 + (i >> 3) / kGroup);
             }
         }
 #pragma unroll
         for (int u = 0; u < kPrepUnroll; ++u) {
             const int64_t i = i0 + u * 256;
-            if (i < a.n8)
-                reinterpret_cast<uint4*>(a.w)[i] = a.mx_scales
-                                                       ? e2m1_scale8_bf16(q[u], e8m0_value(e[u]))
-                                                       : nf4_decode8(q[u], nf4_make_planes(nf4_block_scale(e[u], c[u])));
+            if (i < n8)
+                reinterpret_cast<uint4*>(a.w)[i] = nf4_decode8(q[u], nf4_make_planes(nf4_block_scale(e[u], c[u])));
         }
         griddep_wait();
         return;

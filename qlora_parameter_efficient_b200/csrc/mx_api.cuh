@@ -25,9 +25,8 @@ qlora_status check_mxfp4(const qlora_mxfp4* w) {
     return mx_check_dims(w->d_out, w->d_in);
 }
 
-// CTAs of the stand-alone format kernels: 256 threads, four steps of 8 elements each.
-static_assert(kMxUnroll == 4 && kAct8Unroll == 4, "mx_ctas");
-unsigned mx_ctas(int64_t n8) { return static_cast<unsigned>(cdiv(n8, 1024)); }
+// CTAs of the checkpoint's format kernels: 256 threads, kAct8Unroll steps of 8 elements each.
+unsigned act8_ctas(int64_t n8) { return static_cast<unsigned>(cdiv(n8, 256 * kAct8Unroll)); }
 
 // Routes of the MXFP4 forward by the number of tokens.
 enum MxRoute { kMxDecode, kMxStream64, kMxStream128, kMxPair };
@@ -537,11 +536,10 @@ qlora_status mx_bwd(MxBase base, const void* X, const qlora_act8* X8, const void
             a.absmax_q = base.nf4->absmax_q;
             a.c2 = base.nf4->c2;
         }
-        a.n8 = d_out * d_in / 8;
-        a.col_tiles = mx_col_tiles(d_in);
-        a.per_row = static_cast<uint32_t>(d_in / 8);
+        a.d_out = d_out;
+        a.d_in = d_in;
         a.w = W;
-        a.ctas_w = static_cast<int>(cdiv(a.n8, 256 * kPrepUnroll));
+        a.ctas_w = static_cast<int>(base.mx ? cdiv(d_out, 128) * mx_col_tiles(d_in) : cdiv(d_out * d_in / 8, 256 * kPrepUnroll));
         a.zero = at<int>(ws, p.pair + p.sched.part_bytes);
         a.n_zero = p.sched.n_cnt;
         QL_TRY(prepare(a));
@@ -657,7 +655,7 @@ qlora_status mxfp4_quantize(const void* W, qlora_dtype w_dtype, int64_t rows, in
 qlora_status mxfp4_dequantize(const qlora_mxfp4* w, void* W_out, qlora_dtype out_dtype, cudaStream_t stream) {
     if (!aligned16(W_out) || (out_dtype != QLORA_F32 && out_dtype != QLORA_BF16)) return QLORA_ERR_INVALID_ARG;
     QL_TRY(check_mxfp4(w));
-    const dim3 grid(mx_ctas(w->d_out * w->d_in / 8));
+    const dim3 grid(static_cast<unsigned>(cdiv(w->d_out, 128) * mx_col_tiles(w->d_in)));
     if (out_dtype == QLORA_F32)
         k_mxfp4_dequant<float><<<grid, 256, 0, stream>>>(w->codes, w->scales, w->d_out, w->d_in,
                                                          static_cast<float*>(W_out));
@@ -717,9 +715,9 @@ qlora_status qlora_act8_quantize(const void* X, qlora_dtype x_dtype, int64_t T, 
     QL_TRY(qlora_act8_sizes(T, d_in, &qb, &sb));
     const int64_t n8 = T * d_in / 8;
     if (x_dtype == QLORA_F32)
-        k_act8_quantize<float><<<mx_ctas(n8), 256, 0, stream>>>(static_cast<const float*>(X), n8, q, scales);
+        k_act8_quantize<float><<<act8_ctas(n8), 256, 0, stream>>>(static_cast<const float*>(X), n8, q, scales);
     else
-        k_act8_quantize<__nv_bfloat16><<<mx_ctas(n8), 256, 0, stream>>>(static_cast<const __nv_bfloat16*>(X), n8, q,
+        k_act8_quantize<__nv_bfloat16><<<act8_ctas(n8), 256, 0, stream>>>(static_cast<const __nv_bfloat16*>(X), n8, q,
                                                                        scales);
     QL_LAUNCH_CHECK();
     return QLORA_OK;
@@ -733,9 +731,9 @@ qlora_status qlora_act8_dequantize(const qlora_act8* a, int64_t T, int64_t d_in,
     QL_TRY(qlora_act8_sizes(T, d_in, &qb, &sb));
     const int64_t n8 = T * d_in / 8;
     if (out_dtype == QLORA_F32)
-        k_act8_dequant<float><<<mx_ctas(n8), 256, 0, stream>>>(a->q, a->scales, n8, static_cast<float*>(X_out));
+        k_act8_dequant<float><<<act8_ctas(n8), 256, 0, stream>>>(a->q, a->scales, n8, static_cast<float*>(X_out));
     else
-        k_act8_dequant<__nv_bfloat16><<<mx_ctas(n8), 256, 0, stream>>>(a->q, a->scales, n8,
+        k_act8_dequant<__nv_bfloat16><<<act8_ctas(n8), 256, 0, stream>>>(a->q, a->scales, n8,
                                                                       static_cast<__nv_bfloat16*>(X_out));
     QL_LAUNCH_CHECK();
     return QLORA_OK;

@@ -769,15 +769,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGemmSmem<MX, BN>
                 last = __shfl_sync(0xffffffffu, ticket, 0) == args.split - 1;
                 if (last) __threadfence();
             }
-            // MX: the columns that the other accumulator shares come first (the last 64 of
-            // buffer 0, the first 64 of buffer 1)
-            const int rot = (MX && buf == 0) ? 6 : 0;
+            auto release = [&]() {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote_async_payload(free_leader + static_cast<uint32_t>(buf * 8));
+            };
+            auto store = [&](int c, const uint32_t (&r)[32]) {
+                const int gc = gc0 + c * 32;
+                if (grow >= args.M) return;
+                __nv_bfloat16* o = args.out + grow * args.ld_out + gc;
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    if (gc + 8 * g + 8 <= args.N && vec_rows) {
+                        uint4 v;
+                        v.x = pack_bf16x2(__uint_as_float(r[8 * g + 0]), __uint_as_float(r[8 * g + 1]));
+                        v.y = pack_bf16x2(__uint_as_float(r[8 * g + 2]), __uint_as_float(r[8 * g + 3]));
+                        v.z = pack_bf16x2(__uint_as_float(r[8 * g + 4]), __uint_as_float(r[8 * g + 5]));
+                        v.w = pack_bf16x2(__uint_as_float(r[8 * g + 6]), __uint_as_float(r[8 * g + 7]));
+                        *reinterpret_cast<uint4*>(o + 8 * g) = v;
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (gc + 8 * g + e < args.N) o[8 * g + e] = __float2bfloat16_rn(__uint_as_float(r[8 * g + e]));
+                    }
+                }
+            };
+            if constexpr (MX) {
+                // the 64 columns that the other accumulator shares (the last of buffer 0, the first of
+                // buffer 1) are read first, and the next tile's MMAs released before anything is stored
+                const int c0 = buf == 0 ? 6 : 0;
+                uint32_t r0[32], r1[32];
+                tmem_ld_32x32b_x32(tbase + c0 * 32, r0);
+                tmem_ld_32x32b_x32(tbase + c0 * 32 + 32, r1);
+                tmem_ld_wait();
+                release();
+                store(c0, r0);
+                store(c0 + 1, r1);
 #pragma unroll 1
-            for (int i = 0; i < BN / 32; ++i) {
-                const int c = (i + rot) & 7;
-                uint32_t r[32];
-                if (last) {
-                    if (split) {
+                for (int i = 0; i < 6; ++i) {
+                    const int c = buf == 0 ? i : i + 2;
+                    tmem_ld_32x32b_x32(tbase + c * 32, r0);
+                    tmem_ld_wait();
+                    store(c, r0);
+                }
+            } else {
+#pragma unroll 1
+                for (int c = 0; c < BN / 32; ++c) {
+                    uint32_t r[32];
+                    if (split && last) {
                         // all other parts' values of the chunk in flight at once, added in K order whichever
                         // part is last
                         float4 o[kPairMaxSplit][8];
@@ -806,34 +845,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGemmSmem<MX, BN>
                             r[4 * g + 2] = __float_as_uint(v[g].z);
                             r[4 * g + 3] = __float_as_uint(v[g].w);
                         }
-                    } else {
+                    } else if (last) {
                         tmem_ld_32x32b_x32(tbase + c * 32, r);
                         tmem_ld_wait();
                     }
-                    const int gc = gc0 + c * 32;
-                    if (grow < args.M) {
-                        __nv_bfloat16* o = args.out + grow * args.ld_out + gc;
-#pragma unroll
-                        for (int g = 0; g < 4; ++g) {
-                            if (gc + 8 * g + 8 <= args.N && vec_rows) {
-                                uint4 v;
-                                v.x = pack_bf16x2(__uint_as_float(r[8 * g + 0]), __uint_as_float(r[8 * g + 1]));
-                                v.y = pack_bf16x2(__uint_as_float(r[8 * g + 2]), __uint_as_float(r[8 * g + 3]));
-                                v.z = pack_bf16x2(__uint_as_float(r[8 * g + 4]), __uint_as_float(r[8 * g + 5]));
-                                v.w = pack_bf16x2(__uint_as_float(r[8 * g + 6]), __uint_as_float(r[8 * g + 7]));
-                                *reinterpret_cast<uint4*>(o + 8 * g) = v;
-                            } else {
-#pragma unroll
-                                for (int e = 0; e < 8; ++e)
-                                    if (gc + 8 * g + e < args.N) o[8 * g + e] = __float2bfloat16_rn(__uint_as_float(r[8 * g + e]));
-                            }
-                        }
-                    }
-                }
-                if (i == (MX ? 1 : BN / 32 - 1)) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_remote_async_payload(free_leader + static_cast<uint32_t>(buf * 8));
+                    if (c == BN / 32 - 1) release();
+                    if (last) store(c, r);
                 }
             }
         }

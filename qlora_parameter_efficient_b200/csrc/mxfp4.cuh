@@ -203,44 +203,53 @@ __device__ __forceinline__ uint4 e2m1_scale8_bf16(uint32_t q, float s) {
     return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
 }
 
-// Eight elements per thread and step: 4 code bytes in, 16 (bf16) or 32 (fp32) bytes out; kMxUnroll
-// steps' loads are issued together.
-constexpr int kMxUnroll = 4;
+// One 128 x 128 tile of a matrix, as mxfp4_quantize_tile lays it out: the tile's 512 bytes of scales in
+// shared memory, sixteen lanes per row, eight rows' codes (4 bytes a lane) in flight, 16 (bf16) or 32 (fp32)
+// bytes out.
+template <typename T>
+__device__ __forceinline__ void mxfp4_dequantize_tile(const uint8_t* __restrict__ codes,
+                                                      const uint8_t* __restrict__ scales, int64_t rows, int64_t cols,
+                                                      int64_t rt, int64_t kt, T* __restrict__ out, uint8_t* s_sc) {
+    const int seg = threadIdx.x & 15, r0 = threadIdx.x >> 4;
+    const int64_t col = kt * 128 + seg * 8;
+    const int64_t left = col < cols ? rows - rt * 128 : 0;
+    const int64_t at = (rt * 128 + r0) * cols + col;
+    uint32_t q[8];
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+        q[p] = 0;
+        if (p * 16 + r0 < left) q[p] = __ldg(reinterpret_cast<const uint32_t*>(codes + (at + p * 16 * cols) / 2));
+    }
+    if (threadIdx.x < kMxTileBytes / 16)
+        reinterpret_cast<uint4*>(s_sc)[threadIdx.x] =
+            __ldg(reinterpret_cast<const uint4*>(scales + (rt * mx_col_tiles(cols) + kt) * kMxTileBytes) + threadIdx.x);
+    __syncthreads();
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+        const int lr = p * 16 + r0;
+        if (lr >= left) continue;
+        const float s = e8m0_value(s_sc[(lr & 31) * 16 + (lr >> 5) * 4 + (seg >> 2)]);
+        T* o = out + at + p * 16 * cols;
+        if constexpr (sizeof(T) == 4) {
+            float f[8];
+            e2m1_scale8(q[p], s, f);
+            reinterpret_cast<float4*>(o)[0] = make_float4(f[0], f[1], f[2], f[3]);
+            reinterpret_cast<float4*>(o)[1] = make_float4(f[4], f[5], f[6], f[7]);
+        } else {
+            *reinterpret_cast<uint4*>(o) = e2m1_scale8_bf16(q[p], s);
+        }
+    }
+}
+
+// grid: one CTA per scale tile, column tiles fastest.
 template <typename T>
 __global__ void __launch_bounds__(256) k_mxfp4_dequant(const uint8_t* __restrict__ codes,
                                                        const uint8_t* __restrict__ scales, int64_t rows,
                                                        int64_t cols, T* __restrict__ out) {
+    __shared__ __align__(16) uint8_t s_sc[kMxTileBytes];
     griddep_enter();
-    const int64_t n8 = rows * cols / 8, kts = mx_col_tiles(cols);
-    const uint32_t per_row = static_cast<uint32_t>(cols / 8);
-    const int64_t i0 = static_cast<int64_t>(blockIdx.x) * (256 * kMxUnroll) + threadIdx.x;
-    uint32_t q[kMxUnroll], e[kMxUnroll];
-#pragma unroll
-    for (int u = 0; u < kMxUnroll; ++u) {
-        const int64_t i = i0 + u * 256;
-        q[u] = e[u] = 0;
-        if (i < n8) {
-            // (a row index by 32-bit division where the matrix has fewer than 2^35 elements)
-            const int64_t row = n8 >> 32 ? i / per_row : static_cast<uint32_t>(i) / per_row;
-            q[u] = __ldg(reinterpret_cast<const uint32_t*>(codes) + i);
-            e[u] = __ldg(scales + mx_scale_offset(row, (i - row * per_row) >> 2, kts));
-        }
-    }
-#pragma unroll
-    for (int u = 0; u < kMxUnroll; ++u) {
-        const int64_t i = i0 + u * 256;
-        if (i >= n8) break;
-        const float s = e8m0_value(e[u]);
-        if constexpr (sizeof(T) == 4) {
-            float f[8];
-            e2m1_scale8(q[u], s, f);
-            float4* o = reinterpret_cast<float4*>(out) + 2 * i;
-            o[0] = make_float4(f[0], f[1], f[2], f[3]);
-            o[1] = make_float4(f[4], f[5], f[6], f[7]);
-        } else {
-            reinterpret_cast<uint4*>(out)[i] = e2m1_scale8_bf16(q[u], s);
-        }
-    }
+    const int64_t kts = mx_col_tiles(cols);
+    mxfp4_dequantize_tile(codes, scales, rows, cols, blockIdx.x / kts, blockIdx.x % kts, out, s_sc);
 }
 
 }  // namespace qlora
