@@ -825,36 +825,40 @@ def _bwd_act(fn, op, w, dev, X, dH, A, B, alpha, U_saved, dX, dA, dB, ws, want_d
         raise ValueError('phase="dx" reads the workspace of the preceding phase="grads" call')
     if accumulate and phase != "dx" and (dA is None or dB is None):
         raise ValueError("accumulate=True adds into dA and dB: both must be given")
-    T, r = dH.shape[0], A.shape[0]
+    T, r, d_out, d_in = dH.shape[0], A.shape[0], w.d_out, w.d_in
     x8 = None
     if isinstance(X, Act8):
-        _need("X.q", X.q, torch.int8, (T, w.d_in), dev)
-        x8 = X._c()
+        _need("X.q", X.q, torch.int8, (T, d_in), dev)
+        x8 = ctypes.byref(X._c())
     else:
-        _need("X", X, bf, (T, w.d_in), dev)
-    _need("dH", dH, bf, (T, w.d_out), dev)
-    _need("A", A, bf, (r, w.d_in), dev)
-    _need("B", B, bf, (w.d_out, r), dev)
-    for name, t, dt, shape in (("U_saved", U_saved, bf, (T, r)), ("dX", dX, bf, (T, w.d_in)),
-                               ("dA", dA, f32, (r, w.d_in)), ("dB", dB, f32, (w.d_out, r))):
-        if t is not None:
-            _need(name, t, dt, shape, dev)
+        _need("X", X, bf, (T, d_in), dev)
+    _need("dH", dH, bf, (T, d_out), dev)
+    _need("A", A, bf, (r, d_in), dev)
+    _need("B", B, bf, (d_out, r), dev)
+    if U_saved is not None:
+        _need("U_saved", U_saved, bf, (T, r), dev)
+    if dX is not None:
+        _need("dX", dX, bf, (T, d_in), dev)
+    if dA is not None:
+        _need("dA", dA, f32, (r, d_in), dev)
+    if dB is not None:
+        _need("dB", dB, f32, (d_out, r), dev)
     with _run_on(dev, stream):
-        ws = _need_ws(op, T, w.d_out, w.d_in, r, dev, ws)
+        ws = _need_ws(op, T, d_out, d_in, r, dev, ws)
         if dX is None and want_dx and phase != "grads":
-            dX = _rows(T, w.d_in, bf, dev)
+            dX = _rows(T, d_in, bf, dev)
         if phase != "dx":
             if dA is None:
-                dA = _rows(r, w.d_in, f32, dev)
+                dA = _rows(r, d_in, f32, dev)
             if dB is None:
-                dB = _rows(w.d_out, r, f32, dev)
+                dB = _rows(d_out, r, f32, dev)
         flags = _BWD_PHASES[phase] | (BWD_ACCUMULATE if accumulate else 0)
-        p8 = ctypes.byref(x8) if x8 is not None else None
-        act = (p8,) if op == OP_BWD_ACT8 else (None if x8 is not None else _addr(X), p8)
-        c = w._c()
-        _check(fn, getattr(load(), fn)(
-            ctypes.byref(c) if isinstance(c, _NF4) else c, *act, _addr(dH), T, _addr(A), _addr(B), r, float(alpha), _addr(U_saved), _addr(dX),
-            _addr(dA), _addr(dB), _addr(ws), ws.nbytes, flags, _raw_stream(dev, stream)))
+        rest = (dH.data_ptr(), T, A.data_ptr(), B.data_ptr(), r, float(alpha), _addr(U_saved), _addr(dX), _addr(dA),
+                _addr(dB), ws.data_ptr(), ws.nbytes, flags, _raw_stream(dev, stream))
+        if op == OP_BWD_ACT8:
+            _check(fn, load().qlora_linear_bwd_act8(ctypes.byref(w._c()), x8, *rest))
+        else:
+            _check(fn, load().qlora_linear_bwd_mxfp4(w._c(), None if x8 else X.data_ptr(), x8, *rest))
     return dX, dA, dB
 
 
