@@ -143,7 +143,34 @@ def load() -> ctypes.CDLL:
         f.argtypes = args
         f.restype = res
     _lib = L
+    _load_binding(L)
     return L
+
+
+_bind = None      # the _mx_bind module: plain microscaled calls without ctypes (see csrc/mx_bind.cpp)
+
+
+def _mx_bind_path():
+    return os.path.join(HERE, "_mx_bind.so")
+
+
+def _load_binding(L):
+    global _bind
+    if not os.path.exists(_mx_bind_path()):
+        return                                   # not built: the same calls go through ctypes
+    _torch()
+    from . import _mx_bind
+    _mx_bind.init(*(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in (
+        "qlora_workspace_bytes", "mxfp4_quantize", "mxfp4_dequantize", "qlora_act8_quantize",
+        "qlora_act8_dequantize", "qlora_linear_fwd_mxfp4", "qlora_linear_bwd_mxfp4", "qlora_linear_bwd_act8")))
+    _bind = _mx_bind
+
+
+def _binding():
+    """The _mx_bind module, or None where it is not built."""
+    if _lib is None:
+        load()
+    return _bind
 
 
 def _check(fn, code):
@@ -707,6 +734,11 @@ def mxfp4_sizes(rows, cols):
 
 def mxfp4_quantize(W, codes=None, scales=None, stream=None) -> MXFP4Weight:
     """Quantize a device fp32/bf16 matrix [rows, cols] (a weight or an activation) to MXFP4."""
+    if codes is None and scales is None and stream is None and _binding() is not None:
+        got = _bind.quantize(False, W)
+        if got.__class__ is tuple:
+            rows, cols = W.shape
+            return _made(MXFP4Weight, codes=got[0], scales=got[1], d_out=rows, d_in=cols)
     torch = _torch()
     dev = _need_cuda("W", W)
     if W.dim() != 2:
@@ -734,8 +766,12 @@ def mxfp4_quantize(W, codes=None, scales=None, stream=None) -> MXFP4Weight:
 
 def mxfp4_dequantize(w: MXFP4Weight, dtype, out=None, stream=None):
     torch = _torch()
-    dev = w.codes.device
     dt = _dtype_code(dtype)
+    if out is None and stream is None and _binding() is not None:
+        got = _bind.dequantize(False, w.codes, w.scales, w.d_out, w.d_in, dt == BF16)
+        if got is not None and got.__class__ is not int:
+            return got
+    dev = w.codes.device
     with _run_on(dev, stream):
         if out is None:
             out = _rows(w.d_out, w.d_in, dtype, dev)
@@ -749,6 +785,10 @@ def qlora_linear_fwd_mxfp4(w: MXFP4Weight, X, A, B, alpha, H=None, U_save=None, 
                            save_u=True):
     """H = Q(X) W^T + (alpha/r) (X A^T) B^T over an MXFP4 base, X (bf16) quantized to MXFP4 inside the
     call for the base product.  Returns (H, U_save)."""
+    if stream is None and _binding() is not None:
+        got = _bind.forward(w.codes, w.scales, w.d_out, w.d_in, X, A, B, alpha, H, U_save, save_u, ws)
+        if got.__class__ is tuple:
+            return got
     torch = _torch()
     bf = torch.bfloat16
     dev = w.codes.device
@@ -776,6 +816,10 @@ def qlora_linear_fwd_mxfp4(w: MXFP4Weight, X, A, B, alpha, H=None, U_save=None, 
 
 def act8_quantize(X, q=None, scales=None, stream=None) -> Act8:
     """8-bit checkpoint of a device fp32/bf16 activation [T, d_in]."""
+    if q is None and scales is None and stream is None and _binding() is not None:
+        got = _bind.quantize(True, X)
+        if got.__class__ is tuple:
+            return _made(Act8, q=got[0], scales=got[1])
     torch = _torch()
     dev = _need_cuda("X", X)
     if X.dim() != 2:
@@ -803,9 +847,13 @@ def act8_quantize(X, q=None, scales=None, stream=None) -> Act8:
 def act8_dequantize(a: Act8, dtype, out=None, stream=None):
     """The checkpoint's values (exact in bf16 and fp32)."""
     torch = _torch()
-    dev = a.q.device
     dt = _dtype_code(dtype)
     T, d_in = a.q.shape
+    if out is None and stream is None and _binding() is not None:
+        got = _bind.dequantize(True, a.q, a.scales, T, d_in, dt == BF16)
+        if got is not None and got.__class__ is not int:
+            return got
+    dev = a.q.device
     with _run_on(dev, stream):
         if out is None:
             out = _rows(T, d_in, dtype, dev)
@@ -866,6 +914,12 @@ def qlora_linear_bwd_mxfp4(w: MXFP4Weight, X, dH, A, B, alpha, U_saved=None, dX=
                            ws=None, stream=None, want_dx=True, accumulate=False, phase="all"):
     """Backward of qlora_linear_fwd_mxfp4 from X, a bf16 tensor or the Act8 checkpoint of one.
     Returns (dX, dA, dB); dA, dB fp32.  accumulate and phase as in qlora_linear_bwd."""
+    if stream is None and phase == "all" and _binding() is not None:
+        x, x8 = (X.q, X.scales) if isinstance(X, Act8) else (X, None)
+        got = _bind.backward(w.codes, w.scales, None, w.d_out, w.d_in, x, x8, dH, A, B, alpha, U_saved, dX, dA, dB,
+                             want_dx, accumulate, ws)
+        if got.__class__ is tuple:
+            return got
     return _bwd_act("qlora_linear_bwd_mxfp4", OP_BWD_MXFP4, w, w.codes.device, X, dH, A, B, alpha, U_saved, dX, dA, dB,
                     ws, want_dx, accumulate, phase, stream)
 
@@ -876,6 +930,11 @@ def qlora_linear_bwd_act8(w: NF4Weight, X8: Act8, dH, A, B, alpha, U_saved=None,
     torch = _torch()
     if not isinstance(X8, Act8):
         raise TypeError("X8 must be an Act8 checkpoint (act8_quantize)")
+    if stream is None and phase == "all" and _binding() is not None:
+        got = _bind.backward(w.codes, w.absmax_q, w.c2, w.d_out, w.d_in, X8.q, X8.scales, dH, A, B, alpha, U_saved,
+                             dX, dA, dB, want_dx, accumulate, ws)
+        if got.__class__ is tuple:
+            return got
     dev = _need_cuda("codes", w.codes)
     _need("codes", w.codes, torch.uint8, (w.d_out, w.d_in // 2), dev)
     for name, t in (("absmax_q", w.absmax_q), ("c2", w.c2)):

@@ -1,6 +1,6 @@
 """Builds libqlora.so in-tree with nvcc for sm_100a (B200).
 
-    python -m qlora_parameter_efficient_b200.build            # release: libqlora.so
+    python -m qlora_parameter_efficient_b200.build            # release: libqlora.so, _mx_bind.so
     python -m qlora_parameter_efficient_b200.build --debug    # libqlora_debug.so, QLORA_DEBUG=1
 
 The debug library checks the kernels' index invariants on the device (a failed check is
@@ -18,6 +18,8 @@ LIB = os.path.join(HERE, "libqlora.so")
 DEBUG_LIB = os.path.join(HERE, "libqlora_debug.so")
 SOURCES = ["qlora_api.cu", "noalloc.cu"]
 DEPS = sorted(f for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh")))
+BINDING = os.path.join(HERE, "_mx_bind.so")      # the short Python way into the microscaled calls
+BINDING_SOURCE = os.path.join(CSRC, "mx_bind.cpp")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "qlora.h")
 
 NVCC_FLAGS = [
@@ -58,5 +60,33 @@ def build_library(force: bool = False, verbose: bool = False, debug: bool = Fals
     return lib
 
 
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    """The CPython module csrc/mx_bind.cpp (host code only: g++ against torch's headers)."""
+    if not force and os.path.exists(BINDING) and all(
+            os.path.getmtime(d) <= os.path.getmtime(BINDING) for d in (BINDING_SOURCE, HEADER)):
+        return BINDING
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc())) or "/usr/local/cuda"
+    includes = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    libs = os.path.join(root, "lib")
+    cmd = [os.environ.get("CXX", "g++"), "-std=c++17", "-O2", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[f"-I{i}" for i in includes],
+           "-o", BINDING + ".tmp", BINDING_SOURCE, f"-L{libs}", "-lc10", "-lc10_cuda", "-ltorch_cpu",
+           "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        sys.stderr.write(res.stdout + res.stderr)
+        raise RuntimeError("g++ failed building _mx_bind.so")
+    os.replace(BINDING + ".tmp", BINDING)
+    return BINDING
+
+
 if __name__ == "__main__":
     print(build_library(force="--force" in sys.argv, verbose=True, debug="--debug" in sys.argv))
+    print(build_binding(force="--force" in sys.argv, verbose=True))
