@@ -72,11 +72,12 @@ PairSched pair_schedule(int64_t M, int64_t N, int64_t k_steps, bool mx) {
     return g;
 }
 
-// Ranks of a weight-stream cluster: as many of 4, 2, 1 as K has stages for and two CTAs per SM can take
-// at once (8 ranks of half the length measured 8.0 against 7.0 us at one token of a 4096 x 4096 layer).
-int mx_ranks(int64_t tiles, int64_t chunks) {
+// Ranks of a weight-stream cluster: as many of 4, 2, 1 as K has stages for and `slots` can take at once,
+// two CTAs per SM at T <= 16 (whose rings are small), one above.  8 ranks of half the length measured 8.4
+// against 7.7 us at one token of a 4096 x 4096 layer, the same at 64 tokens of it.
+int mx_ranks(int64_t ctas, int64_t chunks, int64_t slots) {
     for (int c = 4; c > 1; c >>= 1)
-        if (chunks >= c && tiles * c <= 2 * kSmsForSplit) return c;
+        if (chunks >= c && ctas * c <= slots) return c;
     return 1;
 }
 
@@ -164,9 +165,13 @@ qlora_status launch_mx_stream(const CUtensorMap& tw, const CUtensorMap& tx, cons
                               const CUtensorMap& tu, MxStreamArgs g, cudaStream_t st) {
     using L = MxStreamCfg<NT>;
     static std::atomic<uint64_t> configured{0};
-    QL_TRY(allow_smem(k_mx_stream<NT>, L::kTotal, configured));
-    const int64_t tiles = cdiv(g.d_out, 128), tok = cdiv(g.T, NT);
-    g.ranks = L::kQuant ? mx_ranks(tiles, cdiv(g.k64, 4)) : 1;
+    QL_TRY(allow_smem(k_mx_stream<NT>, L::bytes(L::kAlone), configured));
+    const int64_t tiles = cdiv(g.d_out, 128), tok = cdiv(g.T, NT), chunks = cdiv(g.k64, 4);
+    g.ranks = mx_ranks(tiles * tok, chunks, L::kQuant ? 2 * kSmsForSplit : kSmsForSplit);
+    // a ring of all of the shared memory where each CTA has an SM to itself, no longer than its K
+    g.stages = L::kShared;
+    if (tiles * g.ranks * tok <= kSmsForSplit)
+        g.stages = static_cast<int>(std::min<int64_t>(L::kAlone, std::max<int64_t>(L::kShared, cdiv(chunks, g.ranks) + g.ext_steps)));
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -177,7 +182,7 @@ qlora_status launch_mx_stream(const CUtensorMap& tw, const CUtensorMap& tx, cons
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(tiles * g.ranks), static_cast<unsigned>(tok));
     cfg.blockDim = dim3(L::kThreads);
-    cfg.dynamicSmemBytes = L::kTotal;
+    cfg.dynamicSmemBytes = static_cast<size_t>(L::bytes(g.stages));
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = g.ranks > 1 ? 2 : 1;

@@ -143,6 +143,7 @@ struct MxStreamArgs {
     int k64;                  // d_in / 64: MMAs of the whole contraction
     int col_tiles;            // scale tiles per row of tiles (d_in / 128, rounded up)
     int ranks;                // CTAs per cluster, K split over them
+    int stages;               // of the ring
     int ext_steps;            // adapter K steps of 64, taken by the last rank
     int ext_k16_last;
     const uint8_t* w_scales;
@@ -154,35 +155,71 @@ struct MxStreamArgs {
     uint64_t wait_ns;
 };
 
+// Warps that quantize one stage of X at T <= 16: four rows each, 1, 2 or 4 of them.
+__device__ __forceinline__ int quant_warps(int T) { return T <= 4 ? 1 : (T <= 8 ? 2 : 4); }
+
 // NT: tokens per CTA (the MMA's N): 16 or 64 for calls of up to that many tokens, 128 (a whole scale
-// tile) in several token tiles above.  The cluster has 1, 2, 4 or 8 ranks, so that NT tokens divide
-// evenly over them.
+// tile) in several token tiles above.
 template <int NT>
 struct MxStreamCfg {
     static constexpr int kA = 128 * 128;            // codes of 128 weight rows, one stage
     static constexpr int kB = NT * 128;             // codes of the tokens
     static constexpr int kSf = 1024;                // two scale tiles (each operand)
     static constexpr int kStage = kA + kB + 2 * kSf;
-    // two CTAs per SM
-    static constexpr int kStages = NT <= 16 ? 5 : (NT <= 64 ? 4 : 3);
-    static constexpr int kRing = kStages * kStage;
-    static constexpr int kRed = (NT + 4) * 128 * 4; // partials of this rank's share of the rows (over the ring)
-    static constexpr int kTotal = 1024 + kRing + 256;
+    // stages of the ring where two CTAs share an SM, and where each has one to itself (200 tokens of an
+    // 8192 x 8192 layer 28.6 us with three stages, 26.0 with four or more)
+    static constexpr int kShared = NT <= 16 ? 5 : (NT <= 64 ? 4 : 3);
+    static constexpr int kAlone = NT <= 16 ? 11 : (NT <= 64 ? 8 : 6);
+    static constexpr int bytes(int stages) { return 1024 + stages * kStage + 256; }
     static constexpr bool kQuant = NT == 16;
-    static constexpr int kThreads = 192;
+    static constexpr int kRed = NT * 128 * 4; // partials of this rank's share of the rows (over the ring)
+    static constexpr int kQuantWarps = 8, kQuantGroups = 4;
+    static_assert(!kQuant || kQuantGroups <= kShared, "a group per ring stage at most");
+    static constexpr int kThreads = kQuant ? 64 + 32 * kQuantWarps : 192;
     static constexpr int kAcc = NT < 32 ? 32 : NT;  // accumulator columns
-    static constexpr uint32_t kTmem = NT <= 32 ? 64 : (NT <= 64 ? 128 : 256);   // + 2 x 16 scale columns
-    static_assert(kAcc + 32 <= static_cast<int>(kTmem), "tensor memory");
-    static_assert((kTotal + 1024) * 2 <= 233472 && kRed <= kRing, "shared memory budget");
+    // and sets of 16 scale columns: with two, a stage waits for the last but one to complete
+    static constexpr int kSets = 4;
+    static constexpr uint32_t kTmem = NT <= 64 ? 128 : 256;
+    static_assert(kAcc + 16 * kSets <= static_cast<int>(kTmem), "tensor memory");
+    static_assert((bytes(kShared) + 1024) * 2 <= 233472 && bytes(kAlone) <= 232448 && kRed <= kStage * kShared,
+                  "shared memory budget");
 };
 
-// grid: x = weight tile * ranks + rank, y = token tile; clusters of `ranks` along x (NT = 16 only: joining
-// the partials of more tokens through the cluster's shared memory costs more than the shorter K saves,
-// 44 against 20 us at 200 tokens of an 8192 x 8192 layer).
+// Sum of the C ranks' partials of 128 / C weight rows from col0 on, red[rank][token][row], in the order
+// of the ranks (= of K), and its output columns.  By all threads, two rows each and several at once: one
+// element at a time by four warps took 3 us at 64 tokens, 10 us at 128.
+template <int C, int NT, int THREADS>
+__device__ __forceinline__ void mx_join(const float* red, int t_end, int col0, int t0, const MxStreamArgs& args) {
+    constexpr int R = 128 / C;
+    const bool pairs = !(args.d_out & 1);
+#pragma unroll 4
+    for (int i = 2 * threadIdx.x; i < R * t_end; i += 2 * THREADS) {
+        float x = 0.f, y = 0.f;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const float2 v = *reinterpret_cast<const float2*>(red + c * NT * R + i);
+            x += v.x;
+            y += v.y;
+        }
+        const int col = col0 + i % R;
+        __nv_bfloat16* out = args.out + static_cast<int64_t>(t0 + i / R) * args.d_out + col;
+        if (pairs) {
+            if (col < args.d_out) *reinterpret_cast<__nv_bfloat162*>(out) = __floats2bfloat162_rn(x, y);
+        } else {
+            if (col < args.d_out) out[0] = __float2bfloat16_rn(x);
+            if (col + 1 < args.d_out) out[1] = __float2bfloat16_rn(y);
+        }
+    }
+}
+
+// grid: x = weight tile * ranks + rank, y = token tile; clusters of `ranks` along x.
+// Bound: 24 to 34 KB a stage into one SM, 0.29 us (60 bytes a cycle) however many CTAs run, so K is split
+// until every SM has a CTA: 64 tokens of a 4096 x 11008 layer 28.3 us on 32 SMs, 19.3 us on 128
+// (whole forward, weight out of HBM).
 // Launched with programmatic dependent launch: the weight's tiles are read before the kernel in front
 // (which forms U and, for NT > 16, quantizes X) has finished; that kernel is launched without it, so
 // whatever wrote the weight and X is done.  What it writes is read, and H written, after it has ended.
-// NT = 16: warps 2..5 quantize this rank's part of X into the ring themselves, one block of 32 per
+// NT = 16: warps 2..9 quantize this rank's part of X into the ring themselves, one block of 32 per
 // thread and stage, so that the stream does not wait for another kernel before its last step.
 template <int NT>
 __global__ void __launch_bounds__(MxStreamCfg<NT>::kThreads)
@@ -190,7 +227,7 @@ __global__ void __launch_bounds__(MxStreamCfg<NT>::kThreads)
                 const __grid_constant__ CUtensorMap tmBx, const __grid_constant__ CUtensorMap tmUx,
                 const MxStreamArgs args) {
     using L = MxStreamCfg<NT>;
-    constexpr int S = L::kStages;
+    const int S = args.stages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
@@ -199,14 +236,14 @@ __global__ void __launch_bounds__(MxStreamCfg<NT>::kThreads)
     uint8_t* sSa = sB + S * L::kB;
     uint8_t* sSb = sSa + S * L::kSf;
     float* red = reinterpret_cast<float*>(smem);
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kRing);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + S * L::kStage);
     uint64_t* empty = full + S;
     uint64_t* accf = empty + S;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(accf + 1);
     volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = warp_index(), lane = threadIdx.x & 31;
-    const int C = L::kQuant ? args.ranks : 1;
+    const int C = args.ranks;
     const int rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int tile = blockIdx.x / C;
     const int n0 = tile * 128;
@@ -219,7 +256,7 @@ __global__ void __launch_bounds__(MxStreamCfg<NT>::kThreads)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
-            mbar_init(&full[s], L::kQuant ? 5 : 1);      // the copies, and the four quantizing warps
+            mbar_init(&full[s], L::kQuant ? 1 + quant_warps(args.T) : 1);      // the copies, and the quantizing warps
             mbar_init(&empty[s], 1);
         }
         mbar_init(accf, 1);
@@ -302,11 +339,12 @@ __global__ void __launch_bounds__(MxStreamCfg<NT>::kThreads)
         const uint32_t idesc0 = make_idesc_mxf4(128, NT, 0, 0), idesc2 = make_idesc_mxf4(128, NT, 2, 2);
         const uint64_t a_desc = make_sw128_desc(smem_u32(sA), 16, 1024), b_desc = make_sw128_desc(smem_u32(sB), 16, 1024);
         const uint64_t sa_desc = make_scale_desc(smem_u32(sSa)), sb_desc = make_scale_desc(smem_u32(sSb));
-        // scale columns are used in turn: those of step it - 2 are free once its MMAs are done
+        // sets of scale columns are used in turn: that of step it - kSets is free once its MMAs are done
+        // (a ring of no more stages than sets has waited for that already)
         int s2 = 0, ph2 = 0;
         for (int it = 0, s = 0, ph = 0; it < n_iters; ++it) {
             bool ok = mbar_wait_uniform(&full[s], ph, abort, args.wait_ns);
-            if (ok && it >= 2) {
+            if (ok && S > L::kSets && it >= L::kSets) {
                 ok = mbar_wait_uniform(&empty[s2], ph2, abort, args.wait_ns);
                 if (++s2 == S) s2 = 0, ph2 ^= 1;
             }
@@ -319,7 +357,7 @@ __global__ void __launch_bounds__(MxStreamCfg<NT>::kThreads)
             const uint64_t ad = a_desc + static_cast<uint32_t>(s * (L::kA >> 4));
             const uint64_t bd = b_desc + static_cast<uint32_t>(s * (L::kB >> 4));
             if (it < n_main) {
-                const uint32_t sfa = tmem + L::kAcc + (it & 1) * 16, sfb = sfa + 8;
+                const uint32_t sfa = tmem + L::kAcc + (it % L::kSets) * 16, sfb = sfa + 8;
                 const uint64_t sad = sa_desc + static_cast<uint32_t>(s * (L::kSf >> 4));
                 const uint64_t sbd = sb_desc + static_cast<uint32_t>(s * (L::kSf >> 4));
                 const int nk = mmas_of(it);
@@ -351,8 +389,13 @@ __global__ void __launch_bounds__(MxStreamCfg<NT>::kThreads)
         }
         if (elect_one()) umma_commit(accf);
     } else if constexpr (L::kQuant) {
-        // token `row`, block `blk` of each stage's 256 columns
-        const int td = threadIdx.x - 64, row = td >> 3, blk = td & 7;
+        // Groups of just the warps whose rows there are (four rows each), every group its own stages in
+        // turn: quantizing one takes a warp longer (0.6 us) than the stream brings one.  No more groups
+        // than ring stages: the wait for a slot tells its last two uses apart, so a group may ask for it
+        // only after having seen the use before the last one end.  Token `row`, block `blk` of a
+        // stage's 256 columns; rows past T are left as they are (they reach the output columns past T only).
+        const int G = quant_warps(args.T), groups = min(L::kQuantGroups, L::kQuantWarps / G), qw = warp - 2;
+        const int row = qw % G * 4 + (lane >> 3), blk = lane & 7;
         const bool in = row < args.T;
         const __nv_bfloat16* src = args.X + row * args.d_in + static_cast<int64_t>(c_begin) * 256 + blk * 32;
         auto fetch = [&](int it, Raw8<__nv_bfloat16> (&raw)[4]) {
@@ -364,16 +407,18 @@ __global__ void __launch_bounds__(MxStreamCfg<NT>::kThreads)
             }
         };
         Raw8<__nv_bfloat16> nxt[4];
-        fetch(0, nxt);
-        for (int it = 0, s = 0, ph = 0; it < n_iters; ++it) {
+        int it = qw / G < groups ? qw / G : n_iters, s = it, ph = 0;
+        fetch(it, nxt);
+        for (; it < n_iters; it += groups, s += groups) {
+            while (s >= S) s -= S, ph ^= 1;
             Raw8<__nv_bfloat16> cur[4] = {nxt[0], nxt[1], nxt[2], nxt[3]};
-            fetch(it + 1, nxt);
+            fetch(it + groups, nxt);
             if (!mbar_wait_warp(&empty[s], ph ^ 1, abort, args.wait_ns)) {
                 set_error(args.err, kErrTimeout);
                 *abort = 1;
                 break;
             }
-            if (it < n_main) {
+            if (it < n_main && in) {
                 uint32_t e, q[4];
                 mxfp4_block32(cur, e, q);
                 *reinterpret_cast<uint4*>(sB + s * L::kB + row * 128 + ((blk ^ (row & 7)) << 4)) =
@@ -383,7 +428,6 @@ __global__ void __launch_bounds__(MxStreamCfg<NT>::kThreads)
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&full[s]);
-            if (++s == S) s = 0, ph ^= 1;
         }
     }
     __syncwarp();
@@ -393,16 +437,17 @@ __global__ void __launch_bounds__(MxStreamCfg<NT>::kThreads)
     const int row = n0 + q * 32 + lane;                // weight row = output column
     const uint32_t tbase = tmem + (static_cast<uint32_t>(q * 32) << 16);
     const int t_end = min(NT, args.T - t0);
-    if (warp >= 2) {
+    const bool store = warp >= 2 && warp < 6;          // one warp for each quarter
+    if (store) {
         if (!mbar_wait_warp(accf, 0, nullptr, args.wait_ns)) {
             set_error(args.err, kErrTimeout);
             *abort = 1;
         }
         tc_fence_after();
     }
-    if (!L::kQuant || C == 1) {
+    if (C == 1) {
         griddep_wait();          // earlier kernels of the stream may still read or write H
-        if (warp >= 2 && !*abort) {
+        if (store && !*abort) {
 #pragma unroll 1
             for (int c0 = 0; c0 < t_end; c0 += 16) {
                 uint32_t r[16];
@@ -415,39 +460,32 @@ __global__ void __launch_bounds__(MxStreamCfg<NT>::kThreads)
                             __float2bfloat16_rn(__uint_as_float(r[j]));
             }
         }
-    } else if constexpr (L::kQuant) {
+    } else {
         // rank o sums the weight rows [o R, (o + 1) R): every rank sends it its partials of them,
-        // red[source rank][row][tokens], once every rank's MMAs are done with the ring underneath
-        constexpr int kLd = NT + 4;
+        // red[source rank][token][row], once every rank's MMAs are done with the ring underneath; a
+        // warp's 32 rows go as one line
         const int R = 128 / C;
         cluster_barrier();
-        if (warp >= 2 && !*abort) {
+        if (store && !*abort) {
             const int lr = q * 32 + lane;
-            const uint32_t dst = mapa_shared(smem_u32(red + (rank * R + lr % R) * kLd), static_cast<uint32_t>(lr / R));
+            const uint32_t dst = mapa_shared(smem_u32(red + rank * NT * R + lr % R), static_cast<uint32_t>(lr / R));
 #pragma unroll 1
             for (int c0 = 0; c0 < t_end; c0 += 16) {
                 uint32_t r[16];
                 tmem_ld_32x32b_x16(tbase + c0, r);
                 tmem_ld_wait();
 #pragma unroll
-                for (int g = 0; g < 4; ++g)
-                    if (c0 + 4 * g < t_end)
-                        asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + (c0 + 4 * g) * 4),
-                                     "r"(r[4 * g]), "r"(r[4 * g + 1]), "r"(r[4 * g + 2]), "r"(r[4 * g + 3])
-                                     : "memory");
+                for (int j = 0; j < 16; ++j)
+                    if (c0 + j < t_end)
+                        asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(dst + (c0 + j) * R * 4), "r"(r[j]) : "memory");
             }
         }
         cluster_barrier();
         griddep_wait();
-        if (warp >= 2 && !*abort) {
-            const int col0 = n0 + rank * R;
-            for (int i = threadIdx.x - 64; i < R * t_end; i += 128) {
-                const int rl = i % R, t = i / R;
-                float acc = 0.f;
-                for (int c = 0; c < C; ++c) acc += red[(c * R + rl) * kLd + t];
-                if (col0 + rl < args.d_out)
-                    args.out[static_cast<int64_t>(t0 + t) * args.d_out + col0 + rl] = __float2bfloat16_rn(acc);
-            }
+        if (!*abort) {
+            if (C == 2) mx_join<2, NT, L::kThreads>(red, t_end, n0 + 64 * rank, t0, args);
+            else if (C == 4) mx_join<4, NT, L::kThreads>(red, t_end, n0 + 32 * rank, t0, args);
+            else mx_join<8, NT, L::kThreads>(red, t_end, n0 + 16 * rank, t0, args);
         }
     }
     tc_fence_before();
