@@ -396,7 +396,8 @@ qlora_status mxfp4_dequantize(const qlora_mxfp4* w, void* W_out, qlora_dtype out
  * Q(X) the MXFP4 value of X (as mxfp4_quantize), W the stored weight; the base product runs on
  * block-scaled 4-bit tensor cores (exact products, fp32 accumulation), the adapter term takes the
  * unquantized X and is added in the same accumulator with (alpha/r) X A^T rounded to bf16.
- * Any T >= 1, from single tokens up.  U_save as in qlora_linear_fwd.  [MF] "Intrinsic Dimensionality and Low-Rank Parameter Dynamics".
+ * Any T >= 1, from single tokens up.  U_save as in qlora_linear_fwd.
+ * [MF] "Intrinsic Dimensionality and Low-Rank Parameter Dynamics".
  * ws >= qlora_workspace_bytes(QLORA_OP_FWD_MXFP4, QLORA_BF16, T, d_out, d_in, r).
  * Stream order holds for every argument, as for the other calls.                               */
 qlora_status qlora_linear_fwd_mxfp4(const qlora_mxfp4* w, const void* X, int64_t T, const void* A,
@@ -416,7 +417,8 @@ qlora_status qlora_act8_sizes(int64_t T, int64_t d_in, size_t* q_bytes, size_t* 
 
 /* Keep X (bf16 or fp32, device) as 8-bit: per block of 32 e = floor(log2 max|x|) + 127 (0 where
  * that is less), q = x 2^(133 - e) rounded to nearest even, to at most 127 in magnitude: the error
- * is at most 2^-7 of the block's largest |x|, and half of that except at |q| = 127.  Bit-exact.  */
+ * is half a step, below a whole one where 128 would not fit, and in either case at most 2^-7 of the
+ * block's largest |x| (if that is 2^-127 at least).  Bit-exact, deterministic.                  */
 qlora_status qlora_act8_quantize(const void* X, qlora_dtype x_dtype, int64_t T, int64_t d_in,
                                  int8_t* q, uint8_t* scales, cudaStream_t stream);
 
@@ -429,10 +431,11 @@ qlora_status qlora_act8_dequantize(const qlora_act8* a, int64_t T, int64_t d_in,
  *   dX = dH W + s (dH B) A,   dA = s (dH B)^T X~,   dB = s dH^T (X~ A^T),   s = alpha/r,
  * X~ = X or the checkpoint's values.  U_saved (nullable): the forward's U, used for X~ A^T.  dX
  * (nullable: skipped) in bf16; dA, dB fp32, with s (dH B) and a recomputed U carried to the tensor
- * cores as pairs of bf16 (16 significant bits).  flags as in qlora_linear_bwd_ex, the two-phase form
- * included (QLORA_BWD_DX_FROM_WS reads no activation, but one must be given).
+ * cores as three bf16 numbers each (24 significant bits).  flags as in qlora_linear_bwd_ex, the
+ * two-phase form included (QLORA_BWD_DX_FROM_WS reads no activation, but one must be given).
  * [MF] "Gradient Dynamics and Backpropagation Mechanics".
- * ws >= qlora_workspace_bytes(QLORA_OP_BWD_MXFP4, QLORA_BF16, T, d_out, d_in, r): no copy of X.   */
+ * ws >= qlora_workspace_bytes(QLORA_OP_BWD_MXFP4, QLORA_BF16, T, d_out, d_in, r): above 64 tokens the
+ * weight decoded to bf16 (2 d_out d_in bytes) is in it, a copy of X never.                       */
 qlora_status qlora_linear_bwd_mxfp4(const qlora_mxfp4* w, const void* X, const qlora_act8* X8,
                                     const void* dH, int64_t T, const void* A, const void* B,
                                     int32_t r, float alpha, const void* U_saved, void* dX, float* dA,

@@ -9,8 +9,14 @@ namespace {
 
 constexpr int pad8(int64_t n) { return static_cast<int>((n + 7) / 8 * 8); }   // whole 16-byte units of bf16
 constexpr int64_t kMaxDim = 1LL << 30;
-constexpr int64_t kMxStreamMaxT = 512;
-constexpr int64_t kDxFewT = 128;
+// Up to this many tokens the MXFP4 forward streams the weight past tiles of 128 tokens, above it computes
+// 256 x 256 tiles.  Stream against tiles (us): 300 tokens of 11008 x 4096 21.2, 28.4; of 4096 x 4096 18.1,
+// 19.3; of 8192 x 8192 29.3, 28.2; 400 of the same layers 28.9, 29.0; 18.9, 19.7; 33.3, 31.1.
+constexpr int64_t kMxStreamMaxT = 384;
+// Up to this many tokens (one tile of k_act_gemm) dX decodes the weight in the CTA, above it reads the
+// weight decoded to bf16 beforehand.  The whole backward that way and that (us): 64 tokens of 4096 x 4096
+// 29, 33; of 8192 x 8192 58, 77; of 2048 x 2048 23.4, 22.7; 128 tokens (two tiles) 36, 35; 79, 80; 27, 22.7.
+constexpr int64_t kDxFewT = 64;
 
 qlora_status mx_check_dims(int64_t rows, int64_t cols) {
     if (rows < 1 || rows > kMaxDim || cols < 64 || cols % 64 || cols > kMaxDim) return QLORA_ERR_UNSUPPORTED;
@@ -192,8 +198,10 @@ qlora_status launch_mx_stream(const CUtensorMap& tw, const CUtensorMap& tx, cons
 }
 
 // One launch of one or two adapter products.  The cluster size (K ranks) is the one with the shortest
-// schedule on 148 SMs, one CTA each, by the measured costs: a K step of a bf16 product 1 (0.33 us), of a
-// triple 1.3, of one whose operand is decoded or quantized on the way 1.8, a CTA besides 8.
+// schedule by the measured costs: a K step of a bf16 product 1 (0.33 us), of a triple 1.3, of one whose
+// operand is decoded or quantized on the way 1.8, a CTA besides 8.  One CTA fills an SM, and clusters do not
+// fill the card: 33 clusters of four and 15 of eight run at once (cudaOccupancyMaxActiveClusters; dX of 16 tokens,
+// 2048 x 2048, as 16 clusters of eight 25.2 us with the rest, as 16 of four 21.5).
 struct ActLaunch {
     ActGemmArgs g{};
     CUtensorMap a[2], b[2];
@@ -205,7 +213,6 @@ struct ActLaunch {
         j.N = N;
         j.K = K;
         j.k_steps = static_cast<int>(cdiv(K, 64));
-        j.n_tiles = 1;
         j.scale = 1.f;
         return j;
     }
@@ -223,26 +230,31 @@ qlora_status launch_act_gemm(ActLaunch& l, int* err, cudaStream_t st) {
     int64_t tiles = 0;
     int steps = 1 << 30;
     for (int i = 0; i < l.n; ++i) {
-        tiles += cdiv(l.g.job[i].M, 128) * l.g.job[i].n_tiles;
+        tiles += cdiv(l.g.job[i].M, 128);
         steps = std::min(steps, l.g.job[i].mx_codes ? (l.g.job[i].k_steps + 1) / 2 : l.g.job[i].k_steps);
     }
     double best = 0;
     for (int c = 1; c <= 8 && c <= steps; c *= 2) {
-        // one wave ends with its longest CTA; several end, on average, half a CTA after an even share
-        double total = 0, longest = 0;
+        // one wave ends with its longest CTA, several of equal CTAs are whole; others end, on average, half a CTA
+        // after an even share
+        const double slots = c == 8 ? 120 : c == 4 ? 132 : kSmsForSplit;
+        double total = 8.0 * l.g.qx_tiles, longest = 0;
         for (int i = 0; i < l.n; ++i) {
             const ActJob& j = l.g.job[i];
             const double one = cdiv(j.k_steps, c) * ((j.op != kOpBf16 || j.mx_codes) ? 1.8 : j.triple ? 1.3 : 1.0) + 8;
-            total += one * cdiv(j.M, 128) * j.n_tiles * c;
+            total += one * cdiv(j.M, 128) * c;
             longest = std::max(longest, one);
         }
-        const double cost = tiles * c <= kSmsForSplit ? longest : total / kSmsForSplit + longest / 2;
+        const int64_t ctas = tiles * c + l.g.qx_tiles;
+        const double cost = ctas <= slots                     ? longest
+                            : l.n == 1 && l.g.qx_tiles == 0 ? std::ceil(static_cast<double>(ctas) / slots) * longest
+                                                              : total / slots + longest / 2;
         if (c == 1 || cost < best) {
             best = cost;
             l.g.ranks = c;
         }
     }
-    l.g.tiles0 = static_cast<int>(cdiv(l.g.job[0].M, 128) * l.g.job[0].n_tiles);
+    l.g.tiles0 = static_cast<int>(cdiv(l.g.job[0].M, 128));
     l.g.tiles = static_cast<int>(tiles);
     l.g.pad.ctas = static_cast<int>(cdiv(l.g.pad.ctas, l.g.ranks)) * l.g.ranks;
     l.g.qx_ctas = static_cast<int>(cdiv(l.g.qx_tiles, l.g.ranks)) * l.g.ranks;
@@ -385,11 +397,13 @@ qlora_status mx_fwd(const qlora_mxfp4* w, const void* X, int64_t T, const void* 
         ju.ld = RP;
         ju.out2 = static_cast<bf*>(U_save);
         const int64_t qx_tiles = cdiv(T, 128) * mx_col_tiles(d_in);
-        if (cdiv(T, 128) * 8 > kSmsForSplit / 2) {
+        if (cdiv(T, 128) > 5) {
             ju.mx_codes = codes;
             ju.mx_scales = scales;
         } else {
-            // few token tiles: their CTAs (8 at most for each) would be slow at it, the other SMs are free
+            // few token tiles: their CTAs (8 at most for each) would be slow at it, the other SMs are free (640
+            // tokens of 8192 x 8192 44.3 us against 44.7, of 4096 x 4096 20.0 against 22.4; 768 tokens 47.2
+            // against 45.0, 22.9 against 22.5)
             l.g.qx = static_cast<const bf*>(X);
             l.g.qx_rows = T;
             l.g.qx_cols = d_in;
@@ -553,8 +567,6 @@ qlora_status mx_bwd(MxBase base, const void* X, const qlora_act8* X8, const void
     if (want_dx && T <= kDxFewT) {
         ActLaunch l;
         ActJob& j = l.add(d_in, static_cast<int>(T), d_out);
-        const int rpt = T <= 64 ? 64 : 128;
-        j.n_tiles = static_cast<int>(cdiv(T, rpt));
         j.ext_steps = RP / 64;
         j.out = dX;
         if (base.mx) {
@@ -568,11 +580,11 @@ qlora_status mx_bwd(MxBase base, const void* X, const qlora_act8* X8, const void
             j.ld_scales = d_in / 64;
         }
         QL_TRY(tmap_u8(&l.a[0], base.mx ? base.mx->codes : base.nf4->codes, d_out, d_in / 2, d_in / 2, 64, 64));
-        QL_TRY(tmap_bf16(&l.b[0], dH, T, d_out, dh_ld, static_cast<uint32_t>(rpt)));
+        QL_TRY(tmap_bf16(&l.b[0], dH, T, d_out, dh_ld, 64));
         QL_TRY(tmap_bf16(&l.a[1], A, r, d_in, d_in, 64));
-        QL_TRY(tmap_bf16(&l.b[1], g3, T, r, tr.ld, static_cast<uint32_t>(rpt)));
+        QL_TRY(tmap_bf16(&l.b[1], g3, T, r, tr.ld, 64));
         l.pdl = !first;
-        QL_TRY(act_gemm<kRoleDx>(rpt, l, err, st));
+        QL_TRY((launch_act_gemm<64, kRoleDx>(l, err, st)));
     } else if (want_dx) QL_TRY(dx_gemm(W, dH, dh_ld, T, d_out, d_in, g3, A, RP, r, dX, p.sched, at<void>(ws, p.pair), err, st));
     if (grads) {
         // dA^T[d_in, r] = X~^T (s G) and dB[d_out, r] = s dH^T U

@@ -7,7 +7,7 @@ from test_mx_gpu import check_backward, check_forward, q  # noqa: F401 (q: fixtu
 
 pytestmark = pytest.mark.gpu
 
-ROUTES = [1, 4, 5, 8, 9, 16, 17, 64, 65, 128, 129, 512, 513]
+ROUTES = [1, 4, 5, 8, 9, 16, 17, 64, 65, 128, 129, 384, 385, 512, 513]
 
 
 @pytest.mark.parametrize("d_out", [1, 2, 3, 7])
