@@ -947,9 +947,43 @@ def extra_rows(q, torch, S, dev, peaks, args):
         out["merge_4096x4096_r16_bf16"] = {"us": med, "us_min": mn, "GB/s": byts / (med * 1e-6) / 1e9,
                                            "hbm_frac": byts / (med * 1e-6) / 1e9 / hbm}
 
+    # ---- MXFP4 base on the q_proj shape: the forward at 1, 64 and 4096 tokens and the backward from the
+    # 8-bit checkpoint; t_roof of the forward's product at four times the bf16 peak
+    def microscaled_rows():
+        c2_ = S.CONFIGS["q_proj_4096x4096_r16_T4096"]
+        d, k, r, alpha = c2_["d_out"], c2_["d_in"], c2_["r"], c2_["alpha"]
+        gen = torch.Generator(device=dev)
+        gen.manual_seed(17)
+        w0 = q.mxfp4_quantize(torch.randn((d, k), generator=gen, device=dev) * (0.02 ** 0.5))
+        wl = [q.MXFP4Weight(w0.codes.clone(), w0.scales.clone(), d, k) for _ in range(32)]
+        A = (torch.randn((r, k), generator=gen, device=dev) / r ** 0.5).to(bf)
+        B = (torch.randn((d, r), generator=gen, device=dev) * 0.1).to(bf)
+        fast = dict(peaks, bf16_tflops=4 * tc)
+        for T in (1, 64, 4096):
+            X = torch.randn((T, k), generator=gen, device=dev).to(bf)
+            H, U = torch.empty((T, d), dtype=bf, device=dev), torch.empty((T, r), dtype=bf, device=dev)
+            ws = torch.empty(q.workspace_bytes(q.OP_FWD_MXFP4, q.BF16, T, d, k, r), dtype=torch.uint8, device=dev)
+            med, mn = _graph_time(torch, [(lambda w=w: q.qlora_linear_fwd_mxfp4(w, X, A, B, alpha, H=H, U_save=U, ws=ws))
+                                          for w in wl], reps=10)
+            byts = 0.53125 * d * k + 2 * T * (k + d) + 2 * r * (d + k)
+            out[f"mxfp4_fwd_4096x4096_r16_T{T}"] = {"us": med, "us_min": mn, "bytes": byts,
+                                                    "t_roof_us": t_roof(flops_fwd(T, d, k, r), byts, fast) * 1e6}
+        dH = torch.randn((T, d), generator=gen, device=dev).to(bf)
+        X8 = q.act8_quantize(X)
+        dX = torch.empty((T, k), dtype=bf, device=dev)
+        dA = torch.empty((r, k), dtype=torch.float32, device=dev)
+        dB = torch.empty((d, r), dtype=torch.float32, device=dev)
+        ws = torch.empty(q.workspace_bytes(q.OP_BWD_MXFP4, q.BF16, T, d, k, r), dtype=torch.uint8, device=dev)
+        med, mn = _graph_time(torch, [(lambda w=w: q.qlora_linear_bwd_mxfp4(w, X8, dH, A, B, alpha, U_saved=U, dX=dX,
+                                                                            dA=dA, dB=dB, ws=ws)) for w in wl], reps=3)
+        byts = 0.53125 * d * k + (1.03125 * k + 2 * d + 2 * k) * T + 6 * r * (d + k)
+        out["mxfp4_bwd_checkpoint_4096x4096_r16_T4096"] = {
+            "us": med, "us_min": mn, "bytes": byts, "t_roof_us": t_roof(flops_bwd(T, d, k, r), byts, peaks) * 1e6}
+
     for name, fn in (("decode", decode_rows), ("mlp", mlp_row), ("proj70b", proj70b_rows),
                      ("batched", batched_rows), ("multi", multi_row), ("dora", dora_row),
-                     ("fp8", fp8_row), ("adamw", adamw_row), ("merge", merge_row)):
+                     ("fp8", fp8_row), ("adamw", adamw_row), ("merge", merge_row),
+                     ("microscaled", microscaled_rows)):
         guarded(name, fn)
     return out
 

@@ -143,11 +143,11 @@ def load() -> ctypes.CDLL:
         f.argtypes = args
         f.restype = res
     _lib = L
-    _load_binding(L)
     return L
 
 
-_bind = None      # the _mx_bind module: plain microscaled calls without ctypes (see csrc/mx_bind.cpp)
+_bind = None                # the _mx_bind module: plain microscaled calls without ctypes (csrc/mx_bind.cpp)
+_bind_looked_for = False
 
 
 def _mx_bind_path():
@@ -155,8 +155,9 @@ def _mx_bind_path():
 
 
 def _load_binding(L):
-    global _bind
+    global _bind, _bind_looked_for
     if not os.path.exists(_mx_bind_path()):
+        _bind_looked_for = True
         return                                   # not built: the same calls go through ctypes
     _torch()
     from . import _mx_bind
@@ -164,12 +165,13 @@ def _load_binding(L):
         "qlora_workspace_bytes", "mxfp4_quantize", "mxfp4_dequantize", "qlora_act8_quantize",
         "qlora_act8_dequantize", "qlora_linear_fwd_mxfp4", "qlora_linear_bwd_mxfp4", "qlora_linear_bwd_act8")))
     _bind = _mx_bind
+    _bind_looked_for = True
 
 
 def _binding():
-    """The _mx_bind module, or None where it is not built."""
-    if _lib is None:
-        load()
+    """The _mx_bind module (loaded at the first microscaled call), or None where it is not built."""
+    if not _bind_looked_for:
+        _load_binding(load())
     return _bind
 
 

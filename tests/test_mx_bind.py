@@ -13,9 +13,7 @@ def bind():
     from qlora_parameter_efficient_b200 import build
     build.build_library()
     build.build_binding()
-    q.load()
-    if q._bind is None:            # the library was loaded before the binding was built
-        q._load_binding(q.load())
+    q._load_binding(q.load())       # (looked for before it was built, it stays away otherwise)
     assert q._bind is not None and q._bind.__file__ == _mx_bind_path()
     return q._bind
 
