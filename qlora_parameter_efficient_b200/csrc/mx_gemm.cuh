@@ -596,9 +596,11 @@ struct PairGemmSmem {
 // over `split` pairs each (bf16 only: an MXFP4 tile is over before a join would be).  Every epilogue
 // warp of a split tile writes its fp32 partial and takes a ticket; the last adds all partials in K
 // order, so the result does not depend on which is last, and no CTA waits for another.
-// Bound by the tensor cores (256 x 256 x 256 MXFP4 or x 64 bf16 in 512 cycles; 32 to 35 KB per SM and
-// stage out of L2 fit beside): 4096^3 in 35.1 us MXFP4 (3.9 PFLOP/s; a stage 0.393 us under the power cap, 0.365
-// without its loads) and 93 us bf16 (1.48 PFLOP/s); 8192 tokens of 11008 x 4096 in 470 us (bf16, 1.57).
+// Bound by the tensor cores (256 x 256 x 256 MXFP4 or x 64 bf16 in 512 cycles) where K is long and the
+// waves are full: 8192 tokens of 11008 x 4096 in 470 us (bf16, 1.57 PFLOP/s, tensor pipe 94 % busy).  4096^3 takes
+// 93 us in bf16 (76 % busy) and 35.1 in MXFP4 (3.9 PFLOP/s, 48 %): 3.46 waves in 4, 620 cycles a stage
+// (the 35 KB of its loads come at 55 bytes a cycle), and between two tiles the time to read the columns
+// that their accumulators share.
 template <bool MX, int BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGemmSmem<MX, BN>::kThreads, 1)
     k_pair_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
