@@ -21,6 +21,7 @@
 #include "common.cuh"
 #include "mxfp4.cuh"
 #include "nf4.cuh"
+#include "ring.cuh"
 
 namespace qlora {
 
@@ -233,6 +234,7 @@ struct ActGemmSmem {
     static constexpr int kLdRed = RPT + 4;                      // floats per row of the joining buffer
     static_assert(kTotal <= 232448 && 128 * kLdRed * 4 <= kRing, "shared memory budget");
     static_assert(3 * (kA + kRaw + 3 * RPT / 64 * kChunk) <= kRing, "three stages at least");
+    static_assert(ring_min_stages(kGroups) <= 3, "stages that the groups can share");
 };
 
 // Warp 0: TMA; warp 1: MMA; warps 2..9 and, up to rank 64, 10..17: int8 decode or MXFP4 quantization, one
@@ -481,11 +483,11 @@ __global__ void __launch_bounds__(ActGemmSmem<RPT>::kThreads, 1)
             if (++acc_i == NA) acc_i = 0, acc_ph ^= 1;
         };
         // pairs of stages in turn
-        int s = 2 * group, ph = 0;
-        if (s >= S) s -= S, ph ^= 1;
-        auto skip = [&](int n) {
-            s += n;
-            if (s >= S) s -= S, ph ^= 1;
+        RingPos at(S, kRingRun * group);
+        auto landed = [&]() {
+            return ring_landed<L::kGroups>(
+                at, [&](int i, int par) { return mbar_wait_warp(&empty[i], par, abort, args.wait_ns); },
+                [&](int i, int par) { return mbar_wait_warp(&full[i], par, abort, args.wait_ns); });
         };
         int drained = 0;
         // after the pair at it0: the segments whose MMAs are behind it (those of the next rounds then find
@@ -524,8 +526,9 @@ __global__ void __launch_bounds__(ActGemmSmem<RPT>::kThreads, 1)
                     const uint32_t ev = e[u];
                     const float cv = c2[u];
                     fetch(it0 + u + 2 * L::kGroups, e[u], c2[u]);
-                    ok = mbar_wait_warp(&full[s], ph, abort, args.wait_ns);
+                    ok = landed();
                     if (!ok) break;
+                    const int s = at.s;
                     if (it0 + u < n_main) {
                         // (codes outside the weight are 0: the value 0 in MXFP4; NF4's is not, but meets only
                         // rows of dH that are 0 or columns past d_in)
@@ -547,9 +550,9 @@ __global__ void __launch_bounds__(ActGemmSmem<RPT>::kThreads, 1)
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&decoded[s]);
-                    skip(1);
+                    at.skip(1);
                 }
-                if (L::kGroups > 1) skip(2);
+                at.skip(kRingRun * (L::kGroups - 1));
                 if (drains) drain_behind(it0);
             }
         } else if ((ROLE == kRoleUG || ROLE == kRoleAB) && dec) {
@@ -576,8 +579,9 @@ __global__ void __launch_bounds__(ActGemmSmem<RPT>::kThreads, 1)
                     if (!ok || it0 + u >= n_iters) break;
                     const float st = act8_step(e[u]);
                     e[u] = scale_at(it0 + u + 2 * L::kGroups);
-                    ok = mbar_wait_warp(&full[s], ph, abort, args.wait_ns);
+                    ok = landed();
                     if (!ok) break;
+                    const int s = at.s;
                     // (elements outside the matrix were filled with 0 by the copy)
                     const uint4* src = reinterpret_cast<const uint4*>(sR + s * L::kRaw + td * 32);
                     const uint4 v0 = src[0], v1 = src[1];
@@ -589,9 +593,9 @@ __global__ void __launch_bounds__(ActGemmSmem<RPT>::kThreads, 1)
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&decoded[s]);
-                    skip(1);
+                    at.skip(1);
                 }
-                if (L::kGroups > 1) skip(2);
+                at.skip(kRingRun * (L::kGroups - 1));
                 if (drains) drain_behind(it0);
             }
         } else if (quant) {
@@ -607,8 +611,9 @@ __global__ void __launch_bounds__(ActGemmSmem<RPT>::kThreads, 1)
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     if (!ok || it0 + u >= n_iters) break;
-                    ok = mbar_wait_warp(&full[s], ph, abort, args.wait_ns);
+                    ok = landed();
                     if (!ok) break;
+                    const int s = at.s;
                     const uint8_t* src = sA + s * L::kA + row * 128;
                     Raw8<__nv_bfloat16> raw[4];
 #pragma unroll
@@ -623,10 +628,10 @@ __global__ void __launch_bounds__(ActGemmSmem<RPT>::kThreads, 1)
                             make_uint4(v[0], v[1], v[2], v[3]);
                     e |= __shfl_xor_sync(0xffffffffu, e, 1) << 8;        // (of the even lane: both blocks' bytes)
                     e_word |= e << (16 * u);
-                    skip(1);
+                    at.skip(1);
                 }
                 if (ok && in && b == 0) *reinterpret_cast<uint32_t*>(word + (it0 >> 1) * kMxTileBytes) = e_word;
-                if (L::kGroups > 1) skip(2);
+                at.skip(kRingRun * (L::kGroups - 1));
                 if (drains) drain_behind(it0);
             }
         }
