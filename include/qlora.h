@@ -395,7 +395,8 @@ qlora_status mxfp4_dequantize(const qlora_mxfp4* w, void* W_out, qlora_dtype out
  *   H = Q(X) W^T + (alpha/r) (X A^T) B^T
  * Q(X) the MXFP4 value of X (as mxfp4_quantize), W the stored weight; the base product runs on
  * block-scaled 4-bit tensor cores (exact products, fp32 accumulation), the adapter term takes the
- * unquantized X and is added in the same accumulator with (alpha/r) X A^T rounded to bf16.
+ * unquantized X and is added in the same accumulator, (alpha/r) X A^T carried as two bf16 numbers
+ * (16 significant bits).
  * Any T >= 1, from single tokens up.  U_save as in qlora_linear_fwd.
  * [MF] "Intrinsic Dimensionality and Low-Rank Parameter Dynamics".
  * ws >= qlora_workspace_bytes(QLORA_OP_FWD_MXFP4, QLORA_BF16, T, d_out, d_in, r).
@@ -431,7 +432,7 @@ qlora_status qlora_act8_dequantize(const qlora_act8* a, int64_t T, int64_t d_in,
  *   dX = dH W + s (dH B) A,   dA = s (dH B)^T X~,   dB = s dH^T (X~ A^T),   s = alpha/r,
  * X~ = X or the checkpoint's values.  U_saved (nullable): the forward's U, used for X~ A^T.  dX
  * (nullable: skipped) in bf16; dA, dB fp32, with s (dH B) and a recomputed U carried to the tensor
- * cores as three bf16 numbers each (24 significant bits).  flags as in qlora_linear_bwd_ex, the
+ * cores as three bf16 numbers each (24 significant bits), two for dX.  flags as in qlora_linear_bwd_ex, the
  * two-phase form included (QLORA_BWD_DX_FROM_WS reads no activation, but one must be given).
  * [MF] "Gradient Dynamics and Backpropagation Mechanics".
  * ws >= qlora_workspace_bytes(QLORA_OP_BWD_MXFP4, QLORA_BF16, T, d_out, d_in, r): above 64 tokens the

@@ -140,12 +140,56 @@ __host__ __device__ __forceinline__ ActTriple act_triple(int r) {
     return t;
 }
 
+// The K steps of 64 by which a layer's product F C^T takes its adapter term: F[., r] is s U or s G and C[., r]
+// is B or A.  F comes as the first two terms of its triple: rounded to one bf16 number it would cost
+// 2^-8 of the adapter term, as much as the rounding of the result (errors of H and dX 2.15e-3 against the 1.66e-3
+// of that alone, Frobenius norm); two carry 16 bits.  C is exact.  Up to rank 64 a step holds 64 of the
+// 2 stride columns of F and all of C, and an MMA of 16 of F's columns takes those of C that belong to them:
+// up to rank 32 one step as with one term.  Above, a step holds half a term and half of C.
+struct ExtSteps {
+    int steps;
+    int n16;      // MMAs per term
+    int wide;     // rank above 64
+    // first of the columns of C that step e holds
+    __host__ __device__ __forceinline__ int c_col(int e) const { return wide ? (e & 1) * 64 : 0; }
+    // which 16 of them go with columns 16 k of F's tile; -1: no MMA
+    __host__ __device__ __forceinline__ int c16(int e, int k) const {
+        if (wide) return 4 * (e & 1) + k < n16 ? k : -1;
+        const int g = 4 * e + k;
+        return g < n16 ? g : g < 2 * n16 ? g - n16 : -1;
+    }
+};
+__host__ __device__ __forceinline__ ExtSteps ext_steps_of(int r) {
+    ExtSteps x;
+    x.n16 = (r + 15) / 16;
+    x.wide = r > 64;
+    x.steps = x.wide ? 4 : (2 * x.n16 + 3) / 4;
+    return x;
+}
+// F alone: [., ld], the two terms `stride` apart, columns past the rank up to 16 n16 of both 0.
+__host__ __device__ __forceinline__ int ext_ld(int r) { return (2 * act_triple(r).stride + 63) & ~63; }
+
+// Two bf16 terms of four values, the second of what the first leaves.  An infinite or NaN value is carried by
+// the first alone (inf - inf would make it NaN); so for a triple.
+__device__ __forceinline__ uint2 bf16_term(float (&x)[4]) {
+    uint2 w;
+    w.x = pack_bf16x2(x[0], x[1]);
+    w.y = pack_bf16x2(x[2], x[3]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const uint32_t h = e < 2 ? w.x : w.y;
+        const float rest = x[e] - __uint_as_float((e & 1) ? h & 0xFFFF0000u : h << 16);
+        x[e] = fabsf(rest) < __int_as_float(0x7F800000) ? rest : 0.f;
+    }
+    return w;
+}
+
 // What becomes of the sum D[M, N] of a product.
 enum : int {
     kActTriple = 0,   // scale D as three bf16 terms (ActTriple layout)
     kActCols = 1,     // fp32 out[j, m] = scale D[m, j]  (dA)
     kActRows = 2,     // fp32 out[m, j] = scale D[m, j]  (dB)
-    kActU = 3,        // bf16 out[m, j] = scale D[m, j] (row stride ld) and out2[m, j] = D[m, j] (nullable)
+    kActU = 3,        // scale D as two bf16 terms (row stride ext_ld) and bf16 out2[m, j] = D[m, j] (nullable)
     kActDx = 4        // bf16 out[j, m] = D[m, j]  (dX of few tokens)
 };
 
@@ -177,12 +221,11 @@ struct ActJob {
     const uint8_t* scales;   // E8M0 bytes (int8: row-major, MXFP4: tiled) or NF4's uint8 constants
     const float* c2;         // NF4's group constants
     int64_t ld_scales;       // scales per stored row (MXFP4: scale tiles)
-    int ext_steps;           // kActDx: the adapter's K steps of 64, taken by the last rank
+    ExtSteps ext;            // kActDx: the adapter's K steps, taken by the last rank
     int mode;                // kRoleAB: kActCols or kActRows
     float scale;
     int accumulate;          // kActCols, kActRows: add to out
     void* out;
-    int ld;
     __nv_bfloat16* out2;
     // Forward: A (bf16 [M, K]) is also quantized to MXFP4 on its way through shared memory (null: not)
     uint8_t *mx_codes, *mx_scales;
@@ -307,7 +350,7 @@ __global__ void __launch_bounds__(ActGemmSmem<RPT>::kThreads, 1)
     const int64_t units = (job.k_steps + unit - 1) / unit;
     const int k_begin = static_cast<int>(units * rank / C) * unit;
     const int n_main = min(job.k_steps, static_cast<int>(units * (rank + 1) / C) * unit) - k_begin;
-    const int n_iters = n_main + (ROLE == kRoleDx && rank == C - 1 ? job.ext_steps : 0);
+    const int n_iters = n_main + (ROLE == kRoleDx && rank == C - 1 ? job.ext.steps : 0);
     const ActTriple tr = act_triple(job.N);
     const bool triple = ROLE == kRoleAB && job.triple;
     const int terms = RPT == 64 && triple ? 3 : 1;             // column groups of an accumulator tile
@@ -396,11 +439,11 @@ __global__ void __launch_bounds__(ActGemmSmem<RPT>::kThreads, 1)
                         tma_load_2d(dst, tmB, &full[s], kx, 0);
                     }
                 } else {
-                    const int kx = (it - n_main) * 64;
+                    const int e = it - n_main, c = job.ext.c_col(e);
                     mbar_arrive_expect_tx(&full[s], L::kA + b_bytes);
-                    tma_load_2d(a, &tmA1, &full[s], m0, kx);
-                    tma_load_2d(a + 8192, &tmA1, &full[s], m0 + 64, kx);
-                    tma_load_2d(dst, &tmB1, &full[s], kx, 0);
+                    tma_load_2d(a, &tmA1, &full[s], m0, c);
+                    tma_load_2d(a + 8192, &tmA1, &full[s], m0 + 64, c);
+                    tma_load_2d(dst, &tmB1, &full[s], e * 64, 0);
                 }
             }
             __syncwarp();
@@ -431,7 +474,19 @@ __global__ void __launch_bounds__(ActGemmSmem<RPT>::kThreads, 1)
             const uint64_t ad = a_desc + static_cast<uint32_t>(s * (L::kA >> 4));
             const uint64_t bd = b_desc + static_cast<uint32_t>(s * (b_bytes >> 4));
             const bool last = in_seg + 1 == seg_len || it == n_iters - 1;
-            if (elect_one()) {
+            if (ROLE == kRoleDx && it >= n_main) {
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int c = job.ext.c16(it - n_main, k);
+                        if (c >= 0)
+                            umma_bf16_ss(d, ad + ((c * a_step) >> 4), bd + ((k * b_step) >> 4), idesc,
+                                         (in_seg > 0 || k > 0) ? 1u : 0u);
+                    }
+                    umma_commit(&empty[s]);
+                    if (last) umma_commit(&accf[acc_i]);
+                }
+            } else if (elect_one()) {
                 for (int b = 0; b < groups; ++b) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
@@ -687,7 +742,7 @@ __global__ void __launch_bounds__(ActGemmSmem<RPT>::kThreads, 1)
             }
         } else {
             // row by row, four columns per thread (the joining buffer's rows are 16-byte units)
-            const int n4 = mode == kActTriple ? tr.stride / 4 : (N + 3) / 4;
+            const int n4 = mode == kActTriple ? tr.stride / 4 : mode == kActU ? 4 * ((N + 15) / 16) : (N + 3) / 4;
             for (int rl = td / n4, g = td - rl * n4; rl < rows;) {
                 float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (4 * g < N)
@@ -703,28 +758,18 @@ __global__ void __launch_bounds__(ActGemmSmem<RPT>::kThreads, 1)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) x[e] *= scale;
 #pragma unroll
-                    for (int k = 0; k < 3; ++k) {
-                        uint2 w;
-                        w.x = pack_bf16x2(x[0], x[1]);
-                        w.y = pack_bf16x2(x[2], x[3]);
-                        *reinterpret_cast<uint2*>(out + k * tr.stride) = w;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            // an infinite or NaN value is carried by the first term alone (inf - inf would make
-                            // it NaN)
-                            const uint32_t h = e < 2 ? w.x : w.y;
-                            const float rest = x[e] - __uint_as_float((e & 1) ? h & 0xFFFF0000u : h << 16);
-                            x[e] = fabsf(rest) < __int_as_float(0x7F800000) ? rest : 0.f;
-                        }
-                    }
+                    for (int k = 0; k < 3; ++k) *reinterpret_cast<uint2*>(out + k * tr.stride) = bf16_term(x);
                 } else if (mode == kActU) {
-                    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(job.out) + row * job.ld + j;
+                    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(job.out) + row * ext_ld(N) + j;
+                    if (job.out2) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (e < left) {
-                            out[e] = __float2bfloat16_rn(scale * x[e]);
-                            if (job.out2) job.out2[row * N + j + e] = __float2bfloat16_rn(x[e]);
-                        }
+                        for (int e = 0; e < 4; ++e)
+                            if (e < left) job.out2[row * N + j + e] = __float2bfloat16_rn(x[e]);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[e] *= scale;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) *reinterpret_cast<uint2*>(out + k * tr.stride) = bf16_term(x);
                 } else {
                     float* out = static_cast<float*>(job.out) + row * N + j;
                     const bool add = job.accumulate != 0;

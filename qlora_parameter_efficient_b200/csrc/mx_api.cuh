@@ -105,7 +105,7 @@ MxFwdPlan mx_fwd_plan(int64_t T, int64_t d_out, int64_t d_in, int r) {
         p.codes = take(static_cast<size_t>(T) * d_in / 2);
         p.scales = take(mx_scale_bytes(T, d_in));
     }
-    p.us = take(static_cast<size_t>(T) * p.RP * 2);
+    p.us = take(static_cast<size_t>(T) * ext_ld(r) * 2);
     if (r % 8) p.b_pad = take(static_cast<size_t>(d_out) * pad8(r) * 2);
     if (mx_route(T) == kMxPair) {
         p.sched = pair_schedule(T, d_out, cdiv(d_in, 256), true);
@@ -177,7 +177,7 @@ qlora_status launch_mx_stream(const CUtensorMap& tw, const CUtensorMap& tx, cons
     // a ring of all of the shared memory where each CTA has an SM to itself, no longer than its K
     g.stages = L::kShared;
     if (tiles * g.ranks * tok <= kSmsForSplit)
-        g.stages = static_cast<int>(std::min<int64_t>(L::kAlone, std::max<int64_t>(L::kShared, cdiv(chunks, g.ranks) + g.ext_steps)));
+        g.stages = static_cast<int>(std::min<int64_t>(L::kAlone, std::max<int64_t>(L::kShared, cdiv(chunks, g.ranks) + g.ext.steps)));
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -223,7 +223,7 @@ qlora_status launch_act_gemm(ActLaunch& l, int* err, cudaStream_t st) {
     auto kern = k_act_gemm<RPT, ROLE>;
     static std::atomic<uint64_t> configured{0};
     QL_TRY(allow_smem(kern, L::kTotal, configured));
-    if (l.n == 1 && !l.g.job[0].ext_steps) {
+    if (l.n == 1 && !l.g.job[0].ext.steps) {
         l.a[1] = l.a[0];
         l.b[1] = l.b[0];
     }
@@ -320,12 +320,12 @@ qlora_status tmap_scales(CUtensorMap* m, const void* base, int64_t rows, int64_t
 
 // dX = dH W + (sG) A over the weight decoded to bf16 in the workspace.
 qlora_status dx_gemm(const void* W, const void* dH, int64_t dh_ld, int64_t T, int64_t d_out, int64_t d_in,
-                     const void* sG, const void* A, int RP, int r, void* dX, const PairSched& sch, void* pair_ws,
+                     const void* sG, const void* A, int r, void* dX, const PairSched& sch, void* pair_ws,
                      int* err, cudaStream_t st) {
     CUtensorMap t[6];
     QL_TRY(tmap_bf16(&t[0], dH, T, d_out, dh_ld, 128));
     QL_TRY(tmap_bf16(&t[1], W, d_out, d_in, d_in, 64));
-    QL_TRY(tmap_bf16(&t[4], sG, T, r, act_triple(r).ld, 128));
+    QL_TRY(tmap_bf16(&t[4], sG, T, 2 * act_triple(r).stride, act_triple(r).ld, 128));
     QL_TRY(tmap_bf16(&t[5], A, r, d_in, d_in, 64));
     t[2] = t[3] = t[0];
     PairGemmArgs g{};
@@ -333,8 +333,7 @@ qlora_status dx_gemm(const void* W, const void* dH, int64_t dh_ld, int64_t T, in
     g.N = static_cast<int>(d_in);
     g.k_steps = static_cast<int>(cdiv(d_out, 64));
     g.k_mma_last = static_cast<int>(cdiv(d_out - 64 * (g.k_steps - 1), 16));
-    g.ext_steps = RP / 64;
-    g.ext_k16_last = static_cast<int>(cdiv(r - 64 * (g.ext_steps - 1), 16));
+    g.ext = ext_steps_of(r);
     g.m_tiles = static_cast<int>(cdiv(T, 256));
     g.n_tiles = static_cast<int>(cdiv(d_in, sch.bn));
     g.out = static_cast<__nv_bfloat16*>(dX);
@@ -379,7 +378,6 @@ qlora_status mx_fwd(const qlora_mxfp4* w, const void* X, int64_t T, const void* 
         a.A = static_cast<const bf*>(A);
         a.T = static_cast<int>(T);
         a.r = r;
-        a.ld_us = RP;
         a.d_in = d_in;
         a.s = s;
         a.u_save = static_cast<bf*>(U_save);
@@ -394,7 +392,6 @@ qlora_status mx_fwd(const qlora_mxfp4* w, const void* X, int64_t T, const void* 
         ActJob& ju = l.add(T, r, d_in);
         ju.scale = s;
         ju.out = us;
-        ju.ld = RP;
         ju.out2 = static_cast<bf*>(U_save);
         const int64_t qx_tiles = cdiv(T, 128) * mx_col_tiles(d_in);
         if (cdiv(T, 128) > 5) {
@@ -422,15 +419,14 @@ qlora_status mx_fwd(const qlora_mxfp4* w, const void* X, int64_t T, const void* 
         QL_TRY(tmap_u8_sw128(&t[1], w->codes, d_out, d_in / 2, d_in / 2, 128));
         QL_TRY(tmap_scales(&t[2], scales, T, d_in));
         QL_TRY(tmap_scales(&t[3], w->scales, d_out, d_in));
-        QL_TRY(tmap_bf16(&t[4], us, T, r, RP, 128));
+        QL_TRY(tmap_bf16(&t[4], us, T, 2 * act_triple(r).stride, ext_ld(r), 128));
         QL_TRY(tmap_bf16(&t[5], b_src, d_out, r, b_ld, 128));
         PairGemmArgs g{};
         g.M = static_cast<int>(T);
         g.N = static_cast<int>(d_out);
         g.k_steps = static_cast<int>(cdiv(d_in, 256));
         g.k_mma_last = static_cast<int>(d_in / 64 - 4 * (g.k_steps - 1));
-        g.ext_steps = RP / 64;
-        g.ext_k16_last = static_cast<int>(cdiv(r - 64 * (g.ext_steps - 1), 16));
+        g.ext = ext_steps_of(r);
         g.m_tiles = static_cast<int>(cdiv(T, 256));
         g.n_tiles = static_cast<int>(cdiv(d_out, 256));
         g.a_sf_tiles = g.b_sf_tiles = static_cast<int>(mx_col_tiles(d_in));
@@ -444,14 +440,13 @@ qlora_status mx_fwd(const qlora_mxfp4* w, const void* X, int64_t T, const void* 
     if (route == kMxDecode) tx = tw;       // (X is quantized in the kernel)
     else QL_TRY(tmap_u8_sw128(&tx, codes, T, d_in / 2, d_in / 2, nt));
     QL_TRY(tmap_bf16(&tb, b_src, d_out, r, b_ld, 128));
-    QL_TRY(tmap_bf16(&tu, us, T, r, RP, nt));
+    QL_TRY(tmap_bf16(&tu, us, T, 2 * act_triple(r).stride, ext_ld(r), nt));
     MxStreamArgs g{};
     g.T = static_cast<int>(T);
     g.d_out = static_cast<int>(d_out);
     g.k64 = static_cast<int>(d_in / 64);
     g.col_tiles = static_cast<int>(mx_col_tiles(d_in));
-    g.ext_steps = RP / 64;
-    g.ext_k16_last = static_cast<int>(cdiv(r - 64 * (g.ext_steps - 1), 16));
+    g.ext = ext_steps_of(r);
     g.w_scales = w->scales;
     g.x_scales = scales;
     g.X = static_cast<const bf*>(X);
@@ -563,11 +558,11 @@ qlora_status mx_bwd(MxBase base, const void* X, const qlora_act8* X8, const void
         a.n_zero = p.sched.n_cnt;
         QL_TRY(prepare(a));
     }
-    // dX = dH W + (sG) A; the adapter term's s G is rounded to bf16 (2^-8 of that term, as dX itself is)
+    // dX = dH W + (sG) A, s G as the first two terms of its triple
     if (want_dx && T <= kDxFewT) {
         ActLaunch l;
         ActJob& j = l.add(d_in, static_cast<int>(T), d_out);
-        j.ext_steps = RP / 64;
+        j.ext = ext_steps_of(r);
         j.out = dX;
         if (base.mx) {
             j.op = kOpMxfp4;
@@ -582,10 +577,10 @@ qlora_status mx_bwd(MxBase base, const void* X, const qlora_act8* X8, const void
         QL_TRY(tmap_u8(&l.a[0], base.mx ? base.mx->codes : base.nf4->codes, d_out, d_in / 2, d_in / 2, 64, 64));
         QL_TRY(tmap_bf16(&l.b[0], dH, T, d_out, dh_ld, 64));
         QL_TRY(tmap_bf16(&l.a[1], A, r, d_in, d_in, 64));
-        QL_TRY(tmap_bf16(&l.b[1], g3, T, r, tr.ld, 64));
+        QL_TRY(tmap_bf16(&l.b[1], g3, T, 2 * tr.stride, tr.ld, 64));
         l.pdl = !first;
         QL_TRY((launch_act_gemm<64, kRoleDx>(l, err, st)));
-    } else if (want_dx) QL_TRY(dx_gemm(W, dH, dh_ld, T, d_out, d_in, g3, A, RP, r, dX, p.sched, at<void>(ws, p.pair), err, st));
+    } else if (want_dx) QL_TRY(dx_gemm(W, dH, dh_ld, T, d_out, d_in, g3, A, r, dX, p.sched, at<void>(ws, p.pair), err, st));
     if (grads) {
         // dA^T[d_in, r] = X~^T (s G) and dB[d_out, r] = s dH^T U
         ActLaunch l;

@@ -75,14 +75,14 @@ __device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t desc) {
 
 // The adapter side of a decode-size call (T <= 16), beside which the weight stream already runs.  CTAs
 // [0, r): one adapter row j each, U[:, j] = X A[j]^T in fp32, written unscaled to u_save (nullable,
-// [T, r]) and as bf16(s U) to us [T, ld_us]; the rest: B copied to padded rows (only where r is not a
-// multiple of 8).  s U in bf16 costs 2^-8 of the adapter term, as the rounding of H costs 2^-8 of H.
+// [T, r]) and s U as two bf16 terms to us [T, ext_ld(r)]; the rest: B copied to padded rows (only where r is
+// not a multiple of 8).
 // Bound by latency (out of HBM 4.9 us at one token of 4096, r = 16; 8.2 us at 13 tokens, r = 64), most
 // of it behind the stream.
 constexpr int kMxDecodeT = 16;
 struct MxPrepArgs {
     const __nv_bfloat16 *X, *A;
-    int T, r, ld_us;
+    int T, r;
     int64_t d_in;
     float s;
     __nv_bfloat16 *u_save, *us;
@@ -126,7 +126,14 @@ __global__ void __launch_bounds__(256) k_mx_prepare(const MxPrepArgs a) {
 #pragma unroll
         for (int w = 0; w < 8; ++w) u += s_red[w][t];
         if (a.u_save) a.u_save[t * a.r + j] = __float2bfloat16_rn(u);
-        a.us[t * a.ld_us + j] = __float2bfloat16_rn(a.s * u);
+        const int stride = act_triple(a.r).stride;
+        __nv_bfloat16* us = a.us + t * ext_ld(a.r) + j;
+        float x[4] = {a.s * u, 0.f, 0.f, 0.f};
+        const uint2 hi = bf16_term(x), lo = bf16_term(x);
+        us[0] = __ushort_as_bfloat16(static_cast<unsigned short>(hi.x));
+        us[stride] = __ushort_as_bfloat16(static_cast<unsigned short>(lo.x));
+        if (j == a.r - 1)
+            for (int c = 1; j + c < ((a.r + 15) & ~15); ++c) us[c] = us[stride + c] = __float2bfloat16_rn(0.f);
     }
 }
 
@@ -146,8 +153,7 @@ struct MxStreamArgs {
     int col_tiles;            // scale tiles per row of tiles (d_in / 128, rounded up)
     int ranks;                // CTAs per cluster, K split over them
     int stages;               // of the ring
-    int ext_steps;            // adapter K steps of 64, taken by the last rank
-    int ext_k16_last;
+    ExtSteps ext;             // the adapter's K steps, taken by the last rank
     const uint8_t* w_scales;
     const uint8_t* x_scales;  // MXFP4 X (NT > 16), or
     const __nv_bfloat16* X;   // X itself (NT = 16), quantized by the CTAs that use it
@@ -254,7 +260,7 @@ __global__ void __launch_bounds__(MxStreamCfg<NT>::kThreads)
     const int c_begin = static_cast<int>(static_cast<int64_t>(chunks) * rank / C);
     const int c_end = static_cast<int>(static_cast<int64_t>(chunks) * (rank + 1) / C);
     const int n_main = c_end - c_begin;
-    const int n_iters = n_main + (rank == C - 1 ? args.ext_steps : 0);
+    const int n_iters = n_main + (rank == C - 1 ? args.ext.steps : 0);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
@@ -323,10 +329,10 @@ __global__ void __launch_bounds__(MxStreamCfg<NT>::kThreads)
                     load_w(it, s);
                     load_x(it, s);
                 } else {
-                    const int kx = (it - n_main) * 64;
+                    const int e = it - n_main;
                     mbar_arrive_expect_tx(&full[s], L::kA + L::kB);
-                    tma_load_2d(sA + s * L::kA, &tmBx, &full[s], kx, n0);
-                    tma_load_2d(sB + s * L::kB, &tmUx, &full[s], kx, t0);
+                    tma_load_2d(sA + s * L::kA, &tmBx, &full[s], args.ext.c_col(e), n0);
+                    tma_load_2d(sB + s * L::kB, &tmUx, &full[s], e * 64, t0);
                 }
             }
             __syncwarp();
@@ -378,11 +384,12 @@ __global__ void __launch_bounds__(MxStreamCfg<NT>::kThreads)
                     umma_commit(&empty[s]);
                 }
             } else {
-                const int nk = it == n_iters - 1 ? args.ext_k16_last : 4;
                 if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (k < nk) umma_bf16_ss(tmem, ad + 2 * k, bd + 2 * k, idesc_x, (it > 0 || k > 0) ? 1u : 0u);
+                    for (int k = 0; k < 4; ++k) {
+                        const int c = args.ext.c16(it - n_main, k);
+                        if (c >= 0) umma_bf16_ss(tmem, ad + 2 * c, bd + 2 * k, idesc_x, (it > 0 || k > 0) ? 1u : 0u);
+                    }
                     umma_commit(&empty[s]);
                 }
             }
@@ -515,8 +522,7 @@ struct PairGemmArgs {
     int M, N;                 // output rows (tokens) and columns
     int k_steps;              // main stages: 256 MXFP4 or 64 bf16 elements of K
     int k_mma_last;           // MMAs of the last main stage (1..4)
-    int ext_steps;            // adapter K stages of 64
-    int ext_k16_last;
+    ExtSteps ext;             // the adapter's K stages
     int m_tiles, n_tiles;     // 256 x BN tiles
     int a_sf_tiles, b_sf_tiles;   // MXFP4: scale tiles per row of tiles (both operands share d_in)
     int split;                // ways the tail tiles are split along K (1: not)
@@ -628,7 +634,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGemmSmem<MX, BN>
     const uint32_t rank = cluster_ctarank();
     const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
     const int n_tiles_total = args.m_tiles * args.n_tiles;
-    const int iters_per_tile = args.k_steps + args.ext_steps;
+    const int iters_per_tile = args.k_steps + args.ext.steps;
     const int tail_base = n_tiles_total - args.tail_tiles;
     // this pair's units: whole tiles pair, pair + npairs, ... < tail_base, then at most one part of a
     // tail tile (part p: main stages [p k / split, (p + 1) k / split), the last part also the adapter's)
@@ -718,14 +724,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGemmSmem<MX, BN>
                             if (BN == 256) tma_load_2d_pair(b + 8192, &tmB, bar, n0 + 64, it * 64);
                         }
                     } else {
-                        const int kx = (it - args.k_steps) * 64;
+                        const int e = it - args.k_steps, c = args.ext.c_col(e);
                         if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * (L::kA + L::kB));
-                        tma_load_2d_pair(a, &tmAx, bar, kx, m0);
+                        tma_load_2d_pair(a, &tmAx, bar, e * 64, m0);
                         if (MX) {
-                            tma_load_2d_pair(b, &tmBx, bar, kx, n0);
+                            tma_load_2d_pair(b, &tmBx, bar, c, n0);
                         } else {
-                            tma_load_2d_pair(b, &tmBx, bar, n0, kx);
-                            if (BN == 256) tma_load_2d_pair(b + 8192, &tmBx, bar, n0 + 64, kx);
+                            tma_load_2d_pair(b, &tmBx, bar, n0, c);
+                            if (BN == 256) tma_load_2d_pair(b + 8192, &tmBx, bar, n0 + 64, c);
                         }
                     }
                 }
@@ -785,15 +791,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGemmSmem<MX, BN>
                                                     sfa + 4 * (k >> 1), sfb + 8 * (k >> 1), (!first || k > 0) ? 1u : 0u);
                             umma_commit_2sm_both(&empty[s]);
                         }
-                    } else {
-                        const int nk = it == iters_per_tile - 1 && it >= args.k_steps ? args.ext_k16_last
-                                       : it == args.k_steps - 1                       ? args.k_mma_last
-                                                                                      : 4;
+                    } else if (it < args.k_steps) {
+                        const int nk = it == args.k_steps - 1 ? args.k_mma_last : 4;
                         if (elect_one()) {
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
                                 if (k < nk)
                                     umma_bf16_ss_2sm(d, ad + 2 * k, bd + kBStep * k, idesc, (!first || k > 0) ? 1u : 0u);
+                            umma_commit_2sm_both(&empty[s]);
+                        }
+                    } else {
+                        if (elect_one()) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const int c = args.ext.c16(it - args.k_steps, k);
+                                if (c >= 0)
+                                    umma_bf16_ss_2sm(d, ad + 2 * k, bd + kBStep * c, idesc, (!first || k > 0) ? 1u : 0u);
+                            }
                             umma_commit_2sm_both(&empty[s]);
                         }
                     }
