@@ -625,6 +625,13 @@ def _need(name, t, dtype, shape, dev):
     raise ValueError(f"{name} must be contiguous")
 
 
+def _need_flat(name, t, dtype, n, dev):
+    """A buffer of at least n elements, whatever its shape."""
+    if t.numel() < n:
+        raise ValueError(f"{name} must have {n} elements, got {t.numel()}")
+    _need(name, t, dtype, t.shape, dev)
+
+
 def _need_cuda(name, t):
     dev = t.device
     if dev.type != "cuda":
@@ -939,9 +946,9 @@ def qlora_linear_bwd_act8(w: NF4Weight, X8: Act8, dH, A, B, alpha, U_saved=None,
             return got
     dev = _need_cuda("codes", w.codes)
     _need("codes", w.codes, torch.uint8, (w.d_out, w.d_in // 2), dev)
-    for name, t in (("absmax_q", w.absmax_q), ("c2", w.c2)):
-        if t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    blocks = w.d_out * w.d_in // 64
+    _need_flat("absmax_q", w.absmax_q, torch.uint8, blocks, dev)
+    _need_flat("c2", w.c2, torch.float32, -(-blocks // 256), dev)
     return _bwd_act("qlora_linear_bwd_act8", OP_BWD_ACT8, w, dev, X8, dH, A, B, alpha, U_saved, dX, dA, dB, ws,
                     want_dx, accumulate, phase, stream)
 
