@@ -693,19 +693,17 @@ def _made(cls, **fields):
 @dataclass(frozen=True)
 class MXFP4Weight:
     """Device buffers of an MXFP4 matrix: packed E2M1 codes and the tiled E8M0 scales (checked when
-    the handle is made)."""
+    the handle is made and when it is used)."""
     codes: object      # uint8 [d_out, d_in/2]
     scales: object     # uint8 [512 * ceil(d_out/128) * ceil(d_in/128)]
     d_out: int
     d_in: int
 
     def _c(self):
-        """The C struct, by reference (built once: the handle keeps its buffers)."""
-        ref = self.__dict__.get("_ref")
-        if ref is None:
-            ref = ctypes.byref(_MXFP4(self.codes.data_ptr(), self.scales.data_ptr(), self.d_out, self.d_in))
-            self.__dict__["_ref"] = ref
-        return ref
+        """The C struct, by reference, of the buffers as they are now (a tensor may have been given other memory
+        since)."""
+        self.__post_init__()
+        return ctypes.byref(_MXFP4(self.codes.data_ptr(), self.scales.data_ptr(), self.d_out, self.d_in))
 
     def __post_init__(self):
         torch = _torch()
@@ -718,11 +716,12 @@ class MXFP4Weight:
 @dataclass(frozen=True)
 class Act8:
     """8-bit checkpoint of an activation [T, d_in]: int8 values and one E8M0 scale per 32 of them
-    (checked when the handle is made)."""
+    (checked when the handle is made and when it is used)."""
     q: object          # int8 [T, d_in]
     scales: object     # uint8 [T, d_in/32]
 
     def _c(self):
+        self.__post_init__()
         return _ACT8(self.q.data_ptr(), self.scales.data_ptr())
 
     def __post_init__(self):

@@ -65,3 +65,48 @@ def test_malformed_nf4_handles_on_the_gpu(monkeypatch, binding):
         for a, b in zip(call("cuda", {**ok, **kw}), ref):
             assert torch.equal(a, b)
     assert np.isfinite(ref[0].float().cpu().numpy()).all() and q.get_device_error() == 0
+
+
+def test_a_handle_keeps_no_addresses(monkeypatch):
+    """What a call passes on are the buffers as they are then, checked; a used handle can be copied."""
+    import copy
+
+    import torch
+    monkeypatch.setattr(q, "_need_cuda", lambda name, t: t.device)
+    u8 = torch.uint8
+    w = q.MXFP4Weight(torch.zeros((8, 32), dtype=u8), torch.zeros(512, dtype=u8), 8, 64)
+    a = q.Act8(torch.zeros((4, 64), dtype=torch.int8), torch.zeros((4, 2), dtype=u8))
+    assert w._c()._obj.codes == w.codes.data_ptr() and a._c().q == a.q.data_ptr()
+    for t in (w.codes, w.scales, a.q, a.scales):
+        t.data = torch.ones_like(t)                   # other memory (the old one is freed)
+    c, c8 = w._c()._obj, a._c()
+    assert (c.codes, c.scales) == (w.codes.data_ptr(), w.scales.data_ptr())
+    assert (c8.q, c8.scales) == (a.q.data_ptr(), a.scales.data_ptr())
+    for h, name in ((w, "codes"), (a, "q")):
+        d = copy.deepcopy(h)
+        assert getattr(d, name).data_ptr() != getattr(h, name).data_ptr()
+        d._c()
+    w.scales.data = torch.zeros(512, dtype=u8)[:256]
+    with pytest.raises(ValueError):
+        w._c()
+    a.scales.data = torch.zeros((3, 2), dtype=u8)
+    with pytest.raises(ValueError):
+        a._c()
+
+
+@pytest.mark.gpu
+def test_a_weight_that_was_given_other_memory():
+    """The same handle before and after its buffers moved, by either way into the library."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(1)
+    W, X = torch.randn(96, 128, generator=g, device="cuda"), torch.randn(20, 128, generator=g, device="cuda").bfloat16()
+    A, B = torch.randn(4, 128, generator=g, device="cuda").bfloat16(), torch.randn(96, 4, generator=g, device="cuda").bfloat16()
+    w, s = q.mxfp4_quantize(W), torch.cuda.current_stream()
+    H = q.qlora_linear_fwd_mxfp4(w, X, A, B, 8.0, stream=s)[0]
+    for t in (w.codes, w.scales):
+        old = t.data
+        t.data = old.clone()
+        old.fill_(0x55)
+    for kw in (dict(), dict(stream=s)):
+        assert torch.equal(q.qlora_linear_fwd_mxfp4(w, X, A, B, 8.0, **kw)[0], H)
+        assert torch.equal(q.mxfp4_dequantize(w, torch.float32, **kw), q.mxfp4_dequantize(q.mxfp4_quantize(W), torch.float32))
