@@ -151,21 +151,37 @@ _bind_looked_for = False
 
 
 def _mx_bind_path():
-    return os.path.join(HERE, "_mx_bind.so")
+    """The compiled module for this Python and this torch, whose C++ interface it uses: one that was built for
+    others has another name."""
+    import sysconfig
+    torch = _torch()
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    return os.path.join(HERE, f"_mx_bind-{sysconfig.get_config_var('SOABI')}-torch{torch.__version__}-cxx11abi{abi}.so")
 
 
 def _load_binding(L):
     global _bind, _bind_looked_for
-    if not os.path.exists(_mx_bind_path()):
-        _bind_looked_for = True
+    _bind_looked_for = True
+    path, name = _mx_bind_path(), __name__ + "._mx_bind"
+    if not os.path.exists(path):
         return                                   # not built: the same calls go through ctypes
-    _torch()
-    from . import _mx_bind
-    _mx_bind.init(*(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in (
+    import importlib.util
+    import sys
+    module = sys.modules.get(name)
+    if module is None or module.__file__ != path:
+        spec = importlib.util.spec_from_file_location(name, path)
+        try:
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+        except ImportError as e:
+            import warnings
+            warnings.warn(f"{path} cannot be loaded ({e}): the microscaled calls go through ctypes", RuntimeWarning)
+            return
+        sys.modules[name] = module
+    module.init(*(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in (
         "qlora_workspace_bytes", "mxfp4_quantize", "mxfp4_dequantize", "qlora_act8_quantize",
         "qlora_act8_dequantize", "qlora_linear_fwd_mxfp4", "qlora_linear_bwd_mxfp4", "qlora_linear_bwd_act8")))
-    _bind = _mx_bind
-    _bind_looked_for = True
+    _bind = module
 
 
 def _binding():

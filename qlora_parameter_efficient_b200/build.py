@@ -1,7 +1,10 @@
 """Builds libqlora.so in-tree with nvcc for sm_100a (B200).
 
-    python -m qlora_parameter_efficient_b200.build            # release: libqlora.so, _mx_bind.so
+    python -m qlora_parameter_efficient_b200.build            # release: libqlora.so, _mx_bind-*.so
     python -m qlora_parameter_efficient_b200.build --debug    # libqlora_debug.so, QLORA_DEBUG=1
+
+libqlora.so needs the CUDA toolkit alone.  _mx_bind-*.so, the short way from Python into the microscaled
+calls, is built where torch and its headers are found; without it the same calls go through ctypes.
 
 The debug library checks the kernels' index invariants on the device (a failed check is
 reported as QLORA_ERR_DEVICE by qlora_get_device_error); load it with QLORA_LIB=<path>.
@@ -18,7 +21,6 @@ LIB = os.path.join(HERE, "libqlora.so")
 DEBUG_LIB = os.path.join(HERE, "libqlora_debug.so")
 SOURCES = ["qlora_api.cu", "noalloc.cu"]
 DEPS = sorted(f for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh")))
-BINDING = os.path.join(HERE, "_mx_bind.so")      # the short Python way into the microscaled calls
 BINDING_SOURCE = os.path.join(CSRC, "mx_bind.cpp")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "qlora.h")
 
@@ -60,31 +62,40 @@ def build_library(force: bool = False, verbose: bool = False, debug: bool = Fals
     return lib
 
 
-def build_binding(force: bool = False, verbose: bool = False) -> str:
-    """The CPython module csrc/mx_bind.cpp (host code only: g++ against torch's headers)."""
-    if not force and os.path.exists(BINDING) and all(
-            os.path.getmtime(d) <= os.path.getmtime(BINDING) for d in (BINDING_SOURCE, HEADER)):
-        return BINDING
-    import sysconfig
-
-    import torch
+def build_binding(force: bool = False, verbose: bool = False) -> str | None:
+    """The CPython module csrc/mx_bind.cpp (host code only: g++ against torch's headers), for the torch and the
+    Python that run this.  None, with a line that says so, where there is no torch to build it against."""
+    try:
+        import torch
+    except ImportError:
+        print("no torch: the Python binding of the microscaled calls is not built", flush=True)
+        return None
     root = os.path.dirname(torch.__file__)
+    if not os.path.exists(os.path.join(root, "include", "torch", "csrc", "autograd", "python_variable.h")):
+        print(f"no headers in {root}: the Python binding of the microscaled calls is not built", flush=True)
+        return None
+    from . import _mx_bind_path
+    binding = _mx_bind_path()
+    if not force and os.path.exists(binding) and all(
+            os.path.getmtime(d) <= os.path.getmtime(binding) for d in (BINDING_SOURCE, HEADER)):
+        return binding
+    import sysconfig
     cuda = os.path.dirname(os.path.dirname(nvcc())) or "/usr/local/cuda"
     includes = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
                 os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
     libs = os.path.join(root, "lib")
     cmd = [os.environ.get("CXX", "g++"), "-std=c++17", "-O2", "-shared", "-fPIC", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[f"-I{i}" for i in includes],
-           "-o", BINDING + ".tmp", BINDING_SOURCE, f"-L{libs}", "-lc10", "-lc10_cuda", "-ltorch_cpu",
+           "-o", binding + ".tmp", BINDING_SOURCE, f"-L{libs}", "-lc10", "-lc10_cuda", "-ltorch_cpu",
            "-ltorch_python"]
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         sys.stderr.write(res.stdout + res.stderr)
-        raise RuntimeError("g++ failed building _mx_bind.so")
-    os.replace(BINDING + ".tmp", BINDING)
-    return BINDING
+        raise RuntimeError("g++ failed building the binding")
+    os.replace(binding + ".tmp", binding)
+    return binding
 
 
 if __name__ == "__main__":
