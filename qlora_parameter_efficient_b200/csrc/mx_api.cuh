@@ -42,42 +42,6 @@ MxRoute mx_route(int64_t T) {
     return T <= kMxStreamMaxT ? kMxStream128 : kMxPair;
 }
 
-// Schedule of k_pair_gemm: pairs of SMs, tiles of 256 x 256 or (bf16) 256 x 128, and how many ways the tiles
-// of an incomplete last wave are split along K: the shortest by the measured costs in microseconds.  A bf16
-// stage takes 0.27 on a 256-wide tile and 0.2 on a 128-wide one, joining two parts 7 (4) and each further
-// part 1.  An MXFP4 tile is done in 5 to 20 us and is never split (4096^3: 49.9 us whole, 56.5 us with
-// its last wave split in two).
-struct PairSched {
-    int bn = 256, pairs = 1, tail = 0, split = 1;
-    size_t part_bytes = 0;
-    int n_cnt = 0;
-    size_t bytes() const { return part_bytes + align256(static_cast<size_t>(n_cnt) * sizeof(int)); }
-};
-PairSched pair_schedule(int64_t M, int64_t N, int64_t k_steps, bool mx) {
-    PairSched g;
-    const int64_t slots = kSmsForSplit / 2;
-    double best = 0;
-    for (int bn = 256; bn >= (mx ? 256 : 128); bn -= 128) {
-        const int64_t tiles = cdiv(M, 256) * cdiv(N, bn), whole = tiles / slots, rem = tiles % slots;
-        const double step = bn == 256 ? 0.27 : 0.2, join = bn == 256 ? 5 : 2;
-        for (int c = 1; c <= (rem && !mx ? kPairMaxSplit : 1); ++c) {
-            if (c > 1 && (c * rem > slots || c > k_steps)) break;
-            const double t = step * static_cast<double>(k_steps * whole + (rem ? cdiv(k_steps, c) : 0)) + (c > 1 ? join + c : 0);
-            if (best > 0 && t >= best) continue;
-            best = t;
-            g.bn = bn;
-            g.split = c;
-            g.tail = c > 1 ? static_cast<int>(rem) : 0;
-            g.pairs = static_cast<int>(whole ? slots : rem * c);
-        }
-    }
-    if (g.split > 1) {
-        g.part_bytes = static_cast<size_t>(g.tail) * 8 * g.split * (g.bn * 8) * 16;
-        g.n_cnt = g.tail * 8;
-    }
-    return g;
-}
-
 // Ranks of a weight-stream cluster: as many of 4, 2, 1 as K has stages for and `slots` can take at once,
 // two CTAs per SM at T <= 16 (whose rings are small), one above.  8 ranks of half the length measured 8.4
 // against 7.7 us at one token of a 4096 x 4096 layer, the same at 64 tokens of it.
@@ -108,7 +72,7 @@ MxFwdPlan mx_fwd_plan(int64_t T, int64_t d_out, int64_t d_in, int r) {
     p.us = take(static_cast<size_t>(T) * ext_ld(r) * 2);
     if (r % 8) p.b_pad = take(static_cast<size_t>(d_out) * pad8(r) * 2);
     if (mx_route(T) == kMxPair) {
-        p.sched = pair_schedule(T, d_out, cdiv(d_in, 256), true);
+        p.sched = pair_schedule(T, d_out, cdiv(d_in, 256), true, kSmsForSplit / 2);
     }
     p.total = off;
     return p;
@@ -136,7 +100,7 @@ MxBwdPlan mx_bwd_plan(int64_t T, int64_t d_out, int64_t d_in, int r) {
     p.g3 = take(triple);
     if (T > kDxFewT) {
         p.w = take(static_cast<size_t>(d_out) * d_in * 2);  // the decoded weight
-        p.sched = pair_schedule(T, d_in, cdiv(d_out, 64), false);
+        p.sched = pair_schedule(T, d_in, cdiv(d_out, 64), false, kSmsForSplit / 2);
         p.pair = take(p.sched.bytes());
     }
     p.total = off;

@@ -21,6 +21,7 @@
 #include "common.cuh"
 #include "mxfp4.cuh"
 #include "nf4_gemm2.cuh"
+#include "pair_schedule.cuh"
 
 namespace qlora {
 
@@ -573,7 +574,6 @@ __device__ __forceinline__ void warp_transpose(uint32_t (&r)[32], int lane) {
 }
 
 // BN: columns of a tile, 256, or for bf16 also 128.
-constexpr int kPairMaxSplit = 4;
 template <bool MX, int BN>
 struct PairGemmSmem {
     static constexpr int kA = 128 * 128;               // this CTA's A half: 128 rows of 128 bytes
