@@ -73,3 +73,55 @@ def test_columns_past_the_rank_are_not_read(q):  # noqa: F811
             for a, b in zip(*outs):
                 assert torch.isfinite(a).all() and torch.equal(a, b), (T, r)
     assert q.get_device_error() == 0
+
+
+# ------------------------------------------------------------------ gradients: three bf16 terms
+
+
+def bf16(x):
+    import torch
+    return torch.from_numpy(np.ascontiguousarray(x, np.float64)).to(torch.bfloat16).double().numpy()
+
+
+def terms(x, n):
+    """The first n bf16 terms of fp32 values, summed."""
+    got = np.zeros_like(x)
+    for _ in range(n):
+        got = got + bf16(x - got)
+    return got
+
+
+@pytest.mark.parametrize("ckpt", [True, False])
+@pytest.mark.parametrize("T,d_out", [(1, 3), (1, 8), (2, 3), (2, 5)])
+@pytest.mark.parametrize("r", [1, 8, 16, 20, 48, 64, 65, 128])
+def test_gradients_carry_24_bits(q, r, T, d_out, ckpt):  # noqa: F811
+    """Sums so short that what carries s G and a recomputed U is the largest error: bounds that its third term is
+    needed for (without it, in the oracle, they do not hold)."""
+    d_in, used = 128, [3, 40, 77, 126]                 # (products with 0 add no error)
+    W, A, B, X, dH = make(1000 * r + T, T, d_out, d_in, r)
+    keep = np.zeros(d_in)
+    keep[used] = 1
+    X = X * keep
+    w, _ = mx_weight(q, W)
+    alpha = np.float32(r / 3)
+    s = float(alpha / np.float32(r))                   # as the library forms it: 24 bits, unlike the products' 16
+    act = bf(X)
+    if ckpt:
+        act = q.act8_quantize(act)
+        X = M.act8_values(*M.act8_quantize(X))
+    _, dA, dB = q.qlora_linear_bwd_mxfp4(w, act, bf(dH), bf(A), bf(B), float(alpha))
+    _, dAr, dBr = M.layer_backward(W * 0.0, X, dH, A, B, s)
+    sG, U = s * (dH @ B), X @ A.T
+    # s G: d_out products summed, scaled; three terms leave 2^-24; T products, two sums of terms
+    e_sG = s * d_out * U32 * (np.abs(dH) @ np.abs(B)) + (2.0 ** -24 + 2.0 ** -24) * np.abs(sG)
+    e_U = len(used) * U32 * (np.abs(X) @ np.abs(A).T) + 2.0 ** -24 * np.abs(U)
+    sums = (T + 3) * U32 * BOTH
+    tol_A = e_sG.T @ np.abs(X) + sums * np.abs(sG).T @ np.abs(X)
+    tol_B = s * (np.abs(dH).T @ e_U + (sums + 2.0 ** -23) * np.abs(dH).T @ np.abs(U))
+    within(f64(dA), dAr, (1 + U16) * tol_A + 1e-30, "dA")
+    within(f64(dB), dBr, (1 + U16) * tol_B + 1e-30, "dB")
+    # two terms: beyond the bounds somewhere
+    two_A = terms(sG, 2).T @ X
+    two_B = s * dH.T @ terms(U, 2)
+    if r >= 8:
+        assert (np.abs(two_A - dAr) > tol_A).any() and (np.abs(two_B - dBr) > tol_B).any()
