@@ -152,7 +152,7 @@ struct MxStreamArgs {
     int T, d_out;
     int k64;                  // d_in / 64: MMAs of the whole contraction
     int col_tiles;            // scale tiles per row of tiles (d_in / 128, rounded up)
-    int ranks;                // CTAs per cluster, K split over them
+    int ranks;                // CTAs per cluster (1, 2 or 4), K split over them
     int stages;               // of the ring
     ExtSteps ext;             // the adapter's K steps, taken by the last rank
     const uint8_t* w_scales;
@@ -494,8 +494,7 @@ __global__ void __launch_bounds__(MxStreamCfg<NT>::kThreads)
         griddep_wait();
         if (!*abort) {
             if (C == 2) mx_join<2, NT, L::kThreads>(red, t_end, n0 + 64 * rank, t0, args);
-            else if (C == 4) mx_join<4, NT, L::kThreads>(red, t_end, n0 + 32 * rank, t0, args);
-            else mx_join<8, NT, L::kThreads>(red, t_end, n0 + 16 * rank, t0, args);
+            else mx_join<4, NT, L::kThreads>(red, t_end, n0 + 32 * rank, t0, args);
         }
     }
     tc_fence_before();
