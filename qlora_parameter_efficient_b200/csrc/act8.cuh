@@ -563,6 +563,7 @@ __global__ void __launch_bounds__(ActGemmSmem<RPT>::kThreads, 1)
             auto fetch = [&](int it, uint32_t& ev, float& cv) {
                 if (it >= lim) return;
                 const int64_t wrow = k0 + it * 64 + row;
+                if (!dcheck(wrow < job.K && mblk * 32 < job.M, args.err)) return;
                 if (op == kOpMxfp4) {
                     ev = __ldg(sc + mx_scale_offset(wrow, mblk, ld));
                 } else {
@@ -620,7 +621,10 @@ __global__ void __launch_bounds__(ActGemmSmem<RPT>::kThreads, 1)
             const uint8_t* sc = job.scales + (amn ? (k0 + row) * ld + m0 / 32 : (m0 + row) * ld + k0 / 32) + blk_in;
             const bool there = amn ? m0 / 32 + blk_in < ld : m0 + row < job.M;
             const int lim = !there ? 0 : min(static_cast<int64_t>(n_iters), amn ? (job.K - k0 - row + 63) / 64 : n_iters);
-            auto scale_at = [&](int it) -> uint32_t { return it < lim ? __ldg(sc + it * step) : 0u; };
+            const int64_t n_scales = (amn ? job.K : job.M) * ld;
+            auto scale_at = [&](int it) -> uint32_t {
+                return it < lim && dcheck(sc + it * step < job.scales + n_scales, args.err) ? __ldg(sc + it * step) : 0u;
+            };
             const int dst_off = amn ? (blk_in >> 1) * 8192 + row * 128 : row * 128;
             const int c0 = amn ? (blk_in & 1) * 4 : blk_in * 4, sw = row & 7;
             // the scales of this group's next pair are in flight while it decodes (a load takes longer than
@@ -678,14 +682,15 @@ __global__ void __launch_bounds__(ActGemmSmem<RPT>::kThreads, 1)
                     if (lane == 0) mbar_arrive(&empty[s]);       // the tile has been read
                     uint32_t e, v[4];
                     mxfp4_block32(raw, e, v);
-                    if (in)
+                    if (in && dcheck(static_cast<int64_t>(k_begin + it0 + u) * 64 + b * 32 < job.K, args.err))
                         *reinterpret_cast<uint4*>(codes + static_cast<int64_t>(k_begin + it0 + u) * 32) =
                             make_uint4(v[0], v[1], v[2], v[3]);
                     e |= __shfl_xor_sync(0xffffffffu, e, 1) << 8;        // (of the even lane: both blocks' bytes)
                     e_word |= e << (16 * u);
                     at.skip(1);
                 }
-                if (ok && in && b == 0) *reinterpret_cast<uint32_t*>(word + (it0 >> 1) * kMxTileBytes) = e_word;
+                if (ok && in && b == 0 && dcheck(static_cast<int64_t>(k_begin + it0) * 64 < job.K, args.err))
+                    *reinterpret_cast<uint32_t*>(word + (it0 >> 1) * kMxTileBytes) = e_word;
                 at.skip(kRingRun * (L::kGroups - 1));
                 if (drains) drain_behind(it0);
             }
@@ -736,6 +741,7 @@ __global__ void __launch_bounds__(ActGemmSmem<RPT>::kThreads, 1)
                 const int j = i >> sh, rl = i & (R - 1);
                 if (rl >= rows) continue;
                 const int64_t at = static_cast<int64_t>(j) * job.M + row0 + rl;
+                if (!dcheck(j < N && row0 + rl < job.M, args.err)) continue;
                 const float v = total(rl, j);
                 if (mode == kActDx) static_cast<__nv_bfloat16*>(job.out)[at] = __float2bfloat16_rn(v);
                 else static_cast<float*>(job.out)[at] = add ? static_cast<float*>(job.out)[at] + scale * v : scale * v;
@@ -751,6 +757,7 @@ __global__ void __launch_bounds__(ActGemmSmem<RPT>::kThreads, 1)
                         v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
                     }
                 const int64_t row = row0 + rl;
+                if (!dcheck(row < job.M && g < n4, args.err)) break;
                 const int j = 4 * g, left = N - j;           // columns of this group that exist
                 float x[4] = {v.x, left > 1 ? v.y : 0.f, left > 2 ? v.z : 0.f, left > 3 ? v.w : 0.f};
                 if (mode == kActTriple) {

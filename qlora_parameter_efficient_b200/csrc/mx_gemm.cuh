@@ -288,6 +288,11 @@ __global__ void __launch_bounds__(MxStreamCfg<NT>::kThreads)
 
     // MMAs (K = 64) and scale tiles of main stage `it`
     auto mmas_of = [&](int it) { return min(4, args.k64 - (c_begin + it) * 4); };
+    // bytes of the scale tiles of stage `c` from row tile `rt` of `rows` rows on
+    auto scales_at = [&](int rt, int c, uint32_t bytes, int rows) {
+        const int64_t at = (static_cast<int64_t>(rt) * args.col_tiles + 2 * c) * kMxTileBytes;
+        return dcheck(at + bytes <= static_cast<int64_t>((rows + 127) / 128) * args.col_tiles * kMxTileBytes, args.err) ? at : 0;
+    };
 
     if (warp == 0) {
         auto load_w = [&](int it, int s) {
@@ -295,17 +300,14 @@ __global__ void __launch_bounds__(MxStreamCfg<NT>::kThreads)
             const uint32_t sf = static_cast<uint32_t>((mmas_of(it) + 1) / 2) * kMxTileBytes;
             mbar_arrive_expect_tx(&full[s], L::kQuant ? L::kA + sf : L::kA + L::kB + 2 * sf);
             tma_load_2d(sA + s * L::kA, &tmW, &full[s], c * 128, n0);
-            bulk_load(sSa + s * L::kSf,
-                      args.w_scales + (static_cast<int64_t>(tile) * args.col_tiles + 2 * c) * kMxTileBytes, sf, &full[s]);
+            bulk_load(sSa + s * L::kSf, args.w_scales + scales_at(tile, c, sf, args.d_out), sf, &full[s]);
         };
         auto load_x = [&](int it, int s) {
             if (L::kQuant) return;
             const int c = c_begin + it;
             const uint32_t sf = static_cast<uint32_t>((mmas_of(it) + 1) / 2) * kMxTileBytes;
             tma_load_2d(sB + s * L::kB, &tmX, &full[s], c * 128, t0);
-            bulk_load(sSb + s * L::kSf,
-                      args.x_scales + (static_cast<int64_t>(t0 >> 7) * args.col_tiles + 2 * c) * kMxTileBytes, sf,
-                      &full[s]);
+            bulk_load(sSb + s * L::kSf, args.x_scales + scales_at(t0 >> 7, c, sf, args.T), sf, &full[s]);
         };
         const int ahead = min(S, n_main);
         if (elect_one())
@@ -847,7 +849,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGemmSmem<MX, BN>
                     uint32_t r[32];
                     tmem_ld_32x32b_x32(tbase + c * 32, r);
                     tmem_ld_wait();
-                    if (grow < args.M) {
+                    if (grow < args.M && dcheck(part_tile < args.tail_tiles && part < args.split, args.err)) {
 #pragma unroll
                         for (int g = 0; g < 8; ++g)
                             mine[g2_part_idx(c, g, lane)] =
