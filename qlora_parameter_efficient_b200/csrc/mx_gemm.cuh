@@ -520,6 +520,9 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* m
         : "memory");
 }
 
+// Limit, after a wait has run out, of that for the copies still in flight (ns).
+constexpr uint64_t kLandNs = 1000000;
+
 struct PairGemmArgs {
     int M, N;                 // output rows (tokens) and columns
     int k_steps;              // main stages: 256 MXFP4 or 64 bf16 elements of K
@@ -694,7 +697,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGemmSmem<MX, BN>
 
     if (warp == 0) {
         const uint32_t full_leader = mapa_shared(smem_u32(&full[0]), 0);
-        int s = 0, ph = 0;
+        int s = 0, ph = 0, issued = 0;
         bool ok = true;
         for (int u = 0; ok && u < n_units; ++u) {
             int tile, k0, k1;
@@ -737,10 +740,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGemmSmem<MX, BN>
                     }
                 }
                 __syncwarp();
+                ++issued;
                 if (++s == S) s = 0, ph ^= 1;
             }
         }
         if (!ok) fail();
+        // given up: the copies in flight land before the teardown lets shared memory go.  They complete on
+        // the leader's barriers, its peer's too; a stage whose other half was never issued ends the wait by its
+        // limit, far above what a copy takes
+        if (rank == 0 && *abort)
+            for (int it = max(0, issued - S); it < issued; ++it) mbar_wait(&full[it % S], (it / S) & 1, nullptr, kLandNs);
     } else if (warp == 1) {
         if (rank == 0) {
             const uint32_t idesc = make_idesc_bf16(256, BN, false, !MX);
@@ -974,7 +983,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGemmSmem<MX, BN>
     }
 
     __syncwarp();
-    if (*abort) __nanosleep(100000);   // copies in flight land before shared memory is released
+    if (*abort) __nanosleep(100000);   // (copies of a peer that ran ahead of the leader)
     tc_fence_before();
     cluster_barrier();
     if (warp == 1) {
