@@ -277,11 +277,11 @@ struct ActGemmSmem {
     static constexpr int kLdRed = RPT + 4;                      // floats per row of the joining buffer
     static_assert(kTotal <= 232448 && 128 * kLdRed * 4 <= kRing, "shared memory budget");
     static_assert(3 * (kA + kRaw + 3 * RPT / 64 * kChunk) <= kRing, "three stages at least");
-    static_assert(ring_min_stages(kGroups) <= 3, "stages that the groups can share");
+    static_assert(kGroups <= 3, "no more groups than stages (ring_landed)");
 };
 
 // Warp 0: TMA; warp 1: MMA; warps 2..9 and, up to rank 64, 10..17: int8 decode or MXFP4 quantization, one
-// 32-element block per thread and stage, the groups taking pairs of stages in turn (one group alone is
+// 32-element block per thread and stage, the groups taking stages in turn (one group alone is
 // bound by the latency of its own chain, 1100 cycles a stage); warps 2..9 also drain the accumulators.
 // A cluster's ranks split K; their sums meet in shared memory, each rank adding and writing 128 / ranks
 // rows in rank order, so no partial goes through memory.  Up to two products share a launch (U and G; dA
@@ -537,8 +537,8 @@ __global__ void __launch_bounds__(ActGemmSmem<RPT>::kThreads, 1)
             if (lane == 0) mbar_arrive(&acc_free[acc_i]);
             if (++acc_i == NA) acc_i = 0, acc_ph ^= 1;
         };
-        // pairs of stages in turn
-        RingPos at(S, kRingRun * group);
+        // every kGroups-th stage, two per turn of the loop
+        RingPos at(S, group);
         auto landed = [&]() {
             return ring_landed<L::kGroups>(
                 at, [&](int i, int par) { return mbar_wait_warp(&empty[i], par, abort, args.wait_ns); },
@@ -574,18 +574,19 @@ __global__ void __launch_bounds__(ActGemmSmem<RPT>::kThreads, 1)
             };
             const int dst_off = (blk_in >> 1) * 8192 + row * 128, c0 = (blk_in & 1) * 4;
 #pragma unroll
-            for (int u = 0; u < 2; ++u) fetch(2 * group + u, e[u], c2[u]);
-            for (int it0 = 2 * group; ok && it0 < n_iters; it0 += 2 * L::kGroups) {
+            for (int u = 0; u < 2; ++u) fetch(group + u * L::kGroups, e[u], c2[u]);
+            for (int it0 = group; ok && it0 < n_iters; it0 += 2 * L::kGroups) {
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    if (!ok || it0 + u >= n_iters) break;
+                    const int it = it0 + u * L::kGroups;
+                    if (!ok || it >= n_iters) break;
                     const uint32_t ev = e[u];
                     const float cv = c2[u];
-                    fetch(it0 + u + 2 * L::kGroups, e[u], c2[u]);
+                    fetch(it + 2 * L::kGroups, e[u], c2[u]);
                     ok = landed();
                     if (!ok) break;
                     const int s = at.s;
-                    if (it0 + u < n_main) {
+                    if (it < n_main) {
                         // (codes outside the weight are 0: the value 0 in MXFP4; NF4's is not, but meets only
                         // rows of dH that are 0 or columns past d_in)
                         const uint4 q = *reinterpret_cast<const uint4*>(sR + s * raw_bytes + row * 64 + blk_in * 16);
@@ -606,9 +607,8 @@ __global__ void __launch_bounds__(ActGemmSmem<RPT>::kThreads, 1)
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&decoded[s]);
-                    at.skip(1);
+                    at.skip(L::kGroups);
                 }
-                at.skip(kRingRun * (L::kGroups - 1));
                 if (drains) drain_behind(it0);
             }
         } else if ((ROLE == kRoleUG || ROLE == kRoleAB) && dec) {
@@ -627,17 +627,18 @@ __global__ void __launch_bounds__(ActGemmSmem<RPT>::kThreads, 1)
             };
             const int dst_off = amn ? (blk_in >> 1) * 8192 + row * 128 : row * 128;
             const int c0 = amn ? (blk_in & 1) * 4 : blk_in * 4, sw = row & 7;
-            // the scales of this group's next pair are in flight while it decodes (a load takes longer than
+            // the scales of this group's next two stages are in flight while it decodes (a load takes longer than
             // a step)
             uint32_t e[2];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) e[u] = scale_at(2 * group + u);
-            for (int it0 = 2 * group; ok && it0 < n_iters; it0 += 2 * L::kGroups) {
+            for (int u = 0; u < 2; ++u) e[u] = scale_at(group + u * L::kGroups);
+            for (int it0 = group; ok && it0 < n_iters; it0 += 2 * L::kGroups) {
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    if (!ok || it0 + u >= n_iters) break;
+                    const int it = it0 + u * L::kGroups;
+                    if (!ok || it >= n_iters) break;
                     const float st = act8_step(e[u]);
-                    e[u] = scale_at(it0 + u + 2 * L::kGroups);
+                    e[u] = scale_at(it + 2 * L::kGroups);
                     ok = landed();
                     if (!ok) break;
                     const int s = at.s;
@@ -652,9 +653,8 @@ __global__ void __launch_bounds__(ActGemmSmem<RPT>::kThreads, 1)
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&decoded[s]);
-                    at.skip(1);
+                    at.skip(L::kGroups);
                 }
-                at.skip(kRingRun * (L::kGroups - 1));
                 if (drains) drain_behind(it0);
             }
         } else if (quant) {
@@ -663,13 +663,13 @@ __global__ void __launch_bounds__(ActGemmSmem<RPT>::kThreads, 1)
             const int64_t grow = static_cast<int64_t>(m0) + row;
             const bool in = grow < job.M;
             uint8_t* codes = job.mx_codes + grow * (job.K / 2) + b * 16;
-            // a pair of stages fills one scale word of the row; its tile advances by 512 bytes with the pair
+            // a stage fills half a scale word of the row; its tile advances by 512 bytes every other stage
             uint8_t* word = job.mx_scales + mx_scale_offset(grow, k_begin * 2, mx_col_tiles(job.K));
-            for (int it0 = 2 * group; ok && it0 < n_iters; it0 += 2 * L::kGroups) {
-                uint32_t e_word = 0;
+            for (int it0 = group; ok && it0 < n_iters; it0 += 2 * L::kGroups) {
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    if (!ok || it0 + u >= n_iters) break;
+                    const int it = it0 + u * L::kGroups;
+                    if (!ok || it >= n_iters) break;
                     ok = landed();
                     if (!ok) break;
                     const int s = at.s;
@@ -682,16 +682,14 @@ __global__ void __launch_bounds__(ActGemmSmem<RPT>::kThreads, 1)
                     if (lane == 0) mbar_arrive(&empty[s]);       // the tile has been read
                     uint32_t e, v[4];
                     mxfp4_block32(raw, e, v);
-                    if (in && dcheck(static_cast<int64_t>(k_begin + it0 + u) * 64 + b * 32 < job.K, args.err))
-                        *reinterpret_cast<uint4*>(codes + static_cast<int64_t>(k_begin + it0 + u) * 32) =
+                    if (in && dcheck(static_cast<int64_t>(k_begin + it) * 64 + b * 32 < job.K, args.err))
+                        *reinterpret_cast<uint4*>(codes + static_cast<int64_t>(k_begin + it) * 32) =
                             make_uint4(v[0], v[1], v[2], v[3]);
                     e |= __shfl_xor_sync(0xffffffffu, e, 1) << 8;        // (of the even lane: both blocks' bytes)
-                    e_word |= e << (16 * u);
-                    at.skip(1);
+                    if (in && b == 0 && dcheck(static_cast<int64_t>(k_begin + it) * 64 < job.K, args.err))
+                        *reinterpret_cast<uint16_t*>(word + (it >> 1) * kMxTileBytes + (it & 1) * 2) = static_cast<uint16_t>(e);
+                    at.skip(L::kGroups);
                 }
-                if (ok && in && b == 0 && dcheck(static_cast<int64_t>(k_begin + it0) * 64 < job.K, args.err))
-                    *reinterpret_cast<uint32_t*>(word + (it0 >> 1) * kMxTileBytes) = e_word;
-                at.skip(kRingRun * (L::kGroups - 1));
                 if (drains) drain_behind(it0);
             }
         }

@@ -70,26 +70,21 @@ struct Model {
     template <int GROUPS>
     void group_warp(int g) {
         using namespace qlora;
-        RingPos at(S, kRingRun * g);
+        RingPos at(S, g);
         auto we = [&](int i, int p) { return wait(empty[i], p); };
         auto wf = [&](int i, int p) { return wait(full[i], p); };
-        for (int it0 = kRingRun * g; it0 < n; it0 += kRingRun * GROUPS) {
-            for (int u = 0; u < kRingRun; ++u) {
-                const int it = it0 + u;
-                if (it >= n) break;
-                if (checked ? !ring_landed<GROUPS>(at, we, wf) : !wf(at.s, at.ph)) return;
-                if (landed[at.s] != it) return fault("read before its load landed", it);
-                pause();                             // decoding takes a while
-                if (landed[at.s] != it) return fault("overwritten while it was read", it);
-                if (quant) {
-                    empty[at.s].arrive();
-                } else {
-                    if (++tile[at.s] > kWarps) return fault("decoded too often", it);
-                    decoded[at.s].arrive();
-                }
-                at.skip(1);
+        for (int it = g; it < n; it += GROUPS) {
+            if (checked ? !ring_landed<GROUPS>(at, we, wf) : !wf(at.s, at.ph)) return;
+            if (landed[at.s] != it) return fault("read before its load landed", it);
+            pause();                             // decoding takes a while
+            if (landed[at.s] != it) return fault("overwritten while it was read", it);
+            if (quant) {
+                empty[at.s].arrive();
+            } else {
+                if (++tile[at.s] > kWarps) return fault("decoded too often", it);
+                decoded[at.s].arrive();
             }
-            at.skip(kRingRun * (GROUPS - 1));
+            at.skip(GROUPS);
         }
     }
     void producer() {
@@ -172,7 +167,7 @@ int main(int argc, char** argv) {
     if (argc != 7) return 2;
     Model m;
     m.G = atoi(argv[1]), m.S = atoi(argv[2]), m.n = atoi(argv[3]), m.quant = atoi(argv[4]), m.checked = atoi(argv[5]);
-    if (m.G < 1 || m.G > 3 || m.S < qlora::ring_min_stages(m.G)) return 2;
+    if (m.G < 1 || m.G > 3 || m.S < m.G) return 2;
     for (int seed = 0; seed < atoi(argv[6]); ++seed)
         if (!m.run(static_cast<unsigned>(seed))) {
             printf("seed %d: %s (stage %d)\n", seed, g_fault, g_fault_it);
