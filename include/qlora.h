@@ -397,6 +397,7 @@ qlora_status mxfp4_dequantize(const qlora_mxfp4* w, void* W_out, qlora_dtype out
  * block-scaled 4-bit tensor cores (exact products, fp32 accumulation), the adapter term takes the
  * unquantized X and is added in the same accumulator, (alpha/r) X A^T carried as two bf16 numbers
  * (16 significant bits).
+ * An infinite entry of B gives NaN where the formula has an infinity (it meets both numbers).
  * Any T >= 1, from single tokens up.  U_save as in qlora_linear_fwd.
  * [MF] "Intrinsic Dimensionality and Low-Rank Parameter Dynamics".
  * ws >= qlora_workspace_bytes(QLORA_OP_FWD_MXFP4, QLORA_BF16, T, d_out, d_in, r).
@@ -434,6 +435,8 @@ qlora_status qlora_act8_dequantize(const qlora_act8* a, int64_t T, int64_t d_in,
  * (nullable: skipped) in bf16; dA, dB fp32, with s (dH B) and a recomputed U carried to the tensor
  * cores as three bf16 numbers each (24 significant bits), two for dX.  flags as in qlora_linear_bwd_ex, the
  * two-phase form included (QLORA_BWD_DX_FROM_WS reads no activation, but one must be given).
+ * An infinite operand of a number carried in parts (X for dA, dH for dB, A for dX) gives NaN where the
+ * formula has an infinity.
  * [MF] "Gradient Dynamics and Backpropagation Mechanics".
  * ws >= qlora_workspace_bytes(QLORA_OP_BWD_MXFP4, QLORA_BF16, T, d_out, d_in, r): above 64 tokens the
  * weight decoded to bf16 (2 d_out d_in bytes) is in it, a copy of X never.                       */
@@ -444,7 +447,9 @@ qlora_status qlora_linear_bwd_mxfp4(const qlora_mxfp4* w, const void* X, const q
                                     cudaStream_t stream);
 
 /* qlora_linear_bwd_ex (bf16) from an 8-bit checkpoint of X instead of X, with the arithmetic and
- * flags of qlora_linear_bwd_mxfp4 over the NF4 base.
+ * flags of qlora_linear_bwd_mxfp4 over the NF4 base.  Its workspace holds the weight decoded to bf16 above
+ * 64 tokens, which qlora_linear_bwd does without: decoded once, the product for dX runs at 1.5 to 1.6
+ * PFLOP/s, with the decode inside at 1.0.
  * ws >= qlora_workspace_bytes(QLORA_OP_BWD_ACT8, QLORA_BF16, T, d_out, d_in, r).                  */
 qlora_status qlora_linear_bwd_act8(const qlora_nf4* w, const qlora_act8* X8, const void* dH, int64_t T,
                                    const void* A, const void* B, int32_t r, float alpha,

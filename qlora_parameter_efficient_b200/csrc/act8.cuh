@@ -31,8 +31,10 @@ __device__ __forceinline__ float act8_step(uint32_t e) {
 }
 
 // Four lanes per block of 32, eight elements per lane, kAct8Unroll chunks of 256 lanes per CTA whose
-// loads are issued together.  n8 (elements / 8) is a multiple of 8, so a block is never split.  Bound by
-// HBM: 4096 x 4096 bf16 in 11.8 us (51 MB, 4.3 TB/s).
+// loads are issued together.  n8 (elements / 8) is a multiple of 8, so a block is never split.
+// 4096 x 4096 bf16 in 11.7 us (51 MB, 4.3 TB/s, two thirds of what a copy gets; the decoder below, with the
+// same loads and stores the other way round, 6.3): what is left is its arithmetic, two products, two clamps and an
+// addition per element.
 constexpr int kAct8Unroll = 4;
 template <typename T>
 __global__ void __launch_bounds__(256) k_act8_quantize(const T* __restrict__ X, int64_t n8,
@@ -293,13 +295,14 @@ struct ActGemmSmem {
 // grows with the chain: 9e-6 of a gradient over 8192 tokens.  So the chain is cut into segments of
 // 16 or 24 MMAs, whose sums warps 2..9 add up in registers, rounding to nearest, from two to four
 // accumulator tiles in turn.
-// Bound by memory: a K step of 64 reads 8 KB of int8 (or 16 KB of bf16) from HBM and the B tiles from
-// L2.  With few tokens dX^T = W^T dH^T is such a product too (kActDx): M = d_in, N = tokens, the weight
+// A K step of 64 reads 8 KB of int8 (or 16 KB of bf16) from HBM and the B tiles from L2.  Bound by the
+// decoding or quantizing of those in the CTA (about 0.6 us a step for one group of warps; DRAM at 21 to 26 % with
+// 4096 tokens, 56 % for U and G of 8192) and, with few tiles, by latency.  With few tokens dX^T = W^T dH^T is such a product too (kActDx): M = d_in, N = tokens, the weight
 // decoded once per CTA and split along d_out over the SMs.  An MMA of M = 128 takes about 75 cycles
 // however small N is (it reads its A tile), hence one of N = 3 stride for a triple and not three.
-// Measured out of HBM: U and G of 4096 tokens, 4096 x 4096, r = 16, from the checkpoint, 13.7 us (50 MB), dA and
-// dB of the same 23.3 us; of 8192 tokens, 11008 x 4096, r = 64, 38 and 81 us (214 MB); U and X's MXFP4 of 200
-// tokens, 8192 wide, 12.5 us.
+// Measured out of HBM: U and G of 4096 tokens, 4096 x 4096, r = 16, from the checkpoint, 14 us (50 MB), dA and
+// dB of the same 25 us; of 8192 tokens, 11008 x 4096, r = 64, 37 and 73 us (214 MB); U and X's MXFP4 of 200
+// tokens, 8192 wide, 11.4 us, of 4096 tokens, 4096 wide, 17.7 us.
 template <int RPT, int ROLE>
 __global__ void __launch_bounds__(ActGemmSmem<RPT>::kThreads, 1)
     k_act_gemm(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmB0,

@@ -78,7 +78,7 @@ __device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t desc) {
 // [0, r): one adapter row j each, U[:, j] = X A[j]^T in fp32, written unscaled to u_save (nullable,
 // [T, r]) and s U as two bf16 terms to us [T, ext_ld(r)]; the rest: B copied to padded rows (only where r is
 // not a multiple of 8).
-// Bound by latency (out of HBM 4.9 us at one token of 4096, r = 16; 8.2 us at 13 tokens, r = 64), most
+// Bound by latency (out of HBM 5.1 us at one token of 4096, r = 16; 9.3 us at 13 tokens, r = 64), most
 // of it behind the stream.
 constexpr int kMxDecodeT = 16;
 struct MxPrepArgs {
@@ -607,8 +607,8 @@ struct PairGemmSmem {
 // warp of a split tile writes its fp32 partial and takes a ticket; the last adds all partials in K
 // order, so the result does not depend on which is last, and no CTA waits for another.
 // Bound by the tensor cores (256 x 256 x 256 MXFP4 or x 64 bf16 in 512 cycles) where K is long and the
-// waves are full: 8192 tokens of 11008 x 4096 in 470 us (bf16, 1.57 PFLOP/s, tensor pipe 94 % busy).  4096^3 takes
-// 93 us in bf16 (76 % busy) and 35.1 in MXFP4 (3.9 PFLOP/s, 48 %): 3.46 waves in 4, 620 cycles a stage
+// waves are full: 8192 tokens of 11008 x 4096 in 458 to 484 us (bf16, 1.6 PFLOP/s, tensor pipe 95 % busy).  4096^3 takes
+// 82 to 94 us in bf16 (76 % busy) and 33 to 36 in MXFP4 (3.9 PFLOP/s, 47 %): 3.46 waves in 4, 620 cycles a stage
 // (the 35 KB of its loads come at 55 bytes a cycle), and between two tiles the time to read the columns
 // that their accumulators share.
 template <bool MX, int BN>
