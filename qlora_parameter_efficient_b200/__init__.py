@@ -718,15 +718,19 @@ class MXFP4Weight:
     def _c(self):
         """The C struct, by reference, of the buffers as they are now (a tensor may have been given other memory
         since)."""
-        self.__post_init__()
+        self._check()
         return ctypes.byref(_MXFP4(self.codes.data_ptr(), self.scales.data_ptr(), self.d_out, self.d_in))
 
-    def __post_init__(self):
-        torch = _torch()
+    def _check(self):
+        u8 = _torch().uint8
         dev = _need_cuda("codes", self.codes)
+        _need("codes", self.codes, u8, (self.d_out, self.d_in // 2), dev)
+        _need("scales", self.scales, u8, (_mx_scale_bytes(self.d_out, self.d_in),), dev)
+
+    def __post_init__(self):
+        _need_cuda("codes", self.codes)
         mxfp4_sizes(self.d_out, self.d_in)
-        _need("codes", self.codes, torch.uint8, (self.d_out, self.d_in // 2), dev)
-        _need("scales", self.scales, torch.uint8, (_mx_scale_bytes(self.d_out, self.d_in),), dev)
+        self._check()
 
 
 @dataclass(frozen=True)
